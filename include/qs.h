@@ -85,8 +85,21 @@ typedef enum qs_op {
   QS_OP_QUANT_SPARSE_LINEAR = 3,
   QS_OP_TERNARY_PACK = 4,
   QS_OP_SPARSE_FFN_GATE_FIRST = 5,
-  QS_OP_QUANT_SPARSE_FFN = 6
+  QS_OP_QUANT_SPARSE_FFN = 6,
+  QS_OP_FP4_SPARSE_LINEAR = 7,
+  QS_OP_MOE_FFN = 8
 } qs_op;
+
+/* Microscaled 4-bit floating point (see qs_fp4_quantize). */
+typedef enum qs_fp4_format {
+  QS_FP4_MX = 0,   /* blocks of 32, the scale a power of two (e8m0) */
+  QS_FP4_NV = 1    /* blocks of 16, the scale an e4m3 number times one f32 per tensor */
+} qs_fp4_format;
+
+typedef enum qs_fp4_scale_layout {
+  QS_FP4_SCALES_ROWS = 0,   /* [R, d / block] bytes, row-major */
+  QS_FP4_SCALES_TILED = 1   /* tiles of 128 rows x 4 blocks, as the tensor cores take them */
+} qs_fp4_scale_layout;
 
 /* Largest row length (d, d_in, d_ff) a top-K row may have: one CTA holds a
  * row's keys in shared memory. */
@@ -384,12 +397,87 @@ qs_status qs_quant_sparse_ffn(const void* x, int dtype, int T, int d_model, int 
                               float* y, float* h_out, void* const* phase_events, void* ws,
                               size_t ws_bytes, void* stream);
 
+/*
+ * qs_fp4_quantize -- rows to microscaled 4-bit floating point: weights once,
+ *   offline; activations before a 4-bit projection; or (values) the rounding
+ *   alone.  The pages' quantized model uses 8-bit activations and ternary
+ *   weights (qs_quant_sparse_linear, qs_ternary_pack); this is the 4-bit form
+ *   that the tensor cores multiply directly.  Definition, in float32 steps
+ *   rounded to nearest even, for each block of B neighbouring values of a row
+ *   (B = 32 for QS_FP4_MX, 16 for QS_FP4_NV; amax = max |x| over the block,
+ *   e2m1(v) = the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with v's sign, ties to
+ *   the even mantissa, larger magnitudes to 6):
+ *     MX: s = 2^(floor(log2 amax) - 2), not below 2^-127;  q = e2m1(x / s);
+ *         the scale byte is the exponent + 127 (0 for an all-zero block).
+ *     NV: s = e4m3((amax / 6) / g), at most 448;  r = s * g;
+ *         q = e2m1(x * (1 / r)), 0 where r < 2^-126;  the scale byte is s.
+ *   The number that a code stands for is q * s (times g for NV).  A block that
+ *   holds an infinity or a NaN gets a NaN scale (byte 255, or 127 for NV) and
+ *   codes 0: it stands for NaNs.
+ *
+ *   x             [R, d] `dtype` (bf16 or f32); d a multiple of 32.
+ *   tensor_scale  1 f32 on the device: g of QS_FP4_NV, finite and > 0; NULL = 1.
+ *                 (max |x| / 2688 lets the largest block use the largest scale.)
+ *                 Ignored by QS_FP4_MX.
+ *   codes         [R, d/2] uint8 out or NULL: value 2i of a row in the low four
+ *                 bits of byte i, value 2i + 1 in the high four; the code is the
+ *                 sign bit and the value's place in the list above.
+ *   scales        qs_fp4_scale_bytes(R, d, format, scale_layout) bytes out or
+ *                 NULL.  QS_FP4_SCALES_ROWS: byte [r, b], row-major.
+ *                 QS_FP4_SCALES_TILED: row r, block b (n = ceil(d / B / 4)) at
+ *                 ((r / 128) * n + b / 4) * 512 + (r % 32) * 16 +
+ *                 (r % 128 / 32) * 4 + b % 4; the bytes of rows behind the last
+ *                 and of blocks behind d are set to 0.
+ *   values        [R, d] `dtype` out or NULL: the numbers the codes stand for,
+ *                 rounded to x's type (exact in bf16 for MX).
+ *   At least one of codes, scales, values.  Needs no workspace.
+ *   Errors: INVALID_ARG (R < 1, d < 1, bad dtype / format / layout, NULL x, no
+ *   output), ALIGNMENT (d not a multiple of 32, a pointer not 16-byte aligned;
+ *   tensor_scale: 4 bytes), CUDA.
+ */
+qs_status qs_fp4_quantize(const void* x, int dtype, int64_t R, int d, int format,
+                          const float* tensor_scale, int scale_layout, uint8_t* codes,
+                          uint8_t* scales, void* values, void* stream);
+
+/* Bytes of the scales of an [R, d] matrix (0 if the arguments are invalid). */
+size_t qs_fp4_scale_bytes(int64_t R, int d, int format, int scale_layout);
+
+/*
+ * qs_fp4_sparse_linear -- Y = fp4(X (.) M) . fp4(W)^T with M the top-K mask of
+ *   |X|: the 4-bit sibling of qs_quant_sparse_linear.  x_s = topK(x, k) (ties
+ *   as everywhere), x_s is quantised (qs_fp4_quantize), and the two 4-bit
+ *   matrices are multiplied on the tensor cores (block scales applied there,
+ *   float32 accumulators):
+ *     y[t, j] = g_x g_w sum_i (qx sx)[t, i] (qw sw)[j, i]
+ *   The weight is read whole, once per 256 tokens: at 4.25 or 4.5 bits a value
+ *   that is less than 70% of its rows in 8 bits.  Results do not depend on
+ *   timing: the same call gives the same bits.
+ *
+ *   x         [T, d_in] `dtype` (bf16 or f32).     k  0..d_in.
+ *   w_codes   [d_out, d_in/2] uint8 and w_scales (QS_FP4_SCALES_TILED) from
+ *             qs_fp4_quantize of W [d_out, d_in] (output-major, as nn.Linear
+ *             stores it).
+ *   x_scale, w_scale   1 f32 each on the device or NULL (= 1): the tensor
+ *             scales of QS_FP4_NV (ignored by QS_FP4_MX).
+ *   y         [T, d_out] `y_dtype` (bf16 or f32) out.
+ *   phase_events  NULL or QS_LINEAR_PHASE_EVENTS events (as qs_sparse_linear;
+ *             the quantisation counts with the top-K).
+ *   ws        qs_workspace_size(QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k) bytes.
+ *   d_in must be a multiple of 32, d_out of 8.
+ *   Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED (d_in or d_out above
+ *   QS_MAX_ROW), CUDA.
+ */
+qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_out, int k,
+                               int format, const float* x_scale, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const float* w_scale, void* y, int y_dtype,
+                               void* const* phase_events, void* ws, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace `op` needs for these sizes (0 if the sizes are invalid).
  * Arguments: QS_OP_TOPK_MASK (T, d, 0, k); QS_OP_SPARSE_LINEAR (T, d_in, d_out,
  * k); QS_OP_SPARSE_FFN, QS_OP_SPARSE_FFN_GATE_FIRST and QS_OP_QUANT_SPARSE_FFN (T,
  * d_model, d_ff, k_h);
- * QS_OP_QUANT_SPARSE_LINEAR (T, d_in, d_out, k); QS_OP_TERNARY_PACK (0, d_in,
- * d_out, 0).  The dtype does
+ * QS_OP_QUANT_SPARSE_LINEAR and QS_OP_FP4_SPARSE_LINEAR (T, d_in, d_out, k);
+ * QS_OP_TERNARY_PACK (0, d_in, d_out, 0).  The dtype does
  * not change the size, and a workspace of this size also serves calls with the
  * same sizes and any other k. */
 size_t qs_workspace_size(int op, int T, int d_in, int d_out, int k);

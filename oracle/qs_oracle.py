@@ -385,6 +385,100 @@ def quant_sparse_ffn(x, t_up, alpha_up, t_gate, alpha_gate, t_down, alpha_down, 
 # --------------------------------------------------------------------------
 
 
+# --------------------------------------------------------------------------
+# microscaled 4-bit floating point
+# --------------------------------------------------------------------------
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+FP4_BLOCK = {"mx": 32, "nv": 16}
+
+
+def _nearest(v, grid):
+    """Index of the grid value nearest to v >= 0, ties to the even index (the
+    even mantissa); values above the grid go to its end."""
+    mid = (grid[:-1] + grid[1:]) / 2
+    lo = np.searchsorted(mid, v, side="left")        # a midpoint stays below
+    hi = np.searchsorted(mid, v, side="right")       # a midpoint goes up
+    return np.where(lo % 2 == 0, lo, hi)
+
+
+def e4m3_grid() -> np.ndarray:
+    """The 127 finite non-negative e4m3 values, by code."""
+    c = np.arange(127)
+    e, m = c // 8, c % 8
+    return np.where(e > 0, np.exp2(e - 7.0) * (1 + m / 8), m * 2.0 ** -9)
+
+
+def fp4_quantize(x, fmt: str, tensor_scale: float = 1.0) -> dict:
+    """Rows x [R, d] (float32 values) -> dict(codes [R, d] 0..15, scale_codes
+    [R, d/block], values [R, d] float64).
+
+    mx: s = 2^(floor(log2 amax) - 2), q = e2m1(x / s).
+    nv: s = e4m3((amax / 6) / g), r = s * g, q = e2m1(x * (1 / r)), in float32
+    steps.  A block with a non-finite value stands for NaNs.
+    """
+    x = np.asarray(x, dtype=np.float32)
+    R, d = x.shape
+    b = x.reshape(R, -1, FP4_BLOCK[fmt])
+    finite = np.isfinite(b).all(-1)
+    b = np.where(finite[..., None], b, np.float32(0))
+    amax = np.abs(b).max(-1)
+    if fmt == "mx":
+        _, e = np.frexp(amax.astype(np.float64))      # amax = m 2^e, m in [1/2, 1)
+        e = np.where(amax > 0, np.maximum(e - 1 - 2, -127), -127)
+        sc = np.where(finite, e + 127, 255).astype(np.int64)
+        back = np.exp2(e.astype(np.float64))
+        v = b.astype(np.float64) / back[..., None]
+    else:
+        g = np.float32(tensor_scale)
+        with np.errstate(over="ignore"):
+            t = np.float32(amax / np.float32(6.0)) / g
+        sc = _nearest(np.minimum(t.astype(np.float64), 448.0), e4m3_grid())
+        s = e4m3_grid()[sc].astype(np.float32)
+        back32 = s * g
+        ok = back32 >= np.float32(2.0 ** -126)
+        inv = np.where(ok, np.float32(1.0) / np.where(ok, back32, np.float32(1.0)), np.float32(0.0))
+        v = (b * inv[..., None].astype(np.float32)).astype(np.float64)
+        back = back32.astype(np.float64)
+        sc = np.where(finite, sc, 127)
+    q = _nearest(np.abs(v), E2M1)
+    codes = np.where(finite[..., None], q + 8 * np.signbit(v), 0)
+    val = np.where(np.signbit(v), -E2M1[q], E2M1[q]) * back[..., None]
+    if fmt == "nv":
+        val = val.astype(np.float32).astype(np.float64)
+    val = np.where(finite[..., None], val, np.nan)
+    return dict(codes=codes.reshape(R, d), scale_codes=sc, values=val.reshape(R, d))
+
+
+def fp4_pack(codes) -> np.ndarray:
+    """Codes [R, d] -> bytes [R, d/2], the even place in the low half."""
+    c = np.asarray(codes).astype(np.uint8)
+    return c[:, 0::2] | (c[:, 1::2] << 4)
+
+
+def fp4_tile_scales(sc) -> np.ndarray:
+    """Scale bytes [R, n] in tiles of 128 rows x 4 blocks (flat uint8), the
+    rows behind the last and the blocks behind n 0."""
+    sc = np.asarray(sc)
+    R, n = sc.shape
+    tpr = -(-n // 4)
+    out = np.zeros(-(-R // 128) * tpr * 512, dtype=np.uint8)
+    for r in range(R):
+        for j in range(n):
+            out[((r // 128) * tpr + j // 4) * 512 + (r % 32) * 16 + (r % 128 // 32) * 4 + j % 4] = sc[r, j]
+    return out
+
+
+def fp4_sparse_linear(x, w_values, k: int, fmt: str, x_scale: float = 1.0) -> dict:
+    """Y = fp4(X (.) M) . W^T in fp64, W given as the values it stands for
+    [d_out, d_in].  Also `mag` = |X| . |W|^T, which bounds rounding."""
+    x = np.asarray(x, dtype=np.float32)
+    xs = x * mask_from_keep(topk_keep(x, k), *x.shape)
+    xq = fp4_quantize(xs.astype(np.float32), fmt, x_scale)["values"]
+    w = np.asarray(w_values, dtype=np.float64)
+    return dict(y=xq @ w.T, mag=np.abs(xq) @ np.abs(w).T, xq=xq)
+
+
 def max_rel_err(y, ref) -> float:
     """max over rows of max_j |y - ref| / max_j |ref| (row infinity norm).
 

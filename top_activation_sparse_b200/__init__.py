@@ -10,6 +10,7 @@ Build the library with ``python -m top_activation_sparse_b200.build``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -42,6 +43,13 @@ QS_OP_QUANT_SPARSE_LINEAR = 3
 QS_OP_TERNARY_PACK = 4
 QS_OP_SPARSE_FFN_GATE_FIRST = 5
 QS_OP_QUANT_SPARSE_FFN = 6
+QS_OP_FP4_SPARSE_LINEAR = 7
+QS_OP_MOE_FFN = 8
+
+QS_FP4_MX = 0
+QS_FP4_NV = 1
+QS_FP4_SCALES_ROWS = 0
+QS_FP4_SCALES_TILED = 1
 
 QS_FAULT_NONE = 0
 QS_FAULT_GATHER_NO_COPIES = 1
@@ -53,6 +61,8 @@ QS_PREFILL_MIN_T = 64
 QS_FFN_PHASE_EVENTS = 5
 QS_LINEAR_PHASE_EVENTS = 3
 
+_FP4_FORMATS = {"mx": QS_FP4_MX, "nv": QS_FP4_NV}
+_FP4_LAYOUTS = {"rows": QS_FP4_SCALES_ROWS, "tiled": QS_FP4_SCALES_TILED}
 _ACTS = {"relu2_glu": QS_ACT_RELU2_GLU, "drelu": QS_ACT_DRELU}
 
 
@@ -77,6 +87,10 @@ _SIGNATURES = {
     "qs_quant_sparse_linear": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _f, _f, _vp, _vp, _vp, _vp,
                                     _vp, _vp, _sz, _vp]),
     "qs_ternary_pack": (_i, [_vp, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "qs_fp4_quantize": (_i, [_vp, _i, ctypes.c_int64, _i, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "qs_fp4_scale_bytes": (_sz, [ctypes.c_int64, _i, _i, _i]),
+    "qs_fp4_sparse_linear": (_i, [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                                  _vp, _sz, _vp]),
     "qs_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "qs_workspace_init": (_i, [_vp, _sz, _vp]),
     "qs_device_status": (_i, [_vp, _vp]),
@@ -211,6 +225,44 @@ def _workspace(ws, op, T, d_in, d_out, k, device):
     if cur is None or cur.numel() < need:
         cur = torch.zeros(max(need, 1), dtype=torch.uint8, device=device)
         _ws_cache[key] = cur
+    return cur
+
+
+def _call_context(dev, stream):
+    """Run a call's allocations and launch on the tensors' device, and on
+    `stream` where one is given."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+_ws_need: dict = {}
+_stream_ws: dict = {}
+_WS_COUNTER_BYTES = 256 + 64 * 1024      # the part that has to be zero before a first use
+
+
+def _stream_workspace(ws, op, T, d_in, d_out, k, device):
+    """The caller's workspace, or one kept per device, stream and op, so that
+    calls on two streams do not share one.  During a stream capture the graph
+    gets one of its own, cleared at each replay."""
+    if ws is not None:
+        return ws
+    size = (op, T, d_in, d_out, k)
+    need = _ws_need.get(size)
+    if need is None:
+        need = _ws_need[size] = qs_workspace_size(*size)
+    if torch.cuda.is_current_stream_capturing():
+        cur = torch.empty(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
+        cur[:_WS_COUNTER_BYTES].zero_()
+        return cur
+    key = (device, torch.cuda.current_stream(device).cuda_stream, op)
+    cur = _stream_ws.get(key)
+    if cur is None or cur.numel() < need:
+        cur = _stream_ws[key] = torch.zeros(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
     return cur
 
 
@@ -519,6 +571,82 @@ def qs_quant_sparse_ffn(x, wp_up, alpha_up: float, wp_gate, alpha_gate: float, w
     return QuantFfnResult(y, h_out)
 
 
+class Fp4Result(NamedTuple):
+    codes: torch.Tensor | None
+    scales: torch.Tensor | None
+    values: torch.Tensor | None
+
+
+def _fp4_code(table, name):
+    return table[name] if isinstance(name, str) else int(name)
+
+
+def _scalar_f32(t, name):
+    if t is not None and (t.numel() != 1 or t.dtype != torch.float32):
+        raise ValueError(f"{name} must be one float32 on the device")
+
+
+def qs_fp4_scale_bytes(R: int, d: int, format="mx", scale_layout="tiled") -> int:
+    """Bytes of the scales of an [R, d] matrix (0: invalid arguments)."""
+    return int(lib().qs_fp4_scale_bytes(int(R), int(d), _fp4_code(_FP4_FORMATS, format),
+                                        _fp4_code(_FP4_LAYOUTS, scale_layout)))
+
+
+def qs_fp4_quantize(x: torch.Tensor, format="mx", scale_layout="tiled", tensor_scale=None, codes=True,
+                    scales=True, values=None, stream=None) -> Fp4Result:
+    """Quantize the rows of x [..., d] to microscaled 4-bit floating point
+    ("mx": blocks of 32, power-of-two scales; "nv": blocks of 16, e4m3 scales
+    times tensor_scale).  codes [..., d/2] uint8; scales uint8, [..., d/block]
+    for scale_layout "rows", one flat array for "tiled" (all rows of x as one
+    matrix); values [..., d]: the rounded x in its own type."""
+    dev = _need_cuda(x, tensor_scale)
+    _scalar_f32(tensor_scale, "tensor_scale")
+    fmt, lay = _fp4_code(_FP4_FORMATS, format), _fp4_code(_FP4_LAYOUTS, scale_layout)
+    d = x.shape[-1]
+    if d < 32 or d % 32:
+        raise QSError("qs_fp4_quantize", QS_ERR_ALIGNMENT)
+    R = x.numel() // d
+    lead = tuple(x.shape[:-1])
+    with _call_context(dev, stream):
+        codes = _out(codes, lead + (d // 2,), torch.uint8, dev)
+        shape = lead + (d // (32 if fmt == QS_FP4_MX else 16),) if lay == QS_FP4_SCALES_ROWS else \
+            (qs_fp4_scale_bytes(R, d, fmt, lay),)
+        scales = _out(scales, shape, torch.uint8, dev)
+        values = _out(values, tuple(x.shape), x.dtype, dev)
+        _need_cuda(x, codes, scales, values)
+        _check("qs_fp4_quantize", lib().qs_fp4_quantize(
+            x.data_ptr(), _dtype_code(x), R, d, fmt, _ptr(tensor_scale), lay, _ptr(codes),
+            _ptr(scales), _ptr(values), _stream_ptr(None)))
+    return Fp4Result(codes, scales, values)
+
+
+def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, k: int,
+                         format="mx", x_scale=None, w_scale=None, y=None, y_dtype=None,
+                         phase_events=None, ws=None, stream=None) -> torch.Tensor:
+    """Y = fp4(X (.) topK-mask(|X|)) . fp4(W)^T: w_codes [d_out, d_in/2] and
+    w_scales (tiled) from qs_fp4_quantize of W [d_out, d_in], x [T, d_in]
+    quantized here.  y_dtype: bfloat16 or float32 (x's type unless given)."""
+    dev = _need_cuda(x, w_codes, w_scales, x_scale, w_scale)
+    _scalar_f32(x_scale, "x_scale")
+    _scalar_f32(w_scale, "w_scale")
+    T, d_in = x.shape
+    d_out = w_codes.shape[0]
+    fmt = _fp4_code(_FP4_FORMATS, format)
+    if tuple(w_codes.shape) != (d_out, d_in // 2) or w_codes.dtype != torch.uint8:
+        raise ValueError("w_codes must be [d_out, d_in/2] uint8")
+    if w_scales.dtype != torch.uint8 or w_scales.numel() != qs_fp4_scale_bytes(d_out, d_in, fmt, QS_FP4_SCALES_TILED):
+        raise ValueError("w_scales must be the tiled uint8 scales of W [d_out, d_in]")
+    with _call_context(dev, stream):
+        y = _out(y if y is not None else True, (T, d_out), y.dtype if y is not None else (y_dtype or x.dtype), dev)
+        _need_cuda(x, y)
+        ws = _stream_workspace(ws, QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, dev)
+        _check("qs_fp4_sparse_linear", lib().qs_fp4_sparse_linear(
+            x.data_ptr(), _dtype_code(x), T, d_in, d_out, k, fmt, _ptr(x_scale), w_codes.data_ptr(),
+            w_scales.data_ptr(), _ptr(w_scale), y.data_ptr(), _dtype_code(y),
+            _events(phase_events, QS_LINEAR_PHASE_EVENTS), ws.data_ptr(), ws.numel(), _stream_ptr(None)))
+    return y
+
+
 def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_out=None, ws=None,
                     stream=None):
     """Ternary-quantize W [d_out, d_in] f32 and pack it input-major 2-bit.
@@ -541,4 +669,4 @@ def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_ou
 
 __all__ = [n for n in dir() if n.startswith(("qs_", "QS_"))] + [
     "lib", "new_workspace", "header_functions", "QSError", "TopkResult", "FfnResult",
-    "QuantResult", "BackwardResult", "QuantFfnResult"]
+    "QuantResult", "BackwardResult", "QuantFfnResult", "Fp4Result"]

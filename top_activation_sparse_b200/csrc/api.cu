@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "fp4.cuh"
 #include "gate_first.cuh"
 #include "qs_internal.cuh"
 
@@ -181,6 +182,18 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       L->alpha_parts = take(kPackSumBlocks * sizeof(double));
       L->alpha = take(sizeof(float));
       break;
+    case QS_OP_FP4_SPARSE_LINEAR: {
+      if (T < 1 || d_in < 32 || d_out < 8 || d_in > QS_MAX_ROW || d_out > QS_MAX_ROW || k < 0 ||
+          k > d_in || (d_in % 32) != 0 || (d_out % 8) != 0)
+        return false;
+      L->xs_masked = take((size_t)T * d_in * sizeof(float));
+      L->fp4_codes = take((size_t)T * (d_in / 2));
+      // the NV form has more scales than the MX form
+      L->fp4_scales = take(qs_fp4_scale_bytes(T, d_in, QS_FP4_NV, QS_FP4_SCALES_TILED));
+      L->parts1_elems = plan_fp4_gemm(T, d_in, d_out).parts_elems;
+      L->parts1 = take(L->parts1_elems * sizeof(float));
+      break;
+    }
     default:
       return false;
   }
@@ -807,6 +820,100 @@ qs_status qs_block_quant_sparse_linear(const void* x, int dtype, int T, int d_in
                                        void* stream) {
   return quant_impl(x, dtype, T, d_in, d_out, k, block, wt_packed, alpha, eps, y, acc, q, idx,
                     phase_events, ws, ws_bytes, stream);
+}
+
+size_t qs_fp4_scale_bytes(int64_t R, int d, int format, int scale_layout) {
+  if (R < 1 || d < 1 || (d % 32) != 0 || (format != QS_FP4_MX && format != QS_FP4_NV)) return 0;
+  const size_t nb = (size_t)(d / fp4_block(format));
+  if (scale_layout == QS_FP4_SCALES_ROWS) return (size_t)R * nb;
+  if (scale_layout == QS_FP4_SCALES_TILED)
+    return ((size_t)R + 127) / 128 * fp4_tiles_per_row((int)nb) * kSfTile;
+  return 0;
+}
+
+qs_status qs_fp4_quantize(const void* x, int dtype, int64_t R, int d, int format,
+                          const float* tensor_scale, int scale_layout, uint8_t* codes,
+                          uint8_t* scales, void* values, void* stream) {
+  if (!valid_dtype(dtype) || x == nullptr || R < 1 || d < 1 ||
+      (format != QS_FP4_MX && format != QS_FP4_NV) ||
+      (scale_layout != QS_FP4_SCALES_ROWS && scale_layout != QS_FP4_SCALES_TILED) ||
+      (codes == nullptr && scales == nullptr && values == nullptr))
+    return QS_ERR_INVALID_ARG;
+  if ((d % 32) != 0 || !aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(values) ||
+      ((uintptr_t)tensor_scale & 3u) != 0)
+    return QS_ERR_ALIGNMENT;
+  Fp4QuantArgs q;
+  q.x = x; q.R = (size_t)R; q.d = d;
+  q.bf16 = dtype == QS_BF16;
+  q.format = format;
+  q.tiled = scale_layout == QS_FP4_SCALES_TILED;
+  q.tensor_scale = tensor_scale;
+  q.codes = codes; q.scales = scales; q.values = values;
+  return from_cuda(launch_fp4_quantize(q, (cudaStream_t)stream));
+}
+
+qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_out, int k,
+                               int format, const float* x_scale, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const float* w_scale, void* y, int y_dtype,
+                               void* const* phase_events, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(y_dtype) || x == nullptr || w_codes == nullptr ||
+      w_scales == nullptr || y == nullptr || T < 1 || d_in < 1 || d_out < 1 || k < 0 || k > d_in ||
+      (format != QS_FP4_MX && format != QS_FP4_NV))
+    return QS_ERR_INVALID_ARG;
+  if (d_in > QS_MAX_ROW || d_out > QS_MAX_ROW) return QS_ERR_UNSUPPORTED;
+  if ((d_in % 32) != 0 || (d_out % 8) != 0 || !aligned16(x) || !aligned16(w_codes) ||
+      !aligned16(w_scales) || !aligned16(y) || ((uintptr_t)x_scale & 3u) != 0 ||
+      ((uintptr_t)w_scale & 3u) != 0)
+    return QS_ERR_ALIGNMENT;
+  WsLayout L;
+  const qs_status st = check_ws(QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, ws, ws_bytes, &L);
+  if (st != QS_OK) return st;
+  const Fp4GemmPlan plan = plan_fp4_gemm(T, d_in, d_out);
+  if (!fp4_gemm_supported() || kTkGemv + plan.tickets > kTkGemvEnd ||
+      (long long)plan.mtiles * plan.ntiles * plan.nk >= (1ll << 31))
+    return QS_ERR_UNSUPPORTED;
+  WsView w{(unsigned char*)ws};
+  cudaStream_t s = (cudaStream_t)stream;
+  auto mark = [&](int i) -> cudaError_t {
+    if (phase_events == nullptr) return cudaSuccess;
+    return cudaEventRecord((cudaEvent_t)phase_events[i], s);
+  };
+  QS_TRY_CUDA(mark(0));
+  Fp4QuantArgs q;
+  q.x = x;
+  if (k < d_in) {
+    TopkArgs a;
+    a.x = x; a.T = T; a.d = d_in; a.k = k;
+    a.kind = dtype == QS_F32 ? TK_F32 : TK_BF16;
+    a.xs = w.at<void>(L.xs_masked);
+    a.status = w.status();
+    QS_TRY_CUDA(launch_topk(a, s));
+    q.x = a.xs;
+  }
+  q.R = (size_t)T; q.d = d_in;
+  q.bf16 = dtype == QS_BF16;
+  q.format = format;
+  q.pad_rows = 0;                  // they scale tokens that are not there
+  q.tensor_scale = x_scale;
+  q.codes = w.at<uint8_t>(L.fp4_codes);
+  q.scales = w.at<uint8_t>(L.fp4_scales);
+  QS_TRY_CUDA(launch_fp4_quantize(q, s));
+  QS_TRY_CUDA(mark(1));
+  Fp4GemmArgs g;
+  g.xc = q.codes; g.xs = q.scales;
+  g.wc = w_codes; g.ws = w_scales;
+  g.x_scale = x_scale; g.w_scale = w_scale;
+  g.y = y;
+  g.y_bf16 = y_dtype == QS_BF16;
+  g.T = T; g.d_in = d_in; g.d_out = d_out;
+  g.format = format;
+  g.parts = w.at<float>(L.parts1);
+  g.tickets = w.ticket(L, kTkGemv);
+  g.status = w.status();
+  g.plan = plan;
+  QS_TRY_CUDA(launch_fp4_gemm(g, s));
+  QS_TRY_CUDA(mark(2));
+  return QS_OK;
 }
 
 qs_status qs_sparse_linear_backward(const void* x, int dtype, int T, int d_in, int d_out, int k,

@@ -1,0 +1,495 @@
+// Product of two microscaled 4-bit matrices on the 5th-generation tensor cores
+// (tcgen05.mma with block scales, accumulators and scales in tensor memory).
+//
+//   y[t, j] = g_x g_w sum_b sx[t, b] sw[j, b] sum_{i in block b} qx[t, i] qw[j, i]
+//
+// A product of two e2m1 numbers is a multiple of 1/4 of at most 36, so a
+// block's sum is exact; the scaled sums are added in float32.
+//
+// The weight is the MMA's M side (tiles of 128 outputs) whatever the number of
+// tokens, which are its N side (8 to 256): a few tokens then cost what the
+// weight's bytes cost, and many tokens fill 128 x 256 tiles.
+//   * warp 0 copies steps of 256 inputs into a ring: 128 weight rows and the
+//     tile's tokens (128-byte rows, 128-byte swizzle, 2-D TMA) and the scales'
+//     512-byte tiles (plain bulk copies; their layout in global memory is the
+//     one tensor memory wants).  The weights of the first steps are asked for
+//     before the kernel waits for the one that quantises x: they do not depend
+//     on it.
+//   * one thread of warp 1 copies a step's scales to tensor memory
+//     (tcgen05.cp, one 512-byte tile per 4 columns, a place of its own per ring
+//     stage: the commit that frees the stage frees both) and issues its four
+//     MMAs of K = 64.
+//   * warps 2 to 5 read the accumulator and store y, column by token.
+// Up to 128 tokens the steps of all tiles are dealt out evenly over the SMs
+// (few tiles: a tile's steps are shared by several CTAs, which leave partial
+// sums in the workspace; the last to arrive adds them in the order of their
+// steps, so that results do not depend on timing).  Every wait is bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "fp4.cuh"
+
+namespace qs {
+namespace {
+
+constexpr int kGThreads = 192;
+constexpr int kGM = 128;                 // outputs per tile
+constexpr int kGK = 256;                 // inputs per step: 128 bytes of codes per row
+constexpr int kGABytes = kGM * kGK / 2;  // 16 KB
+constexpr int kGSmemCap = 222 * 1024;
+
+constexpr int gmin(int a, int b) { return a < b ? a : b; }
+
+template <bool NV, int NT>
+struct GShape {
+  static constexpr int kAtoms = kGK / (NV ? 16 : 32) / 4;    // 512-byte scale tiles per step (4 / 2)
+  static constexpr int kRT = NT > 128 ? 2 : 1;               // 128-row scale tiles of the tokens
+  static constexpr int kB = NT * kGK / 2;
+  static constexpr int kSfA = kAtoms * kSfTile;
+  static constexpr int kSfB = kAtoms * kRT * kSfTile;
+  static constexpr int kStage = kGABytes + kB + kSfA + kSfB;
+  static constexpr int kAcc = NT < 32 ? 32 : NT;             // accumulator columns (allocated)
+  static constexpr int kNacc = 2 * kAcc <= 256 ? 2 : 1;      // two accumulators up to 128 tokens
+  static constexpr int kSfCols = kAtoms * 4 * (1 + kRT);     // tensor-memory columns per stage
+  static constexpr int kStages = gmin((kGSmemCap - 1024) / kStage, (512 - kNacc * kAcc) / kSfCols);
+  static constexpr int kSmem = kStages * kStage + 1024;
+  static_assert(kStage % 1024 == 0, "the swizzled tiles start on 1 KB");
+  static_assert(kStages >= 3, "ring too short");
+};
+
+// instruction descriptor of the block-scaled 4-bit MMA: A and B e2m1, both
+// K-major, f32 accumulators, M = 128, N = NT; scale type e8m0 (1) or e4m3 (0);
+// MX: which half of the 4 scale bytes (0 or 2) this K = 64 takes
+template <bool NV, int NT>
+__device__ constexpr uint32_t g_idesc(uint32_t sf_id) {
+  return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) |
+         ((NV ? 0u : 1u) << 23) | ((uint32_t)(kGM >> 4) << 24) | (sf_id << 29);
+}
+
+__device__ __forceinline__ uint64_t g_desc(uint32_t saddr, uint32_t sbo, uint32_t layout) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;                          // leading offset: unused by these layouts
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;                          // sm_100 descriptor version
+  d |= (uint64_t)layout << 61;
+  return d;
+}
+
+template <bool NV>
+__device__ __forceinline__ void g_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                      uint32_t sfb, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales (32 rows of 16 bytes) -> 4 tensor-memory columns, the
+// same in each of the four lane quarters
+__device__ __forceinline__ void g_cp_sf(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void g_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void g_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void g_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void g_tma(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void g_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void g_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void g_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// The steps [0, total) of all tiles dealt out over `grid` CTAs: CTA c has
+// [first(c), first(c + 1)).
+struct GDeal {
+  long long total;
+  int grid;
+  __host__ __device__ long long first(int c) const { return total * c / grid; }
+  // the CTA that has step s
+  __host__ __device__ int owner(long long s) const {
+    int c = (int)(s * grid / total);
+    while (c + 1 < grid && first(c + 1) <= s) ++c;
+    while (c > 0 && first(c) > s) --c;
+    return c;
+  }
+};
+
+// A CTA's steps in order: a range of all steps (shared tiles), or whole tiles
+// blockIdx.x + i * gridDim.x.
+struct GWalk {
+  int nk, ntiles, stride;
+  int tile, ks, mt, nt;
+  __device__ GWalk(const Fp4GemmPlan& P, const GDeal& deal)
+      : nk(P.nk), ntiles(P.ntiles), stride(P.split ? 1 : (int)gridDim.x) {
+    const long long s = P.split ? deal.first(blockIdx.x) : (long long)blockIdx.x * nk;
+    tile = (int)(s / nk);
+    ks = (int)(s - (long long)tile * nk);
+    place();
+  }
+  __device__ void place() { mt = tile / ntiles, nt = tile - mt * ntiles; }
+  __device__ void next() {
+    if (++ks == nk) ks = 0, tile += stride, place();
+  }
+};
+
+// bounded wait that also ends when another role of the CTA gave up
+__device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, int* abort_flag, DevStatus* st, uint32_t where) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15u) == 15u && *(volatile int*)abort_flag) return false;
+  }
+  dev_fail(st, DEV_TIMEOUT, where, 0u);
+  atomicExch(abort_flag, 1);
+  return false;
+}
+
+template <bool NV, int NT>
+__global__ void __launch_bounds__(kGThreads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                    Fp4GemmArgs a) {
+  using S = GShape<NV, NT>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t s_full[S::kStages];
+  __shared__ __align__(8) uint64_t s_empty[S::kStages];
+  __shared__ __align__(8) uint64_t s_tfull[2], s_tempty[2];
+  __shared__ __align__(8) uint64_t s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const Fp4GemmPlan& P = a.plan;
+  const int nk = P.nk;
+  const int tiles = P.mtiles * P.ntiles;
+  const int nblocks = a.d_in / (NV ? 16 : 32);
+  const size_t tpr = fp4_tiles_per_row(nblocks);
+  const GDeal deal{(long long)tiles * nk, (int)gridDim.x};
+  const int n = P.split ? (int)(deal.first(blockIdx.x + 1) - deal.first(blockIdx.x))
+                        : ((tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * nk;   // this CTA's steps
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_tfull[b], 1);
+      mbar_init(&s_tempty[b], 4);
+    }
+    mbar_init(&s_done, 1);
+    mbar_fence_init();
+    s_abort = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  g_before();
+  __syncthreads();
+  g_after();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- copies ----
+      // a row's last step may have fewer scale tiles, the last tokens' tile only one of two
+      auto atoms_at = [&](int ks) { return gmin(S::kAtoms, (int)tpr - ks * S::kAtoms); };
+      auto token_tiles = [&](int nt) { return gmin(S::kRT, (a.T - nt * NT + 127) / 128); };
+      auto copy_w = [&](const GWalk& w, int sl) {
+        const int at = atoms_at(w.ks);
+        const uint32_t st = base + (uint32_t)(sl * S::kStage);
+        mbar_arrive_expect_tx(&s_full[sl], (uint32_t)(kGABytes + S::kB + at * kSfTile * (1 + token_tiles(w.nt))));
+        g_tma(st, &map_w, w.ks * (kGK / 2), w.mt * kGM, &s_full[sl]);
+        g_bulk(st + kGABytes + S::kB, a.ws + ((size_t)w.mt * tpr + (size_t)w.ks * S::kAtoms) * kSfTile,
+               (uint32_t)(at * kSfTile), &s_full[sl]);
+      };
+      auto copy_x = [&](const GWalk& w, int sl) {
+        const int at = atoms_at(w.ks);
+        const uint32_t st = base + (uint32_t)(sl * S::kStage);
+        g_tma(st + kGABytes, &map_x, w.ks * (kGK / 2), w.nt * NT, &s_full[sl]);
+        const int rts = token_tiles(w.nt);
+        for (int r = 0; r < rts; ++r)
+          g_bulk(st + kGABytes + S::kB + S::kSfA + (uint32_t)(r * S::kAtoms * kSfTile),
+                 a.xs + ((size_t)(w.nt * S::kRT + r) * tpr + (size_t)w.ks * S::kAtoms) * kSfTile,
+                 (uint32_t)(at * kSfTile), &s_full[sl]);
+      };
+      const int head = n < S::kStages ? n : S::kStages;
+      GWalk w(P, deal), wx(P, deal);
+      for (int i = 0; i < head; ++i, w.next()) copy_w(w, i);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int i = 0; i < head; ++i, wx.next()) copy_x(wx, i);
+      int i = head;
+      for (int sl = 0, ph = 0; i < n; ++i, w.next()) {
+        if (!g_wait(&s_empty[sl], (uint32_t)ph, &s_abort, a.status, 60)) break;
+        copy_w(w, sl);
+        copy_x(w, sl);
+        if (++sl == S::kStages) sl = 0, ph ^= 1;
+      }
+      // after a give-up: let the copies in flight land
+      if (*(volatile int*)&s_abort)
+        for (int j = 0; j < S::kStages && j < i; ++j) {
+          const int g = i - 1 - j;
+          mbar_wait(&s_full[g % S::kStages], (uint32_t)(g / S::kStages) & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- scales and MMAs ----
+      int piece = -1;
+      bool fresh = true;
+      GWalk w(P, deal);
+      for (int i = 0, sl = 0, ph = 0; i < n; ++i, w.next()) {
+        const int ks = w.ks;
+        if (i == 0 || ks == 0) {             // a new tile: its accumulator is free?
+          ++piece;
+          fresh = true;
+          if (piece >= S::kNacc &&
+              !g_wait(&s_tempty[piece % S::kNacc], (uint32_t)((piece / S::kNacc) - 1) & 1u, &s_abort, a.status, 61))
+            break;
+          g_after();
+        }
+        if (!g_wait(&s_full[sl], (uint32_t)ph, &s_abort, a.status, 62)) break;
+        g_after();
+        const uint32_t st = base + (uint32_t)(sl * S::kStage);
+        const uint32_t acc = tmem + (uint32_t)((piece % S::kNacc) * S::kAcc);
+        const uint32_t sfa = tmem + (uint32_t)(S::kNacc * S::kAcc + sl * S::kSfCols);
+        const uint32_t sfb = sfa + S::kAtoms * 4;
+#pragma unroll
+        for (int t = 0; t < S::kAtoms; ++t) {
+          g_cp_sf(sfa + t * 4, g_desc(st + kGABytes + S::kB + t * kSfTile, 128, 0));
+#pragma unroll
+          for (int r = 0; r < S::kRT; ++r)
+            g_cp_sf(sfb + (t * S::kRT + r) * 4,
+                    g_desc(st + kGABytes + S::kB + S::kSfA + (r * S::kAtoms + t) * kSfTile, 128, 0));
+        }
+        const int rest = a.d_in - ks * kGK;                    // inputs from this step on
+#pragma unroll
+        for (int kk = 0; kk < kGK / 64; ++kk) {
+          if (kk * 64 < rest) {
+            const uint64_t ad = g_desc(st + kk * 32, 1024, 2);
+            const uint64_t bd = g_desc(st + kGABytes + kk * 32, 1024, 2);
+            const int t = NV ? kk : kk >> 1;
+            const uint32_t id = NV ? 0u : (uint32_t)(kk & 1) * 2u;
+            g_mma<NV>(acc, ad, bd, g_idesc<NV, NT>(id), sfa + t * 4, sfb + t * S::kRT * 4, fresh ? 0u : 1u);
+            fresh = false;
+          }
+        }
+        g_commit(&s_empty[sl]);
+        if (ks == nk - 1 || i == n - 1) g_commit(&s_tfull[piece % S::kNacc]);
+        if (++sl == S::kStages) sl = 0, ph ^= 1;
+      }
+      g_commit(&s_done);                    // every MMA issued has completed when this arrives
+      mbar_wait(&s_done, 0u);
+    }
+  } else {
+    // ---- results ----
+    asm volatile("griddepcontrol.wait;" ::: "memory");         // the tensor scale, and y's last readers
+    const int q = warp & 3;
+    float scale = 1.0f;
+    if (NV) scale = __fmul_rn(a.x_scale ? *(volatile const float*)a.x_scale : 1.0f,
+                              a.w_scale ? *(volatile const float*)a.w_scale : 1.0f);
+    int piece = 0;
+    GWalk w(P, deal);
+    for (int left = n; left > 0; ++piece) {
+      const int t = w.tile, mt = w.mt, nt = w.nt, ks0 = w.ks;
+      const int len = gmin(left, nk - ks0);
+      const bool whole = ks0 == 0 && len == nk;
+      const int col = mt * kGM + q * 32 + lane;
+      const int tok0 = nt * NT, ntok = gmin(NT, a.T - tok0);
+      // after a give-up the pieces are not read, but their hand-overs still
+      // take place, so that the tickets return to zero
+      const bool ok = g_wait(&s_tfull[piece % S::kNacc], (uint32_t)(piece / S::kNacc) & 1u, &s_abort, a.status, 63);
+      g_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((piece % S::kNacc) * S::kAcc);
+      // a piece that starts inside its tile is its CTA's first: slot 0; one that
+      // ends inside is its last: slot 1
+      float* part = a.parts + (((size_t)blockIdx.x * 2 + (ks0 ? 0 : 1)) * NT) * kGM + q * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < ntok && ok; c += 8) {
+        uint32_t v[8];
+        g_ld8(acc + (uint32_t)c, v);
+        g_ld_wait();
+        if (whole) {
+          if (col < a.d_out) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (c + e < ntok) {
+                const size_t o = (size_t)(tok0 + c + e) * a.d_out + col;
+                const float f = NV ? __fmul_rn(__uint_as_float(v[e]), scale) : __uint_as_float(v[e]);
+                if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(f);
+                else reinterpret_cast<float*>(a.y)[o] = f;
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e < ntok) __stcg(part + (size_t)(c + e) * kGM, __uint_as_float(v[e]));
+        }
+      }
+      g_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_tempty[piece % S::kNacc]);
+      if (!whole) {
+        // shared tile: the last of its CTAs adds the parts, in step order
+        const int c0 = deal.owner((long long)t * nk), c1 = deal.owner((long long)(t + 1) * nk - 1);
+        __threadfence();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (threadIdx.x == 64) {
+          const int before = atomicAdd(&a.tickets[t], 1);
+          s_last = before == c1 - c0;
+          if (before == c1 - c0) a.tickets[t] = 0;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (s_last) {
+          __threadfence();
+          if (col < a.d_out) {
+            const float* p0 = a.parts + q * 32 + lane;
+#pragma unroll 4
+            for (int c = 0; c < ntok; ++c) {
+              float sum = __ldcg(p0 + (((size_t)c0 * 2 + 1) * NT + c) * kGM);
+              for (int k = c0 + 1; k <= c1; ++k) sum += __ldcg(p0 + (((size_t)k * 2) * NT + c) * kGM);
+              const float f = NV ? __fmul_rn(sum, scale) : sum;
+              const size_t o = (size_t)(tok0 + c) * a.d_out + col;
+              if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(f);
+              else reinterpret_cast<float*>(a.y)[o] = f;
+            }
+          }
+        }
+      }
+      left -= len;
+      w.ks = nk - 1;
+      w.next();
+    }
+  }
+  g_before();
+  __syncthreads();
+  if (warp == 1) {
+    g_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode_fn() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// codes [rows][pitch bytes]: box of 128 bytes (256 values) x box_rows, 128-byte swizzle
+bool g_map(CUtensorMap* m, const void* ptr, uint64_t pitch, uint64_t rows, uint32_t box_rows) {
+  auto fn = g_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {pitch, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {kGK / 2, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool NV, int NT>
+cudaError_t g_launch(const CUtensorMap& mw, const CUtensorMap& mx, const Fp4GemmArgs& a, cudaStream_t s) {
+  static unsigned configured = 0;
+  cudaError_t e = ensure_smem_attr(fp4_gemm_kernel<NV, NT>, GShape<NV, NT>::kSmem, &configured);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(fp4_gemm_kernel<NV, NT>, dim3((unsigned)a.plan.grid), dim3(kGThreads), (size_t)GShape<NV, NT>::kSmem, s,
+                 mw, mx, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+template <bool NV>
+cudaError_t g_dispatch(const CUtensorMap& mw, const CUtensorMap& mx, const Fp4GemmArgs& a, cudaStream_t s) {
+  switch (a.plan.nt) {
+    case 8: return g_launch<NV, 8>(mw, mx, a, s);
+    case 16: return g_launch<NV, 16>(mw, mx, a, s);
+    case 32: return g_launch<NV, 32>(mw, mx, a, s);
+    case 64: return g_launch<NV, 64>(mw, mx, a, s);
+    case 128: return g_launch<NV, 128>(mw, mx, a, s);
+    case 256: return g_launch<NV, 256>(mw, mx, a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+bool fp4_gemm_supported() { return g_encode_fn() != nullptr; }
+
+Fp4GemmPlan plan_fp4_gemm(int T, int d_in, int d_out) {
+  Fp4GemmPlan p;
+  p.mtiles = (d_out + kGM - 1) / kGM;
+  p.nk = (d_in + kGK - 1) / kGK;
+  // tiles of 256 tokens where they give every SM one, else the smallest tile
+  // that holds the tokens (at most 128)
+  if (T > 128 && (long)p.mtiles * ((T + 255) / 256) >= kNumSMs) {
+    p.nt = 256;
+    p.ntiles = (T + 255) / 256;
+    p.split = 0;
+    p.grid = kNumSMs;
+    return p;
+  }
+  p.nt = 8;
+  while (p.nt < T && p.nt < 128) p.nt *= 2;
+  p.ntiles = (T + p.nt - 1) / p.nt;
+  p.split = 1;
+  // at least 2 steps per CTA: a shared tile's partial sums and hand-over cost
+  // more than a step
+  const long total = (long)p.mtiles * p.ntiles * p.nk;
+  long g = total / 2;
+  if (g < 1) g = 1;
+  p.grid = (int)(g < kNumSMs ? g : kNumSMs);
+  p.parts_elems = (size_t)p.grid * 2 * p.nt * kGM;
+  p.tickets = p.mtiles * p.ntiles;
+  return p;
+}
+
+cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t s) {
+  CUtensorMap mw, mx;
+  if (!g_map(&mw, a.wc, (uint64_t)(a.d_in / 2), (uint64_t)a.d_out, kGM) ||
+      !g_map(&mx, a.xc, (uint64_t)(a.d_in / 2), (uint64_t)a.T, (uint32_t)a.plan.nt))
+    return cudaErrorInvalidValue;
+  return a.format == QS_FP4_NV ? g_dispatch<true>(mw, mx, a, s) : g_dispatch<false>(mw, mx, a, s);
+}
+
+}  // namespace qs
