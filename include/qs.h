@@ -109,6 +109,9 @@ typedef enum qs_fp4_scale_layout {
 #define QS_PREFILL_MIN_T 64
 /* Largest Block Q-Sparse block (tokens sharing one selection). */
 #define QS_MAX_BLOCK 64
+/* Limits of qs_moe_ffn. */
+#define QS_MOE_MAX_EXPERTS 256
+#define QS_MOE_MAX_TOP_K 16
 /* Number of cudaEvent_t handles qs_sparse_ffn records when given phase events. */
 #define QS_FFN_PHASE_EVENTS 5
 /* ... and qs_sparse_linear / qs_quant_sparse_linear (before the top-K, after
@@ -472,10 +475,57 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
                                const uint8_t* w_scales, const float* w_scale, void* y, int y_dtype,
                                void* const* phase_events, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * qs_moe_ffn -- a mixture-of-experts FFN layer, router included, as one kernel
+ *   (per 64 tokens).
+ *   Source: Turbo Sparse summary (blog.csdn.net): the method applied to a
+ *   model of experts, of which each token uses 2 of 8, and Eq. 2 (dReLU); the
+ *   squared-ReLU form is that of qs_sparse_ffn.  The pages give no router; the
+ *   usual one is built:
+ *     l = x.W_r^T; the token's experts e_1..e_K are those of its top_k largest
+ *     l (ties -> lower expert); p = softmax over l[e_1..e_K]
+ *     h_j = act(x.W_up[e_j]^T, x.W_gate[e_j]^T)         (float32)
+ *     y   = sum_j p_j h_j.W_down[e_j]^T
+ *   x is used dense.  A neuron whose first factor (dReLU: the gate; squared
+ *   ReLU: up) is 0 for every token of its expert is not computed further, and
+ *   a down row is read only where some token's h is not 0: exact skipping, as
+ *   in qs_sparse_ffn_gate_first.  Weights of experts that no token uses are
+ *   not read.  Each expert weight is read once per 32 of its tokens.
+ *
+ *   x         [T, d_model] bf16.
+ *   w_router  [n_experts, d_model] bf16.
+ *   w_gate, w_up, w_down   [n_experts, d_ff, d_model], neuron by neuron: gate
+ *             and up output-major (nn.Linear), down input-major (W_down^T).
+ *             s_gate, s_up, s_down all NULL: bf16.  All given: 4-bit codes
+ *             [n_experts, d_ff, d_model/2] and scales [n_experts, d_ff,
+ *             d_model/32] (qs_fp4_quantize of these matrices, QS_FP4_MX,
+ *             QS_FP4_SCALES_ROWS); they enter as the numbers they stand for,
+ *             x is not quantised.
+ *   b_gate, b_up  [n_experts, d_ff] f32 or NULL (= 0); QS_ACT_DRELU only.
+ *   y         [T, d_model] `y_dtype` (bf16 or f32) out.
+ *   experts   [T, top_k] int32 out or NULL: e_1..e_K, largest l first.
+ *   weights   [T, top_k] f32 out or NULL: p.
+ *   ws        qs_workspace_size(QS_OP_MOE_FFN, T, d_model, d_ff, top_k) bytes.
+ *   h enters the down projection as the sum of two bf16 numbers (relative
+ *   error 2^-17).  Sums are taken in a fixed order: the same call gives the
+ *   same bits.  Non-finite values propagate where they are computed with (a
+ *   closed neuron's other weights are not).
+ *   d_model must be a multiple of 32, d_ff of 8.
+ *   Errors: INVALID_ARG (also: some but not all scales given, top_k >
+ *   n_experts), ALIGNMENT, WORKSPACE, UNSUPPORTED (d_model or d_ff above
+ *   QS_MAX_ROW, n_experts above QS_MOE_MAX_EXPERTS, top_k above
+ *   QS_MOE_MAX_TOP_K), CUDA.
+ */
+qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts, int top_k, int act,
+                     const void* w_router, const void* w_gate, const void* w_up, const void* w_down,
+                     const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down,
+                     const float* b_gate, const float* b_up, void* y, int y_dtype, int32_t* experts,
+                     float* weights, void* ws, size_t ws_bytes, void* stream);
+
 /* Bytes of workspace `op` needs for these sizes (0 if the sizes are invalid).
  * Arguments: QS_OP_TOPK_MASK (T, d, 0, k); QS_OP_SPARSE_LINEAR (T, d_in, d_out,
  * k); QS_OP_SPARSE_FFN, QS_OP_SPARSE_FFN_GATE_FIRST and QS_OP_QUANT_SPARSE_FFN (T,
- * d_model, d_ff, k_h);
+ * d_model, d_ff, k_h); QS_OP_MOE_FFN (T, d_model, d_ff, top_k);
  * QS_OP_QUANT_SPARSE_LINEAR and QS_OP_FP4_SPARSE_LINEAR (T, d_in, d_out, k);
  * QS_OP_TERNARY_PACK (0, d_in, d_out, 0).  The dtype does
  * not change the size, and a workspace of this size also serves calls with the

@@ -8,5 +8,5 @@ from .qs_oracle import (  # noqa: F401
     relu, ffn_hidden,
     sparse_ffn, absmax_quantize, ternary_quantize, ternary_pack, ternary_unpack,
     quant_sparse_linear, ffn_hidden_f32, quant_sparse_ffn, max_rel_err,
-    E2M1, e4m3_grid, fp4_quantize, fp4_pack, fp4_tile_scales, fp4_sparse_linear,
+    E2M1, e4m3_grid, fp4_quantize, fp4_pack, fp4_tile_scales, fp4_sparse_linear, moe_ffn,
 )

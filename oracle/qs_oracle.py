@@ -479,6 +479,33 @@ def fp4_sparse_linear(x, w_values, k: int, fmt: str, x_scale: float = 1.0) -> di
     return dict(y=xq @ w.T, mag=np.abs(xq) @ np.abs(w).T, xq=xq)
 
 
+# --------------------------------------------------------------------------
+# mixture of experts
+# --------------------------------------------------------------------------
+
+def moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act: str, b_gate=None, b_up=None) -> dict:
+    """y = sum over each token's top_k experts of p_e h_e . W_down[e] (fp64).
+
+    x [T, d_model], w_router [E, d_model], w_gate / w_up / w_down
+    [E, d_ff, d_model].  Experts: the top_k largest logits, ties to the lower
+    expert, largest first; p = softmax over them.
+    """
+    x = np.asarray(x, dtype=np.float64)
+    logits = x @ np.asarray(w_router, dtype=np.float64).T
+    experts = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    best = np.take_along_axis(logits, experts, 1)
+    p = np.exp(best - best[:, :1])
+    p /= p.sum(1, keepdims=True)
+    y = np.zeros_like(x)
+    for t in range(x.shape[0]):
+        for j, e in enumerate(experts[t]):
+            wg, wu, wd = (np.asarray(w[e], dtype=np.float64) for w in (w_gate, w_up, w_down))
+            h = ffn_hidden(wu @ x[t], wg @ x[t], act, None if b_up is None else b_up[e],
+                           None if b_gate is None else b_gate[e])
+            y[t] += p[t, j] * (h @ wd)
+    return dict(y=y, experts=experts, weights=p, logits=logits)
+
+
 def max_rel_err(y, ref) -> float:
     """max over rows of max_j |y - ref| / max_j |ref| (row infinity norm).
 

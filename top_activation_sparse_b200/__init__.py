@@ -59,6 +59,8 @@ QS_MAX_BLOCK = 64
 QS_NOALLOC_SCRATCH_BYTES = 4 << 20
 QS_PREFILL_MIN_T = 64
 QS_FFN_PHASE_EVENTS = 5
+QS_MOE_MAX_EXPERTS = 256
+QS_MOE_MAX_TOP_K = 16
 QS_LINEAR_PHASE_EVENTS = 3
 
 _FP4_FORMATS = {"mx": QS_FP4_MX, "nv": QS_FP4_NV}
@@ -91,6 +93,8 @@ _SIGNATURES = {
     "qs_fp4_scale_bytes": (_sz, [ctypes.c_int64, _i, _i, _i]),
     "qs_fp4_sparse_linear": (_i, [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp,
                                   _vp, _sz, _vp]),
+    "qs_moe_ffn": (_i, [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                        _i, _vp, _vp, _vp, _sz, _vp]),
     "qs_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "qs_workspace_init": (_i, [_vp, _sz, _vp]),
     "qs_device_status": (_i, [_vp, _vp]),
@@ -647,6 +651,51 @@ def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch
     return y
 
 
+class MoeResult(NamedTuple):
+    y: torch.Tensor
+    experts: torch.Tensor | None
+    weights: torch.Tensor | None
+
+
+def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, s_up=None, s_down=None,
+               b_gate=None, b_up=None, y=None, y_dtype=None, experts=None, weights=None, ws=None,
+               stream=None) -> MoeResult:
+    """Mixture-of-experts FFN layer, router included: x [T, d_model] bf16,
+    w_router [E, d_model] bf16, w_gate / w_up / w_down [E, d_ff, d_model] bf16,
+    or 4-bit codes [E, d_ff, d_model/2] with scales s_* [E, d_ff, d_model/32]
+    (qs_fp4_quantize, "mx", "rows").  experts / weights: True to get each
+    token's experts and their shares."""
+    dev = _need_cuda(x, w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, b_gate, b_up)
+    T, d_model = x.shape
+    E, d_ff = w_gate.shape[0], w_gate.shape[1]
+    if x.dtype != torch.bfloat16 or w_router.dtype != torch.bfloat16 or tuple(w_router.shape) != (E, d_model):
+        raise ValueError("x and w_router [E, d_model] must be bfloat16")
+    fp4 = s_gate is not None
+    shape, dtype = ((E, d_ff, d_model // 2), torch.uint8) if fp4 else ((E, d_ff, d_model), torch.bfloat16)
+    for w in (w_gate, w_up, w_down):
+        if tuple(w.shape) != shape or w.dtype != dtype:
+            raise ValueError(f"expert weights must be {shape} {dtype}")
+    for s in (s_gate, s_up, s_down):
+        if (s is not None) != fp4 or (fp4 and (tuple(s.shape) != (E, d_ff, d_model // 32) or s.dtype != torch.uint8)):
+            raise ValueError(f"scales must be given for all three weights or none, {(E, d_ff, d_model // 32)} uint8")
+    for b in (b_gate, b_up):
+        if b is not None and (tuple(b.shape) != (E, d_ff) or b.dtype != torch.float32):
+            raise ValueError("biases must be [E, d_ff] float32")
+    act_code = _ACTS[act] if isinstance(act, str) else int(act)
+    with _call_context(dev, stream):
+        y = _out(y if y is not None else True, (T, d_model), y.dtype if y is not None else (y_dtype or x.dtype), dev)
+        experts = _out(experts, (T, top_k), torch.int32, dev)
+        weights = _out(weights, (T, top_k), torch.float32, dev)
+        _need_cuda(x, y, experts, weights)
+        ws = _stream_workspace(ws, QS_OP_MOE_FFN, T, d_model, d_ff, top_k, dev)
+        _check("qs_moe_ffn", lib().qs_moe_ffn(
+            x.data_ptr(), T, d_model, d_ff, E, top_k, act_code, w_router.data_ptr(), w_gate.data_ptr(),
+            w_up.data_ptr(), w_down.data_ptr(), _ptr(s_gate), _ptr(s_up), _ptr(s_down), _ptr(b_gate),
+            _ptr(b_up), y.data_ptr(), _dtype_code(y), _ptr(experts), _ptr(weights), ws.data_ptr(),
+            ws.numel(), _stream_ptr(None)))
+    return MoeResult(y, experts, weights)
+
+
 def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_out=None, ws=None,
                     stream=None):
     """Ternary-quantize W [d_out, d_in] f32 and pack it input-major 2-bit.
@@ -669,4 +718,4 @@ def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_ou
 
 __all__ = [n for n in dir() if n.startswith(("qs_", "QS_"))] + [
     "lib", "new_workspace", "header_functions", "QSError", "TopkResult", "FfnResult",
-    "QuantResult", "BackwardResult", "QuantFfnResult", "Fp4Result"]
+    "QuantResult", "BackwardResult", "QuantFfnResult", "Fp4Result", "MoeResult"]

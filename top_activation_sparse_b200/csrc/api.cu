@@ -6,6 +6,7 @@
 
 #include "fp4.cuh"
 #include "gate_first.cuh"
+#include "moe.cuh"
 #include "qs_internal.cuh"
 
 namespace qs {
@@ -29,7 +30,11 @@ constexpr int kUnionX = 4096, kUnionH = 4096 + QS_MAX_ROW / 32;
 constexpr int kGateBits = kUnionH + QS_MAX_ROW / 32;
 // grid-barrier counters of the one-kernel FFN (zero between calls)
 constexpr int kTkFusedBar = kGateBits + QS_MAX_ROW / 32;
-static_assert(kTkFusedBar + 5 <= (int)(64 * 1024 / 4), "ticket region too small");
+// counters of the mixture-of-experts layer (zero between calls)
+constexpr int kTkMoe = kTkFusedBar + 8;
+static_assert(kTkMoe + MC_COUNT <= (int)(64 * 1024 / 4), "ticket region too small");
+static_assert(QS_MOE_MAX_EXPERTS == kMoeMaxE && QS_MOE_MAX_TOP_K == kMoeMaxK && QS_PREFILL_MIN_T == kMoeMaxT,
+              "limits of the mixture-of-experts layer");
 
 size_t align_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
@@ -191,6 +196,22 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       // the NV form has more scales than the MX form
       L->fp4_scales = take(qs_fp4_scale_bytes(T, d_in, QS_FP4_NV, QS_FP4_SCALES_TILED));
       L->parts1_elems = plan_fp4_gemm(T, d_in, d_out).parts_elems;
+      L->parts1 = take(L->parts1_elems * sizeof(float));
+      break;
+    }
+    case QS_OP_MOE_FFN: {
+      // (k: experts per token; the number of experts does not enter)
+      if (T < 1 || d_in < 32 || d_out < 8 || d_in > QS_MAX_ROW || d_out > QS_MAX_ROW || k < 1 ||
+          k > kMoeMaxK || (d_in % 32) != 0 || (d_out % 8) != 0)
+        return false;
+      const size_t slots = (size_t)Tc * k;
+      L->moe_logits = take((size_t)Tc * kMoeMaxE * sizeof(float));
+      L->moe_table = take(kMtSize * sizeof(int32_t));
+      L->moe_share = take(slots * sizeof(float));
+      L->h = take(slots * d_out * sizeof(float));
+      L->moe_nz = take((slots < kMoeMaxE ? slots : kMoeMaxE) * d_out);
+      // (a shorter last chunk may split more; its rows are at most as many)
+      L->parts1_elems = (size_t)kMoePartRows * d_in;
       L->parts1 = take(L->parts1_elems * sizeof(float));
       break;
     }
@@ -913,6 +934,62 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   g.plan = plan;
   QS_TRY_CUDA(launch_fp4_gemm(g, s));
   QS_TRY_CUDA(mark(2));
+  return QS_OK;
+}
+
+qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts, int top_k, int act,
+                     const void* w_router, const void* w_gate, const void* w_up, const void* w_down,
+                     const uint8_t* s_gate, const uint8_t* s_up, const uint8_t* s_down,
+                     const float* b_gate, const float* b_up, void* y, int y_dtype, int32_t* experts,
+                     float* weights, void* ws, size_t ws_bytes, void* stream) {
+  const bool fp4 = s_gate != nullptr;
+  if (x == nullptr || w_router == nullptr || w_gate == nullptr || w_up == nullptr || w_down == nullptr ||
+      y == nullptr || !valid_dtype(y_dtype) || T < 1 || d_model < 1 || d_ff < 1 || n_experts < 1 ||
+      top_k < 1 || top_k > n_experts || (act != QS_ACT_RELU2_GLU && act != QS_ACT_DRELU) ||
+      (s_up != nullptr) != fp4 || (s_down != nullptr) != fp4)
+    return QS_ERR_INVALID_ARG;
+  if (d_model > QS_MAX_ROW || d_ff > QS_MAX_ROW || n_experts > kMoeMaxE || top_k > kMoeMaxK)
+    return QS_ERR_UNSUPPORTED;
+  if ((d_model % 32) != 0 || (d_ff % 8) != 0) return QS_ERR_ALIGNMENT;
+  for (const void* p : {x, w_router, w_gate, w_up, w_down, (const void*)s_gate, (const void*)s_up,
+                        (const void*)s_down, (const void*)b_gate, (const void*)b_up, (const void*)y,
+                        (const void*)experts, (const void*)weights})
+    if (!aligned16(p)) return QS_ERR_ALIGNMENT;
+  WsLayout L;
+  const qs_status st = check_ws(QS_OP_MOE_FFN, T, d_model, d_ff, top_k, ws, ws_bytes, &L);
+  if (st != QS_OK) return st;
+  WsView w{(unsigned char*)ws};
+  MoeArgs a;
+  a.d_model = d_model; a.d_ff = d_ff; a.E = n_experts; a.top_k = top_k;
+  a.drelu = act == QS_ACT_DRELU;
+  a.fp4 = fp4;
+  a.router = (const __nv_bfloat16*)w_router;
+  a.w1 = (const uint8_t*)(a.drelu ? w_gate : w_up);
+  a.w2 = (const uint8_t*)(a.drelu ? w_up : w_gate);
+  a.wd = (const uint8_t*)w_down;
+  a.s1 = a.drelu ? s_gate : s_up;
+  a.s2 = a.drelu ? s_up : s_gate;
+  a.sd = s_down;
+  a.b1 = a.drelu ? b_gate : nullptr;
+  a.b2 = a.drelu ? b_up : nullptr;
+  a.y_bf16 = y_dtype == QS_BF16;
+  a.ctl = w.ticket(L, kTkMoe);
+  a.logits = w.at<float>(L.moe_logits);
+  a.table = w.at<int32_t>(L.moe_table);
+  a.share = w.at<float>(L.moe_share);
+  a.h = w.at<float>(L.h);
+  a.nz = w.at<uint8_t>(L.moe_nz);
+  a.parts = w.at<float>(L.parts1);
+  a.status = w.status();
+  for (int t0 = 0; t0 < T; t0 += kMoeMaxT) {
+    a.T = T - t0 < kMoeMaxT ? T - t0 : kMoeMaxT;
+    a.x = (const __nv_bfloat16*)x + (size_t)t0 * d_model;
+    a.y = (unsigned char*)y + (size_t)t0 * d_model * elem_bytes(y_dtype);
+    a.experts = experts ? experts + (size_t)t0 * top_k : nullptr;
+    a.weights = weights ? weights + (size_t)t0 * top_k : nullptr;
+    a.plan = plan_moe(a.T, d_model, d_ff, n_experts, top_k, fp4);
+    QS_TRY_CUDA(launch_moe(a, (cudaStream_t)stream));
+  }
   return QS_OK;
 }
 

@@ -1,0 +1,65 @@
+// Mixture-of-experts FFN layer for a few tokens (moe.cu): arguments and plan.
+#pragma once
+
+#include "qs_internal.cuh"
+
+namespace qs {
+
+constexpr int kMoeMaxT = 64;          // tokens per launch
+constexpr int kMoePartRows = 1024;    // rows of partial sums (splits x tokens x experts per token)
+
+// counters, zero between calls
+enum MoeCtl { MC_QUEUE = 0, MC_ROUTED = 1, MC_READY = 2, MC_HIDDEN = 3, MC_DOWN = 4, MC_EXIT = 5, MC_COUNT = 8 };
+
+struct MoePlan {
+  int grid = 0;
+  int router_items = 0;     // queue items of the router
+  int hidden_items = 0;     // ... of the hidden layer
+  int out_items = 0;        // ... of the final sums
+  int col_tiles = 0;        // column tiles of the down projection
+  int tile_warps = 0;       // warps of a tile (each a strip of columns)
+  int max_splits = 0;       // splits of an expert's neurons the buffers hold
+};
+MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4);
+
+struct MoeArgs {
+  const __nv_bfloat16* x = nullptr;       // [T, d_model]
+  int T = 0, d_model = 0, d_ff = 0, E = 0, top_k = 0;
+  int drelu = 0;                          // else ReLU(u)^2 g
+  int fp4 = 0;
+  const __nv_bfloat16* router = nullptr;  // [E, d_model]
+  // the matrix whose ReLU decides which neurons are open comes first: gate for
+  // dReLU, up for squared ReLU.  [E, d_ff, d_model] bf16, or codes
+  const uint8_t* w1 = nullptr;
+  const uint8_t* w2 = nullptr;
+  const uint8_t* wd = nullptr;
+  const uint8_t* s1 = nullptr;            // MX scales [E, d_ff, d_model/32]
+  const uint8_t* s2 = nullptr;
+  const uint8_t* sd = nullptr;
+  const float* b1 = nullptr;              // [E, d_ff] or NULL (dReLU)
+  const float* b2 = nullptr;
+  void* y = nullptr;                      // [T, d_model]
+  int y_bf16 = 1;
+  int32_t* experts = nullptr;             // [T, top_k] or NULL
+  float* weights = nullptr;               // [T, top_k] or NULL
+  // workspace
+  int32_t* ctl = nullptr;                 // MC_COUNT counters
+  float* logits = nullptr;                // [T, E]
+  int32_t* table = nullptr;               // routing tables (see moe.cu)
+  float* share = nullptr;                 // [T, top_k]
+  float* h = nullptr;                     // [T * top_k, d_ff]
+  uint8_t* nz = nullptr;                  // [min(E, T * top_k), d_ff]
+  float* parts = nullptr;                 // [splits][T * top_k][d_model]
+  DevStatus* status = nullptr;
+  MoePlan plan{};
+};
+cudaError_t launch_moe(const MoeArgs& a, cudaStream_t s);
+
+// routing tables, int32: [0] active experts A, then per active expert its
+// number, first slot and number of tokens, then per slot its token, then per
+// (token, choice) its slot
+constexpr int kMoeMaxE = 256, kMoeMaxK = 16, kMoeMaxSlots = kMoeMaxT * kMoeMaxK;
+constexpr int kMtExpert = 8, kMtFirst = kMtExpert + kMoeMaxE, kMtCount = kMtFirst + kMoeMaxE,
+              kMtToken = kMtCount + kMoeMaxE, kMtSlot = kMtToken + kMoeMaxSlots, kMtSize = kMtSlot + kMoeMaxSlots;
+
+}  // namespace qs

@@ -223,6 +223,10 @@ struct WsLayout {
   size_t xs_masked = 0;       // [T, d_in] X_sparse in x's type (4-bit projection)
   size_t fp4_codes = 0;       // [T, d_in/2] 4-bit codes of X_sparse
   size_t fp4_scales = 0;      // their scales, tiled
+  size_t moe_logits = 0;      // [Tc, experts] f32 (mixture of experts)
+  size_t moe_table = 0;       // routing tables, int32
+  size_t moe_share = 0;       // [Tc, top_k] f32
+  size_t moe_nz = 0;          // [active experts, d_ff] flags
   size_t alpha_parts = 0;     // f64 partial sums (ternary pack)
   size_t alpha = 0;           // f32 (ternary pack)
   size_t fpug = 0;            // one-kernel FFN: per-split up/gate partial sums
