@@ -506,8 +506,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   experts   [T, top_k] int32 out or NULL: e_1..e_K, largest l first.
  *   weights   [T, top_k] f32 out or NULL: p.
  *   ws        qs_workspace_size(QS_OP_MOE_FFN, T, d_model, d_ff, top_k) bytes.
- *   h enters the down projection as the sum of two bf16 numbers (relative
- *   error 2^-17).  Sums are taken in a fixed order: the same call gives the
+ *   h enters the down projection as the sum of three bf16 numbers, i.e. with
+ *   all 24 bits.  Sums are taken in a fixed order: the same call gives the
  *   same bits.  Non-finite values propagate where they are computed with (a
  *   closed neuron's other weights are not).
  *   d_model must be a multiple of 32, d_ff of 8.

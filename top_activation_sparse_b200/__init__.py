@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 from typing import NamedTuple
@@ -232,6 +233,12 @@ def _workspace(ws, op, T, d_in, d_out, k, device):
     return cur
 
 
+def _current_stream_ptr(dev) -> int:
+    """The device's current stream as the library takes it, without building a
+    Stream object (a third of a small call's time on the host)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _call_context(dev, stream):
     """Run a call's allocations and launch on the tensors' device, and on
     `stream` where one is given."""
@@ -263,7 +270,7 @@ def _stream_workspace(ws, op, T, d_in, d_out, k, device):
         cur = torch.empty(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
         cur[:_WS_COUNTER_BYTES].zero_()
         return cur
-    key = (device, torch.cuda.current_stream(device).cuda_stream, op)
+    key = (device, _current_stream_ptr(device), op)
     cur = _stream_ws.get(key)
     if cur is None or cur.numel() < need:
         cur = _stream_ws[key] = torch.zeros(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
@@ -590,6 +597,7 @@ def _scalar_f32(t, name):
         raise ValueError(f"{name} must be one float32 on the device")
 
 
+@functools.lru_cache(maxsize=4096)
 def qs_fp4_scale_bytes(R: int, d: int, format="mx", scale_layout="tiled") -> int:
     """Bytes of the scales of an [R, d] matrix (0: invalid arguments)."""
     return int(lib().qs_fp4_scale_bytes(int(R), int(d), _fp4_code(_FP4_FORMATS, format),
@@ -620,7 +628,7 @@ def qs_fp4_quantize(x: torch.Tensor, format="mx", scale_layout="tiled", tensor_s
         _need_cuda(x, codes, scales, values)
         _check("qs_fp4_quantize", lib().qs_fp4_quantize(
             x.data_ptr(), _dtype_code(x), R, d, fmt, _ptr(tensor_scale), lay, _ptr(codes),
-            _ptr(scales), _ptr(values), _stream_ptr(None)))
+            _ptr(scales), _ptr(values), _current_stream_ptr(dev)))
     return Fp4Result(codes, scales, values)
 
 
@@ -647,7 +655,7 @@ def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch
         _check("qs_fp4_sparse_linear", lib().qs_fp4_sparse_linear(
             x.data_ptr(), _dtype_code(x), T, d_in, d_out, k, fmt, _ptr(x_scale), w_codes.data_ptr(),
             w_scales.data_ptr(), _ptr(w_scale), y.data_ptr(), _dtype_code(y),
-            _events(phase_events, QS_LINEAR_PHASE_EVENTS), ws.data_ptr(), ws.numel(), _stream_ptr(None)))
+            _events(phase_events, QS_LINEAR_PHASE_EVENTS), ws.data_ptr(), ws.numel(), _current_stream_ptr(dev)))
     return y
 
 
@@ -692,7 +700,7 @@ def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, 
             x.data_ptr(), T, d_model, d_ff, E, top_k, act_code, w_router.data_ptr(), w_gate.data_ptr(),
             w_up.data_ptr(), w_down.data_ptr(), _ptr(s_gate), _ptr(s_up), _ptr(s_down), _ptr(b_gate),
             _ptr(b_up), y.data_ptr(), _dtype_code(y), _ptr(experts), _ptr(weights), ws.data_ptr(),
-            ws.numel(), _stream_ptr(None)))
+            ws.numel(), _current_stream_ptr(dev)))
     return MoeResult(y, experts, weights)
 
 

@@ -195,8 +195,6 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       L->fp4_codes = take((size_t)T * (d_in / 2));
       // the NV form has more scales than the MX form
       L->fp4_scales = take(qs_fp4_scale_bytes(T, d_in, QS_FP4_NV, QS_FP4_SCALES_TILED));
-      L->parts1_elems = plan_fp4_gemm(T, d_in, d_out).parts_elems;
-      L->parts1 = take(L->parts1_elems * sizeof(float));
       break;
     }
     case QS_OP_MOE_FFN: {
@@ -890,7 +888,7 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   const qs_status st = check_ws(QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, ws, ws_bytes, &L);
   if (st != QS_OK) return st;
   const Fp4GemmPlan plan = plan_fp4_gemm(T, d_in, d_out);
-  if (!fp4_gemm_supported() || kTkGemv + plan.tickets > kTkGemvEnd ||
+  if (!fp4_gemm_supported() ||
       (long long)plan.mtiles * plan.ntiles * plan.nk >= (1ll << 31))
     return QS_ERR_UNSUPPORTED;
   WsView w{(unsigned char*)ws};
@@ -928,8 +926,6 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   g.y_bf16 = y_dtype == QS_BF16;
   g.T = T; g.d_in = d_in; g.d_out = d_out;
   g.format = format;
-  g.parts = w.at<float>(L.parts1);
-  g.tickets = w.ticket(L, kTkGemv);
   g.status = w.status();
   g.plan = plan;
   QS_TRY_CUDA(launch_fp4_gemm(g, s));

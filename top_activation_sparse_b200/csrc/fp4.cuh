@@ -81,10 +81,8 @@ struct Fp4GemmPlan {
   int mtiles = 0;      // tiles of 128 outputs
   int ntiles = 0;      // tiles of nt tokens
   int nk = 0;          // steps of 256 inputs
-  int split = 0;       // 1: the steps of all tiles are dealt out evenly, tiles may be shared
+  int cluster = 1;     // CTAs that share a tile's steps
   int grid = 0;
-  size_t parts_elems = 0;
-  int tickets = 0;
 };
 Fp4GemmPlan plan_fp4_gemm(int T, int d_in, int d_out);
 
@@ -99,8 +97,6 @@ struct Fp4GemmArgs {
   int y_bf16 = 1;
   int T = 0, d_in = 0, d_out = 0;
   int format = QS_FP4_MX;
-  float* parts = nullptr;           // shared tiles' partial sums
-  int32_t* tickets = nullptr;       // one per tile, zero between calls
   DevStatus* status = nullptr;
   Fp4GemmPlan plan{};
 };

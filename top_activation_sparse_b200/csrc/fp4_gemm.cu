@@ -20,10 +20,14 @@
 //     stage: the commit that frees the stage frees both) and issues its four
 //     MMAs of K = 64.
 //   * warps 2 to 5 read the accumulator and store y, column by token.
-// Up to 128 tokens the steps of all tiles are dealt out evenly over the SMs
-// (few tiles: a tile's steps are shared by several CTAs, which leave partial
-// sums in the workspace; the last to arrive adds them in the order of their
-// steps, so that results do not depend on timing).  Every wait is bounded.
+// Where the tiles are fewer than the SMs, a cluster of up to 8 CTAs shares a
+// tile's steps: each leaves its partial sums in its own shared memory, and
+// after a cluster barrier each adds a slice of them over the cluster, in the
+// order of the steps (results do not depend on timing, and no partial sum
+// leaves the chip).  An earlier form dealt the steps of all tiles out evenly
+// over 148 CTAs with the partial sums in global memory, handed over by
+// tickets: its fences, tickets and re-reads cost more than the data (one token,
+// 4096 -> 11008: 18.9 us against MEASURE_A now).  Every wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -129,33 +133,18 @@ __device__ __forceinline__ void g_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 __device__ __forceinline__ void g_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The steps [0, total) of all tiles dealt out over `grid` CTAs: CTA c has
-// [first(c), first(c + 1)).
-struct GDeal {
-  long long total;
-  int grid;
-  __host__ __device__ long long first(int c) const { return total * c / grid; }
-  // the CTA that has step s
-  __host__ __device__ int owner(long long s) const {
-    int c = (int)(s * grid / total);
-    while (c + 1 < grid && first(c + 1) <= s) ++c;
-    while (c > 0 && first(c) > s) --c;
-    return c;
-  }
-};
-
-// A CTA's steps in order: a range of all steps (shared tiles), or whole tiles
-// blockIdx.x + i * gridDim.x.
+// A CTA's steps in order: with one CTA per tile the whole tiles blockIdx.x +
+// i * gridDim.x, else its share of its cluster's tile.
 struct GWalk {
   int nk, ntiles, stride;
   int tile, ks, mt, nt;
-  __device__ GWalk(const Fp4GemmPlan& P, const GDeal& deal)
-      : nk(P.nk), ntiles(P.ntiles), stride(P.split ? 1 : (int)gridDim.x) {
-    const long long s = P.split ? deal.first(blockIdx.x) : (long long)blockIdx.x * nk;
-    tile = (int)(s / nk);
-    ks = (int)(s - (long long)tile * nk);
+  __device__ GWalk(const Fp4GemmPlan& P)
+      : nk(P.nk), ntiles(P.ntiles), stride((int)gridDim.x) {
+    tile = (int)blockIdx.x / P.cluster;
+    ks = P.cluster > 1 ? first_step(P, (int)blockIdx.x % P.cluster) : 0;
     place();
   }
+  __device__ static int first_step(const Fp4GemmPlan& P, int rank) { return P.nk * rank / P.cluster; }
   __device__ void place() { mt = tile / ntiles, nt = tile - mt * ntiles; }
   __device__ void next() {
     if (++ks == nk) ks = 0, tile += stride, place();
@@ -173,6 +162,12 @@ __device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, int* abor
   return false;
 }
 
+__device__ __forceinline__ void g_store(const Fp4GemmArgs& a, size_t o, float f, bool nv, float scale) {
+  if (nv) f = __fmul_rn(f, scale);
+  if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(f);
+  else reinterpret_cast<float*>(a.y)[o] = f;
+}
+
 template <bool NV, int NT>
 __global__ void __launch_bounds__(kGThreads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -184,7 +179,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
   __shared__ __align__(8) uint64_t s_tfull[2], s_tempty[2];
   __shared__ __align__(8) uint64_t s_done;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -193,9 +188,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
   const int tiles = P.mtiles * P.ntiles;
   const int nblocks = a.d_in / (NV ? 16 : 32);
   const size_t tpr = fp4_tiles_per_row(nblocks);
-  const GDeal deal{(long long)tiles * nk, (int)gridDim.x};
-  const int n = P.split ? (int)(deal.first(blockIdx.x + 1) - deal.first(blockIdx.x))
-                        : ((tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * nk;   // this CTA's steps
+  const int C = P.cluster, rank = (int)blockIdx.x % C;
+  const int n = C > 1 ? GWalk::first_step(P, rank + 1) - GWalk::first_step(P, rank)
+                      : ((tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * nk;   // this CTA's steps
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
@@ -220,6 +215,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
   g_after();
   const uint32_t tmem = s_tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  float scale = 1.0f;                       // the NV form's tensor scales
 
   if (warp == 0) {
     if (lane == 0) {
@@ -246,7 +243,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                  (uint32_t)(at * kSfTile), &s_full[sl]);
       };
       const int head = n < S::kStages ? n : S::kStages;
-      GWalk w(P, deal), wx(P, deal);
+      GWalk w(P), wx(P);
       for (int i = 0; i < head; ++i, w.next()) copy_w(w, i);
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = 0; i < head; ++i, wx.next()) copy_x(wx, i);
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       // ---- scales and MMAs ----
       int piece = -1;
       bool fresh = true;
-      GWalk w(P, deal);
+      GWalk w(P);
       for (int i = 0, sl = 0, ph = 0; i < n; ++i, w.next()) {
         const int ks = w.ks;
         if (i == 0 || ks == 0) {             // a new tile: its accumulator is free?
@@ -317,82 +314,76 @@ __global__ void __launch_bounds__(kGThreads, 1)
     // ---- results ----
     asm volatile("griddepcontrol.wait;" ::: "memory");         // the tensor scale, and y's last readers
     const int q = warp & 3;
-    float scale = 1.0f;
     if (NV) scale = __fmul_rn(a.x_scale ? *(volatile const float*)a.x_scale : 1.0f,
                               a.w_scale ? *(volatile const float*)a.w_scale : 1.0f);
     int piece = 0;
-    GWalk w(P, deal);
+    GWalk w(P);
     for (int left = n; left > 0; ++piece) {
-      const int t = w.tile, mt = w.mt, nt = w.nt, ks0 = w.ks;
-      const int len = gmin(left, nk - ks0);
-      const bool whole = ks0 == 0 && len == nk;
-      const int col = mt * kGM + q * 32 + lane;
-      const int tok0 = nt * NT, ntok = gmin(NT, a.T - tok0);
-      // after a give-up the pieces are not read, but their hand-overs still
-      // take place, so that the tickets return to zero
+      const int len = gmin(left, nk - w.ks);
+      const int col = w.mt * kGM + q * 32 + lane;
+      const int tok0 = w.nt * NT, ntok = gmin(NT, a.T - tok0);
       const bool ok = g_wait(&s_tfull[piece % S::kNacc], (uint32_t)(piece / S::kNacc) & 1u, &s_abort, a.status, 63);
       g_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((piece % S::kNacc) * S::kAcc);
-      // a piece that starts inside its tile is its CTA's first: slot 0; one that
-      // ends inside is its last: slot 1
-      float* part = a.parts + (((size_t)blockIdx.x * 2 + (ks0 ? 0 : 1)) * NT) * kGM + q * 32 + lane;
+      // a shared tile's partial sums: [token][output] in the ring, which every
+      // MMA has read by now
+      const uint32_t part = base + (uint32_t)((q * 32 + lane) * 4);
 #pragma unroll 1
       for (int c = 0; c < ntok && ok; c += 8) {
         uint32_t v[8];
         g_ld8(acc + (uint32_t)c, v);
         g_ld_wait();
-        if (whole) {
+        if (C == 1) {
           if (col < a.d_out) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              if (c + e < ntok) {
-                const size_t o = (size_t)(tok0 + c + e) * a.d_out + col;
-                const float f = NV ? __fmul_rn(__uint_as_float(v[e]), scale) : __uint_as_float(v[e]);
-                if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(f);
-                else reinterpret_cast<float*>(a.y)[o] = f;
-              }
+              if (c + e < ntok) g_store(a, (size_t)(tok0 + c + e) * a.d_out + col, __uint_as_float(v[e]), NV, scale);
             }
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (c + e < ntok) __stcg(part + (size_t)(c + e) * kGM, __uint_as_float(v[e]));
+            if (c + e < ntok)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(part + (uint32_t)((c + e) * kGM * 4)), "r"(v[e]) : "memory");
         }
       }
       g_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_tempty[piece % S::kNacc]);
-      if (!whole) {
-        // shared tile: the last of its CTAs adds the parts, in step order
-        const int c0 = deal.owner((long long)t * nk), c1 = deal.owner((long long)(t + 1) * nk - 1);
-        __threadfence();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (threadIdx.x == 64) {
-          const int before = atomicAdd(&a.tickets[t], 1);
-          s_last = before == c1 - c0;
-          if (before == c1 - c0) a.tickets[t] = 0;
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (s_last) {
-          __threadfence();
-          if (col < a.d_out) {
-            const float* p0 = a.parts + q * 32 + lane;
-#pragma unroll 4
-            for (int c = 0; c < ntok; ++c) {
-              float sum = __ldcg(p0 + (((size_t)c0 * 2 + 1) * NT + c) * kGM);
-              for (int k = c0 + 1; k <= c1; ++k) sum += __ldcg(p0 + (((size_t)k * 2) * NT + c) * kGM);
-              const float f = NV ? __fmul_rn(sum, scale) : sum;
-              const size_t o = (size_t)(tok0 + c) * a.d_out + col;
-              if (a.y_bf16) reinterpret_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(f);
-              else reinterpret_cast<float*>(a.y)[o] = f;
-            }
-          }
-        }
-      }
       left -= len;
       w.ks = nk - 1;
       w.next();
     }
+  }
+  if (C > 1) {
+    // every thread of the cluster reaches both barriers
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp >= 2) {
+      const GWalk w(P);
+      const int tok0 = w.nt * NT, ntok = gmin(NT, a.T - tok0);
+      const int items = ntok * (kGM / 4);
+      for (int i = rank * 128 + (int)threadIdx.x - 64; i < items; i += C * 128) {
+        const int t = i / (kGM / 4), c = (i % (kGM / 4)) * 4, col = w.mt * kGM + c;
+        if (col >= a.d_out) continue;               // d_out is a multiple of 8
+        const uint32_t local = base + (uint32_t)((t * kGM + c) * 4);
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < C; ++r) {
+          uint32_t remote;
+          float v[4];
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(r));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                       : "r"(remote)
+                       : "memory");
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] += v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g_store(a, (size_t)(tok0 + t) * a.d_out + col + e, sum[e], NV, scale);
+      }
+    }
+    // no CTA leaves while another may still read its shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   g_before();
   __syncthreads();
@@ -433,10 +424,56 @@ cudaError_t g_launch(const CUtensorMap& mw, const CUtensorMap& mx, const Fp4Gemm
   static unsigned configured = 0;
   cudaError_t e = ensure_smem_attr(fp4_gemm_kernel<NV, NT>, GShape<NV, NT>::kSmem, &configured);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fp4_gemm_kernel<NV, NT>, dim3((unsigned)a.plan.grid), dim3(kGThreads), (size_t)GShape<NV, NT>::kSmem, s,
-                 mw, mx, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.plan.grid);
+  cfg.blockDim = dim3(kGThreads);
+  cfg.dynamicSmemBytes = (size_t)GShape<NV, NT>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.plan.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<NV, NT>, mw, mx, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+// Clusters of c CTAs that are resident at once (one CTA per SM; every instance
+// takes most of an SM's shared memory, so one of them answers for all).
+int g_max_clusters(int c) {
+  static std::once_flag once;
+  static int n[9] = {0};
+  std::call_once(once, [] {
+    auto k = fp4_gemm_kernel<true, 128>;
+    constexpr int smem = GShape<true, 128>::kSmem;
+    static_assert(smem > 114 * 1024, "one CTA per SM");
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return;
+    }
+    for (int i = 1; i <= 8; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(i * kNumSMs));
+      cfg.blockDim = dim3(kGThreads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)i;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int m = 0;
+      if (cudaOccupancyMaxActiveClusters(&m, k, &cfg) == cudaSuccess) n[i] = m;
+      (void)cudaGetLastError();
+    }
+  });
+  return n[c];
 }
 
 template <bool NV>
@@ -464,23 +501,18 @@ Fp4GemmPlan plan_fp4_gemm(int T, int d_in, int d_out) {
   // that holds the tokens (at most 128)
   if (T > 128 && (long)p.mtiles * ((T + 255) / 256) >= kNumSMs) {
     p.nt = 256;
-    p.ntiles = (T + 255) / 256;
-    p.split = 0;
-    p.grid = kNumSMs;
-    return p;
+  } else {
+    p.nt = 8;
+    while (p.nt < T && p.nt < 128) p.nt *= 2;
   }
-  p.nt = 8;
-  while (p.nt < T && p.nt < 128) p.nt *= 2;
   p.ntiles = (T + p.nt - 1) / p.nt;
-  p.split = 1;
-  // at least 2 steps per CTA: a shared tile's partial sums and hand-over cost
-  // more than a step
-  const long total = (long)p.mtiles * p.ntiles * p.nk;
-  long g = total / 2;
-  if (g < 1) g = 1;
-  p.grid = (int)(g < kNumSMs ? g : kNumSMs);
-  p.parts_elems = (size_t)p.grid * 2 * p.nt * kGM;
-  p.tickets = p.mtiles * p.ntiles;
+  const long tiles = (long)p.mtiles * p.ntiles;
+  // the largest cluster of which every tile has one at once, with at least 2
+  // steps per CTA (a step is less than the hand-over costs)
+  p.cluster = 1;
+  for (int c = 2; c <= 8 && 2 * c <= p.nk; ++c)
+    if (tiles <= g_max_clusters(c)) p.cluster = c;
+  p.grid = p.cluster > 1 ? (int)tiles * p.cluster : (int)(tiles < kNumSMs ? tiles : kNumSMs);
   return p;
 }
 

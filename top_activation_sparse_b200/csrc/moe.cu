@@ -31,7 +31,7 @@
 // the operands go from global memory to registers without shared memory (the
 // sum over k may be permuted freely as long as both operands agree; a lane's
 // 16 bytes are its k values).  x and bf16 weights enter exactly; h enters as
-// the sum of two bf16 numbers (relative error 2^-17).  4-bit weights are
+// the sum of three bf16 numbers (relative error below 2^-24).  4-bit weights are
 // expanded in registers to bf16, exactly.
 #include "moe.cuh"
 
@@ -55,8 +55,7 @@ struct Smem {
       uint8_t flag[kRowsA];
     } a;
     struct {
-      __nv_bfloat16 hi[8 * kMaxNg * kHPitch];
-      __nv_bfloat16 lo[8 * kMaxNg * kHPitch];
+      __nv_bfloat16 h[3][8 * kMaxNg * kHPitch];
       uint16_t list[kListD];
     } d;
     struct {
@@ -527,7 +526,7 @@ __device__ void hidden_item(const MoeArgs& a, Smem& sm, int item, int lane, int 
 
 // ---- down projection ---------------------------------------------------------
 // a strip of 64 (bf16) or 128 (4-bit) columns per warp; the CTA's flagged
-// neurons of [j0, j1) are listed once and their h staged as two bf16 parts
+// neurons of [j0, j1) are listed once and their h staged as three bf16 parts
 template <bool FP4, int NG>
 __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, int nt, int j0, int j1, int strip,
                           int split, int lane, int warp) {
@@ -575,16 +574,19 @@ __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, 
     }
     for (int l0 = 0; l0 < total; l0 += kRowsD) {
       const int n = min(kRowsD, total - l0), np = (n + 15) & ~15;
-      // h of these neurons, hi + lo
+      // h of these neurons as three bf16 numbers
       for (int i = tid; i < np * 8 * NG; i += kMThreads) {
         const int r = i % np, c = i / np;
         float h = 0.0f;
         if (r < n && c < nt) h = __ldcg(a.h + (size_t)(slot0 + c) * a.d_ff + jl + sm.d.list[l0 + r]);
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        float rest = h - __bfloat162float(hi);
-        if (!(fabsf(h) < 3.0e38f)) rest = 0.0f;      // an infinity or NaN has no rest
-        sm.d.hi[c * kHPitch + r] = hi;
-        sm.d.lo[c * kHPitch + r] = __float2bfloat16_rn(rest);
+        // (an infinity or a NaN has no rest)
+        const bool finite = fabsf(h) <= 3.0e38f;
+#pragma unroll
+        for (int v = 0; v < 3; ++v) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(h);
+          sm.d.h[v][c * kHPitch + r] = b;
+          h = finite ? h - __bfloat162float(b) : 0.0f;
+        }
       }
       __syncthreads();
       if (works) {
@@ -604,17 +606,17 @@ __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, 
           }
         };
         auto step = [&](int st, const Vec (&v)[4], const uint32_t (&s)[4]) {
-          uint2 bh[NG], bl[NG];
+          uint2 b[NG][3];
 #pragma unroll
-          for (int t = 0; t < NG; ++t) {
-            bh[t] = *reinterpret_cast<const uint2*>(sm.d.hi + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
-            bl[t] = *reinterpret_cast<const uint2*>(sm.d.lo + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
-          }
+          for (int t = 0; t < NG; ++t)
+#pragma unroll
+            for (int v = 0; v < 3; ++v)
+              b[t][v] = *reinterpret_cast<const uint2*>(sm.d.h[v] + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
           auto mmas = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int t = 0; t < NG; ++t) {
-              mma_bf16(acc[m][t], a0, a1, a2, a3, bh[t].x, bh[t].y);
-              mma_bf16(acc[m][t], a0, a1, a2, a3, bl[t].x, bl[t].y);
+#pragma unroll
+              for (int v = 0; v < 3; ++v) mma_bf16(acc[m][t], a0, a1, a2, a3, b[t][v].x, b[t][v].y);
             }
           };
           if constexpr (!FP4) {
