@@ -112,6 +112,7 @@ typedef enum qs_fp4_scale_layout {
 /* Limits of qs_moe_ffn. */
 #define QS_MOE_MAX_EXPERTS 256
 #define QS_MOE_MAX_TOP_K 16
+#define QS_MOE_MAX_MODEL 8192
 /* Number of cudaEvent_t handles qs_sparse_ffn records when given phase events. */
 #define QS_FFN_PHASE_EVENTS 5
 /* ... and qs_sparse_linear / qs_quant_sparse_linear (before the top-K, after
@@ -490,7 +491,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   ReLU: up) is 0 for every token of its expert is not computed further, and
  *   a down row is read only where some token's h is not 0: exact skipping, as
  *   in qs_sparse_ffn_gate_first.  Weights of experts that no token uses are
- *   not read.  Each expert weight is read once per 32 of its tokens.
+ *   not read.  Each expert weight is read once per 16 of its tokens
+ *   (8 where d_model > 4096).
  *
  *   x         [T, d_model] bf16.
  *   w_router  [n_experts, d_model] bf16.
@@ -512,8 +514,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   closed neuron's other weights are not).
  *   d_model must be a multiple of 32, d_ff of 8.
  *   Errors: INVALID_ARG (also: some but not all scales given, top_k >
- *   n_experts), ALIGNMENT, WORKSPACE, UNSUPPORTED (d_model or d_ff above
- *   QS_MAX_ROW, n_experts above QS_MOE_MAX_EXPERTS, top_k above
+ *   n_experts), ALIGNMENT, WORKSPACE, UNSUPPORTED (d_model above
+ *   QS_MOE_MAX_MODEL, d_ff above QS_MAX_ROW, n_experts above QS_MOE_MAX_EXPERTS, top_k above
  *   QS_MOE_MAX_TOP_K), CUDA.
  */
 qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts, int top_k, int act,

@@ -62,6 +62,7 @@ QS_PREFILL_MIN_T = 64
 QS_FFN_PHASE_EVENTS = 5
 QS_MOE_MAX_EXPERTS = 256
 QS_MOE_MAX_TOP_K = 16
+QS_MOE_MAX_MODEL = 8192
 QS_LINEAR_PHASE_EVENTS = 3
 
 _FP4_FORMATS = {"mx": QS_FP4_MX, "nv": QS_FP4_NV}

@@ -199,7 +199,7 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
     }
     case QS_OP_MOE_FFN: {
       // (k: experts per token; the number of experts does not enter)
-      if (T < 1 || d_in < 32 || d_out < 8 || d_in > QS_MAX_ROW || d_out > QS_MAX_ROW || k < 1 ||
+      if (T < 1 || d_in < 32 || d_out < 8 || d_in > kMoeMaxModel || d_out > QS_MAX_ROW || k < 1 ||
           k > kMoeMaxK || (d_in % 32) != 0 || (d_out % 8) != 0)
         return false;
       const size_t slots = (size_t)Tc * k;
@@ -207,6 +207,7 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       L->moe_table = take(kMtSize * sizeof(int32_t));
       L->moe_share = take(slots * sizeof(float));
       L->h = take(slots * d_out * sizeof(float));
+      L->moe_xup = take((size_t)Tc * sizeof(float));
       L->moe_nz = take((slots < kMoeMaxE ? slots : kMoeMaxE) * d_out);
       // (a shorter last chunk may split more; its rows are at most as many)
       L->parts1_elems = (size_t)kMoePartRows * d_in;
@@ -944,7 +945,7 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
       top_k < 1 || top_k > n_experts || (act != QS_ACT_RELU2_GLU && act != QS_ACT_DRELU) ||
       (s_up != nullptr) != fp4 || (s_down != nullptr) != fp4)
     return QS_ERR_INVALID_ARG;
-  if (d_model > QS_MAX_ROW || d_ff > QS_MAX_ROW || n_experts > kMoeMaxE || top_k > kMoeMaxK)
+  if (d_model > kMoeMaxModel || d_ff > QS_MAX_ROW || n_experts > kMoeMaxE || top_k > kMoeMaxK)
     return QS_ERR_UNSUPPORTED;
   if ((d_model % 32) != 0 || (d_ff % 8) != 0) return QS_ERR_ALIGNMENT;
   for (const void* p : {x, w_router, w_gate, w_up, w_down, (const void*)s_gate, (const void*)s_up,
@@ -973,6 +974,7 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
   a.logits = w.at<float>(L.moe_logits);
   a.table = w.at<int32_t>(L.moe_table);
   a.share = w.at<float>(L.moe_share);
+  a.xup = w.at<float>(L.moe_xup);
   a.h = w.at<float>(L.h);
   a.nz = w.at<uint8_t>(L.moe_nz);
   a.parts = w.at<float>(L.parts1);

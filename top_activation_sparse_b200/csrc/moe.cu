@@ -26,46 +26,79 @@
 // drains whatever part of the grid is resident (two calls at once share the
 // SMs), and no result depends on which CTA does what.  Waits are bounded.
 //
-// Products run on mma.sync m16n8k16 (16 neurons x 8 tokens, or 16 columns x 8
-// tokens): with weights read once, up to 64 tokens stay bound by bytes, and
-// the operands go from global memory to registers without shared memory (the
-// sum over k may be permuted freely as long as both operands agree; a lane's
-// 16 bytes are its k values).  x and bf16 weights enter exactly; h enters as
-// the sum of three bf16 numbers (relative error below 2^-24).  4-bit weights are
-// expanded in registers to bf16, exactly.
+// The hidden layer's rows come through a ring in shared memory, filled by one
+// warp with a bulk copy per row (a row is contiguous: 8 KB of bf16 at d_model =
+// 4096).  Loading them from the warps straight to registers, 64 or 128 bytes of
+// each of 16 rows at a time, reached 1.4 to 3.3 TB/s: DRAM wants its pages read
+// in one go.  The order of the rows hides the dependence on what is open: first
+// factors of batch b + 1, then second factors of batch b, and, with one token,
+// the down rows of batch b - 1.
+//
+// Products run on mma.sync m16n8k16 (16 tokens x 8 neurons; 16 columns x 8
+// tokens in the down projection): with weights read once, a few tokens stay
+// bound by bytes.  x stays in registers: each of 16 warps holds its part of
+// d_model for all tokens of the pass.  The sum over k may be permuted freely as
+// long as both operands agree; a lane's 16 bytes are its k values.  x and bf16
+// weights enter exactly; h enters as the sum of three bf16 numbers (relative
+// error below 2^-24).  4-bit weights are expanded in registers, exactly.
+#include "fp4.cuh"
 #include "moe.cuh"
 
 namespace qs {
 namespace {
 
-constexpr int kMThreads = 256;
-constexpr int kMWarps = kMThreads / 32;
-constexpr int kMaxNg = 4;              // groups of 8 tokens per pass
-constexpr int kRowsA = 128;            // neurons per round of the hidden layer
+constexpr int kMWarps = 16;            // warps that compute
+constexpr int kMThreads = kMWarps * 32;
+constexpr int kThreads = kMThreads + 32;   // and one that copies
+constexpr int kMaxNg = 2;              // groups of 8 tokens per pass
+constexpr int kBatch = 64;             // neurons per batch (32 with two groups of tokens)
 constexpr int kListD = 2048;           // neurons per round of the down projection
 constexpr int kRowsD = 128;            // flagged neurons whose h is staged at a time
 constexpr int kHPitch = kRowsD + 16;   // bf16 entries per token (pitch = 32 bytes mod 128)
+constexpr int kRing = 165 * 1024;      // ring of rows
+constexpr int kMaxStages = 8;
 
 struct Smem {
+  unsigned char ring[kRing];
   union {
-    struct {
-      float red[kMWarps * 32 * 8 * kMaxNg];      // 32 KB: the warps' partial sums of a 32-neuron tile
-      float first[kRowsA * 8 * kMaxNg];          // 16 KB: first factors
-      int rows[kRowsA];                          // neurons of the current pass (-1: none)
-      uint8_t flag[kRowsA];
-    } a;
+    float red[kMWarps * kBatch * 8];             // 32 KB: the warps' sums
     struct {
       __nv_bfloat16 h[3][8 * kMaxNg * kHPitch];
       uint16_t list[kListD];
     } d;
-    struct {
-      int sel[kMoeMaxSlots];
-    } r;
+    int sel[kMoeMaxSlots];
   };
+  float first[2][kBatch * 8];                    // first factors of two batches
+  int rows[2][kBatch];                           // their open neurons
+  int nrows[2];
+  int drows[2][kBatch];                          // one token: neurons with h != 0, and p h
+  float dval[2][kBatch];
+  int ndrows[2];
+  float hval[kBatch];
+  uint32_t mask[kMWarps];
+  // this call's routing
+  int16_t expert[kMoeMaxE], firsts[kMoeMaxE], count[kMoeMaxE];
+  int16_t token[kMoeMaxSlots], slot[kMoeMaxSlots];
+  float share[kMoeMaxSlots];
+  float xup[kMoeMaxT];                           // 4-bit weights: the power of two x is multiplied with
+  int active;
   int tok[8 * kMaxNg];                           // the pass's tokens (-1: none)
   int scan[kMWarps];
-  int item, count, last;
+  int item, last, abort;
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t open[2], down[2];                     // lists of rows ready for the copying warp
 };
+static_assert(sizeof(Smem) <= 227 * 1024 - 1024, "shared memory");
+
+// (by name, not by reference: functions of their own would reach a reference
+// through generic addresses)
+__device__ __forceinline__ Smem& smem() {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  return *reinterpret_cast<Smem*>(smem_raw);
+}
+
+// the computing warps' barrier
+__device__ __forceinline__ void csync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 ld_w(const uint8_t* p) {
   uint4 r;
@@ -131,7 +164,7 @@ __device__ __forceinline__ int ld_acquire(const int32_t* p) {
   return v;
 }
 
-// thread 0 waits until *p >= n; everyone leaves together
+// thread 0 waits until *p >= n; the computing warps leave together
 __device__ __forceinline__ bool wait_for(const int32_t* p, int n, DevStatus* st, uint32_t where, Smem& sm) {
   if (threadIdx.x == 0) {
     uint32_t i = 0;
@@ -146,53 +179,87 @@ __device__ __forceinline__ bool wait_for(const int32_t* p, int n, DevStatus* st,
     __threadfence();
     sm.last = ok;
   }
-  __syncthreads();
+  csync();
   return sm.last != 0;
 }
 
-// the CTA's writes are visible before the count goes up; the count before, to all
+// the computing warps' writes are visible before the count goes up; the count
+// before, to all of them
 __device__ __forceinline__ int finish(int32_t* p, Smem& sm) {
   __threadfence();
-  __syncthreads();
+  csync();
   if (threadIdx.x == 0) sm.last = atomicAdd(p, 1);
-  __syncthreads();
+  csync();
   return sm.last;
 }
 
+// bounded wait on a barrier of this CTA; after one that gave up, none waits
+__device__ __forceinline__ bool ring_wait(uint64_t* b, uint32_t parity, Smem& sm, DevStatus* st, uint32_t where) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(b, parity)) return true;
+    if ((i & 15u) == 15u && *(volatile int*)&sm.abort) return false;
+  }
+  dev_fail(st, DEV_TIMEOUT, where, 0u);
+  atomicExch(&sm.abort, 1);
+  return false;
+}
+
 // ---- router ------------------------------------------------------------------
-// item: 8 experts (one per warp) x 8 tokens
-__device__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
-  const int ngr = (a.T + 7) / 8;
-  const int e = (item / ngr) * kMWarps + warp, t0 = (item % ngr) * 8;
-  if (e >= a.E) return;
-  const int nt = min(8, a.T - t0);
+// item: 16 tasks, one per warp, of one expert and router_tokens tokens
+__device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
+  const int nt = a.plan.router_tokens, groups = (a.T + nt - 1) / nt;
+  const int task = item * kMWarps + warp;
+  if (task >= a.E * groups) return;
+  const int e = task / groups, t0 = (task % groups) * nt;
   const __nv_bfloat16* w = a.router + (size_t)e * a.d_model;
-  float s[8];
+  const __nv_bfloat16* px[4];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) s[t] = 0.0f;
+  for (int t = 0; t < 4; ++t) px[t] = a.x + (size_t)min(t0 + min(t, nt - 1), a.T - 1) * a.d_model;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](const uint4& wv, const uint4& xv, float& v) {
+    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w}, xx[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v = fmaf(bf16lo(ww[i]), bf16lo(xx[i]), v);
+      v = fmaf(bf16hi(ww[i]), bf16hi(xx[i]), v);
+    }
+  };
+  if (nt == 1) {
+#pragma unroll 8
+    for (int k = lane * 8; k < a.d_model; k += 256) add(ld_x(w + k), ld_x(px[0] + k), s[0]);
+  } else {
 #pragma unroll 4
-  for (int k = lane * 8; k < a.d_model; k += 256) {
-    const uint4 wv = ld_x(w + k);
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    for (int k = lane * 8; k < a.d_model; k += 256) {
+      const uint4 wv = ld_x(w + k);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if (t < nt) {
-        const uint4 xv = ld_x(a.x + (size_t)(t0 + t) * a.d_model + k);
-        const uint32_t xx[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[t] = fmaf(bf16lo(ww[i]), bf16lo(xx[i]), s[t]);
-          s[t] = fmaf(bf16hi(ww[i]), bf16hi(xx[i]), s[t]);
-        }
-      }
+      for (int t = 0; t < 4; ++t) add(wv, ld_x(px[t] + k), s[t]);
     }
   }
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
+  for (int t = 0; t < 4; ++t) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
-    if (lane == 0 && t < nt) __stcg(a.logits + (size_t)(t0 + t) * a.E + e, s[t]);
+    if (lane == 0 && t < nt && t0 + t < a.T) __stcg(a.logits + (size_t)(t0 + t) * a.E + e, s[t]);
   }
+}
+
+// The power of two that brings a token's largest |x| into [2^7, 2^8).
+__device__ __forceinline__ float x_power(const __nv_bfloat16* x, int d, int lane) {
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int k = lane * 8; k < d; k += 256) {
+    const uint4 v = ld_x(x + k);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+  }
+#pragma unroll
+  for (int i = 16; i; i >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, i));
+  const int e = (int)(m >> 7);                      // biased exponent of the largest
+  // (nothing but subnormal numbers, or a non-finite one: no useful power);
+  // at most 2^126, so that its reciprocal is a normal number
+  const int up = e == 0 || e == 255 ? 0 : min(126, 127 + 7 - e);
+  return __uint_as_float((uint32_t)(up + 127) << 23);
 }
 
 // larger float, larger key (NaN above all)
@@ -202,8 +269,12 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// experts and shares of every token, then the experts' token lists
-__device__ void select_experts(const MoeArgs& a, Smem& sm, int lane, int warp) {
+// Experts and shares of every token from logits [T, E], then the experts' token
+// lists, into sm.  (logits may be the union's memory: they are read before a
+// barrier, the choices are written to it after.)
+template <bool SHARED>
+__device__ __noinline__ void select_experts(const MoeArgs& a, const float* logits, bool publish, int lane, int warp) {
+  Smem& sm = smem();
   const int K = a.top_k;
   for (int t = warp; t < a.T; t += kMWarps) {
     float v[kMoeMaxE / 32];
@@ -211,7 +282,7 @@ __device__ void select_experts(const MoeArgs& a, Smem& sm, int lane, int warp) {
 #pragma unroll
     for (int i = 0; i < kMoeMaxE / 32; ++i) {
       const int e = lane + 32 * i;
-      v[i] = e < a.E ? __ldcg(a.logits + (size_t)t * a.E + e) : 0.0f;
+      v[i] = e < a.E ? (SHARED ? logits[t * a.E + e] : __ldcg(logits + (size_t)t * a.E + e)) : 0.0f;
     }
     float best = 0.0f, sum = 0.0f, mine = 0.0f;
     int choice = 0;                           // lane j: choice j
@@ -244,28 +315,33 @@ __device__ void select_experts(const MoeArgs& a, Smem& sm, int lane, int warp) {
     }
     if (lane < K) {
       const float p = mine / sum;
-      sm.r.sel[t * K + lane] = choice;
-      __stcg(a.share + t * K + lane, p);
-      if (a.experts) a.experts[t * K + lane] = choice;
-      if (a.weights) a.weights[t * K + lane] = p;
+      sm.slot[t * K + lane] = (int16_t)choice;     // the expert, for now
+      sm.share[t * K + lane] = p;
+      if (publish) {
+        if (a.experts) a.experts[t * K + lane] = choice;
+        if (a.weights) a.weights[t * K + lane] = p;
+      }
     }
   }
-  __syncthreads();
-  // thread e: its tokens in order; experts without tokens drop out
+  csync();
   const int n = a.T * K, e = threadIdx.x;
+  for (int i = threadIdx.x; i < n; i += kMThreads) sm.sel[i] = sm.slot[i];
+  csync();
+  // thread e: its tokens in order; experts without tokens drop out
   int cnt = 0;
   if (e < a.E)
-    for (int i = 0; i < n; ++i) cnt += sm.r.sel[i] == e;
+    for (int i = 0; i < n; ++i) cnt += sm.sel[i] == e;
   const int act = cnt > 0;
-  // exclusive sums over the experts: (active experts, slots), both below 2^16
-  int v = (act << 16) | cnt, inc = v;
+  // sums over the experts: (active experts, slots), both below 2^16
+  const int v = (act << 16) | cnt;
+  int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
   if (lane == 31) sm.scan[warp] = inc;
-  __syncthreads();
+  csync();
   int before = 0, total = 0;
   for (int w = 0; w < kMWarps; ++w) {
     if (w < warp) before += sm.scan[w];
@@ -274,294 +350,685 @@ __device__ void select_experts(const MoeArgs& a, Smem& sm, int lane, int warp) {
   const int ex = before + inc - v;
   if (act) {
     const int ai = ex >> 16, first = ex & 0xffff;
-    __stcg(a.table + kMtExpert + ai, e);
-    __stcg(a.table + kMtFirst + ai, first);
-    __stcg(a.table + kMtCount + ai, cnt);
+    sm.expert[ai] = e;
+    sm.firsts[ai] = first;
+    sm.count[ai] = cnt;
     int at = first;
     for (int i = 0; i < n; ++i)
-      if (sm.r.sel[i] == e) {
-        __stcg(a.table + kMtToken + at, i / K);
-        __stcg(a.table + kMtSlot + i, at);
+      if (sm.sel[i] == e) {
+        sm.token[at] = (int16_t)(i / K);
+        sm.slot[i] = (int16_t)at;
         ++at;
       }
   }
-  if (threadIdx.x == 0) __stcg(a.table, total >> 16);
+  if (threadIdx.x == 0) sm.active = total >> 16;
+  csync();
+}
+
+// the routing from sm to the workspace, and back in every other CTA
+__device__ void publish_routing(const MoeArgs& a, Smem& sm) {
+  const int n = a.T * a.top_k, tid = threadIdx.x;
+  for (int i = tid; i < sm.active; i += kMThreads) {
+    __stcg(a.table + kMtExpert + i, (int)sm.expert[i]);
+    __stcg(a.table + kMtFirst + i, (int)sm.firsts[i]);
+    __stcg(a.table + kMtCount + i, (int)sm.count[i]);
+  }
+  for (int i = tid; i < n; i += kMThreads) {
+    __stcg(a.table + kMtToken + i, (int)sm.token[i]);
+    __stcg(a.table + kMtSlot + i, (int)sm.slot[i]);
+    __stcg(a.share + i, sm.share[i]);
+  }
+  if (tid == 0) __stcg(a.table, sm.active);
+}
+__device__ void fetch_routing(const MoeArgs& a, Smem& sm) {
+  const int n = a.T * a.top_k, tid = threadIdx.x, A = __ldcg(a.table);
+  for (int i = tid; i < A; i += kMThreads) {
+    sm.expert[i] = (int16_t)__ldcg(a.table + kMtExpert + i);
+    sm.firsts[i] = (int16_t)__ldcg(a.table + kMtFirst + i);
+    sm.count[i] = (int16_t)__ldcg(a.table + kMtCount + i);
+  }
+  for (int i = tid; i < n; i += kMThreads) {
+    sm.token[i] = (int16_t)__ldcg(a.table + kMtToken + i);
+    sm.slot[i] = (int16_t)__ldcg(a.table + kMtSlot + i);
+    sm.share[i] = __ldcg(a.share + i);
+  }
+  if (a.fp4)
+    for (int i = tid; i < a.T; i += kMThreads) sm.xup[i] = __ldcg(a.xup + i);
+  if (tid == 0) sm.active = A;
+  csync();
+}
+
+// Local routing: few tokens and a small router (at most 128 KB, from L2), which
+// every CTA evaluates for itself: less time than handing the result over.  A
+// warp's task is four (expert, token) pairs, whose loads overlap, over a slice
+// of d_model where there are few pairs.
+__device__ __noinline__ void route_here(const MoeArgs& a, bool publish, int lane, int warp) {
+  Smem& sm = smem();
+  const int pairs = a.E * a.T, quads = (pairs + 3) / 4;
+  const int slices = quads >= kMWarps ? 1 : min(8, kMWarps / quads);
+  float* part = sm.red;                             // [slices][pairs], at most 2048
+  for (int task = warp; task < quads * slices; task += kMWarps) {
+    const int i0 = (task % quads) * 4, slice = task / quads;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const __nv_bfloat16 *pw[4], *px[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = min(i0 + i, pairs - 1);
+      pw[i] = a.router + (size_t)(at % a.E) * a.d_model;
+      px[i] = a.x + (size_t)(at / a.E) * a.d_model;
+    }
+#pragma unroll 2
+    for (int k = slice * 256 + lane * 8; k < a.d_model; k += 256 * slices) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = ld_x(pw[i] + k), x = ld_x(px[i] + k);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, xx[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          v[i] = fmaf(bf16lo(ww[c]), bf16lo(xx[c]), v[i]);
+          v[i] = fmaf(bf16hi(ww[c]), bf16hi(xx[c]), v[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      if (lane == 0 && i0 + i < pairs) part[slice * pairs + i0 + i] = v[i];
+    }
+  }
+  if (a.fp4)
+    for (int t = warp; t < a.T; t += kMWarps) {
+      const float u = x_power(a.x + (size_t)t * a.d_model, a.d_model, lane);
+      if (lane == 0) sm.xup[t] = u;
+    }
+  csync();
+  // [T, E]; each place is read and written by one thread
+  for (int i = threadIdx.x; i < pairs && slices > 1; i += kMThreads)
+    for (int k = 1; k < slices; ++k) part[i] += part[k * pairs + i];
+  csync();
+  select_experts<true>(a, part, publish, lane, warp);
 }
 
 // ---- hidden layer ------------------------------------------------------------
-// 32 neurons (rows[0..31], -1: none) x 8 NG tokens: the eight warps take every
-// eighth piece of 128 bytes of the rows and leave their sums in red
-template <bool FP4, int NG>
-__device__ __forceinline__ void tile_dot(const uint8_t* w, const uint8_t* sc, const int* rows, const MoeArgs& a,
-                                         const int* tok, float* red, int lane, int warp) {
-  const int g = lane >> 2, q = lane & 3;
-  const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;     // bytes of a row
-  const int sb = a.d_model / 32;
-  constexpr int kLane = FP4 ? 32 : 8;                   // values of a lane's 16 bytes
-  const uint8_t* p[4];
-  const uint8_t* ps[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int j = rows[g + 8 * r];
-    p[r] = j < 0 ? nullptr : w + (size_t)j * rb;
-    ps[r] = (!FP4 || j < 0) ? nullptr : sc + (size_t)j * sb;
-  }
-  const __nv_bfloat16* px[NG];
-#pragma unroll
-  for (int n = 0; n < NG; ++n) px[n] = tok[n * 8 + g] < 0 ? nullptr : a.x + (size_t)tok[n * 8 + g] * a.d_model;
-  float acc[2][NG][4];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-  const int pieces = (a.d_model + 8 * kLane - 1) / (8 * kLane);     // of 128 bytes: two quads of lanes' 16
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-
-  auto load = [&](int pc, uint4 (&wv)[2][4], uint32_t (&s)[2][4]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = pc * 8 * kLane + (h * 4 + q) * kLane;
-      const bool in = pc < pieces && k < a.d_model;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        wv[h][r] = (in && p[r]) ? ld_w(p[r] + (FP4 ? k / 2 : k * 2)) : zero;
-        if (FP4) s[h][r] = (in && ps[r]) ? (uint32_t)__ldg(ps[r] + k / 32) : 0u;
-      }
-    }
-  };
-  uint4 wv[2][2][4];
-  uint32_t s[2][2][4];
-  load(warp, wv[0], s[0]);
-  for (int pc = warp, b = 0; pc < pieces; pc += 2 * kMWarps) {
-#pragma unroll
-    for (b = 0; b < 2; ++b) {
-      const int pb = pc + b * kMWarps;
-      if (pb >= pieces) break;
-      load(pb + kMWarps, wv[b ^ 1], s[b ^ 1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = pb * 8 * kLane + (h * 4 + q) * kLane;
-        const bool in = k < a.d_model;
-        if constexpr (!FP4) {
-          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&wv[b][h][0]);
-          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&wv[b][h][1]);
-          const uint32_t* w2 = reinterpret_cast<const uint32_t*>(&wv[b][h][2]);
-          const uint32_t* w3 = reinterpret_cast<const uint32_t*>(&wv[b][h][3]);
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            const uint4 xv = (in && px[n]) ? ld_x(px[n] + k) : zero;
-            const uint32_t* xw = reinterpret_cast<const uint32_t*>(&xv);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              mma_bf16(acc[0][n], w0[i], w1[i], w0[i + 1], w1[i + 1], xw[i], xw[i + 1]);
-              mma_bf16(acc[1][n], w2[i], w3[i], w2[i + 1], w3[i + 1], xw[i], xw[i + 1]);
-            }
-          }
-        } else {
-          uint32_t lo[4], hi[4];
-          bool big[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            lo[r] = scale_lo(s[b][h][r]) * 0x10001u;
-            hi[r] = scale_hi(s[b][h][r]) * 0x10001u;
-            big[r] = s[b][h][r] > 128u;
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {                // words of 8 codes
-            uint32_t f[4][4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t c = reinterpret_cast<const uint32_t*>(&wv[b][h][r])[i];
-              f[r][0] = weight_pair<0>(c, lo[r], hi[r], big[r]);     // codes 0, 4
-              f[r][1] = weight_pair<1>(c, lo[r], hi[r], big[r]);     // codes 1, 5
-              f[r][2] = weight_pair<2>(c, lo[r], hi[r], big[r]);
-              f[r][3] = weight_pair<3>(c, lo[r], hi[r], big[r]);
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-              const uint4 xv = (in && px[n]) ? ld_x(px[n] + k + 8 * i) : zero;
-              const uint32_t b0 = __byte_perm(xv.x, xv.z, 0x5410), b1 = __byte_perm(xv.x, xv.z, 0x7632);
-              const uint32_t b2 = __byte_perm(xv.y, xv.w, 0x5410), b3 = __byte_perm(xv.y, xv.w, 0x7632);
-              mma_bf16(acc[0][n], f[0][0], f[1][0], f[0][1], f[1][1], b0, b1);
-              mma_bf16(acc[1][n], f[2][0], f[3][0], f[2][1], f[3][1], b0, b1);
-              mma_bf16(acc[0][n], f[0][2], f[1][2], f[0][3], f[1][3], b2, b3);
-              mma_bf16(acc[1][n], f[2][2], f[3][2], f[2][3], f[3][3], b2, b3);
-            }
-          }
-        }
-      }
-    }
-  }
-  float* o = red + warp * 32 * 8 * NG;
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      *reinterpret_cast<float2*>(o + (m * 16 + g) * 8 * NG + n * 8 + 2 * q) = make_float2(acc[m][n][0], acc[m][n][1]);
-      *reinterpret_cast<float2*>(o + (m * 16 + g + 8) * 8 * NG + n * 8 + 2 * q) = make_float2(acc[m][n][2], acc[m][n][3]);
-    }
-}
-
 __device__ __forceinline__ float relu_nan(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
 
-// neurons [j0, j1) of active expert ai for its tokens t0 .. t0 + nt of the list
-template <bool FP4, int NG>
-__device__ void hidden_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, int nt, int j0, int j1, bool add,
-                            bool keep_zeros, int lane, int warp) {
-  const size_t mat = (size_t)a.d_ff * a.d_model;
-  const size_t wo = FP4 ? (size_t)e * (mat / 2) : (size_t)e * mat * 2, so = FP4 ? (size_t)e * (mat / 32) : 0;
-  const int tid = threadIdx.x;
-  const float* b1 = a.b1 ? a.b1 + (size_t)e * a.d_ff : nullptr;
-  const float* b2 = a.b2 ? a.b2 + (size_t)e * a.d_ff : nullptr;
-  for (int jb = j0; jb < j1; jb += kRowsA) {
-    const int nr = min(kRowsA, j1 - jb);
-    // first factor of every neuron
-    for (int i = tid; i < kRowsA; i += kMThreads) {
-      sm.a.rows[i] = i < nr ? jb + i : -1;
-      sm.a.flag[i] = 0;
+// How rows lie in the ring, from the plan; the same in both roles.
+struct Ring {
+  int rb, sb;          // bytes of a row, and of its scales where they travel with it (else 0)
+  int pitch;           // bytes between rows
+  int rps;             // rows per stage
+  int stages;
+};
+
+// The place in the ring, kept by each role across all its rows.
+struct RingAt {
+  int sl = 0, issued = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(const Ring& R) {
+    if (++sl == R.stages) sl = 0, ph ^= 1u;
+  }
+};
+
+// the copying warp: rows list[0..n), or j0 + i without a list, of matrix w
+__device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, DevStatus* st, const uint8_t* w, const uint8_t* sc,
+                                          const int* list, int j0, int n, int lane) {
+  for (int i0 = 0; i0 < n; i0 += R.rps) {
+    const int nr = min(R.rps, n - i0);
+    const bool ok = ring_wait(&sm.empty[at.sl], at.ph ^ 1u, sm, st, 74);
+    if (__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.sl], (uint32_t)(nr * (R.rb + R.sb)));
+      __syncwarp();
+      unsigned char* dst = sm.ring + (size_t)at.sl * R.rps * R.pitch;
+      for (int r = lane; r < nr; r += 32) {
+        const size_t j = (size_t)(list ? list[i0 + r] : j0 + i0 + r);
+        bulk_g2s(dst + r * R.pitch, w + j * R.rb, (uint32_t)R.rb, &sm.full[at.sl]);
+        if (R.sb) bulk_g2s(dst + r * R.pitch + R.rb, sc + j * R.sb, (uint32_t)R.sb, &sm.full[at.sl]);
+      }
+      ++at.issued;
     }
-    __syncthreads();
-    for (int r0 = 0; r0 < nr; r0 += 32) {
-      tile_dot<FP4, NG>(a.w1 + wo, FP4 ? a.s1 + so : nullptr, sm.a.rows + r0, a, sm.tok, sm.a.red, lane, warp);
-      __syncthreads();
-      for (int i = tid; i < 32 * 8 * NG; i += kMThreads) {
-        float v = 0.0f;
+    at.next(R);
+  }
+}
+
+// Up to KU units of 32 values of each row per warp, NG groups of 8 tokens; four
+// registers per unit and group.
+//   bf16 weights: a lane's 8 values of x (16 bytes), in order.
+//   4-bit weights: the products run on e4m3 x e4m3 -> float32 (m16n8k32), whose
+//   sums are correctly rounded float32.  A code's bits, moved to the low
+//   exponent and the high mantissa bit of e4m3, are its value times 2^-6
+//   (subnormals included): no conversion.  x, times the power of two that
+//   brings its token's largest into [2^7, 2^8), is the sum of two e4m3 numbers,
+//   the second times 2^-4: exact for bf16 down to 2^-14 of the largest, and
+//   within 2^-22 of it below that.  The two parts are two rows of the matrix.
+template <int KU, int NG>
+struct XFrag {
+  uint32_t v[KU][NG][4];
+};
+
+// KS warps share the rows' length, 16 / KS groups take the 8-row tiles of a
+// stage in turn.
+struct Split {
+  int units, ks, groups, part, group, per, n;      // units of this warp: part * per .. + n
+  __device__ Split(int d, int ku, int warp) {
+    units = d / 32;
+    ks = 1;
+    while (ks * ku < units) ks *= 2;
+    groups = kMWarps / ks;
+    part = warp % ks;
+    group = warp / ks;
+    per = (units + ks - 1) / ks;
+    n = max(0, min(per, units - part * per));
+  }
+};
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_back(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <bool FP4, int KU, int NG>
+__device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const Split& P, XFrag<KU, NG>& x, int lane) {
+  const int g = lane >> 2, q = lane & 3;
 #pragma unroll
-        for (int w = 0; w < kMWarps; ++w) v += sm.a.red[w * 32 * 8 * NG + i];
-        const int r = r0 + i / (8 * NG);
-        if (b1 && r < nr) v += b1[jb + r];
-        v = relu_nan(v);
-        if (!a.drelu) v *= v;
-        sm.a.first[r * 8 * NG + i % (8 * NG)] = v;
-        if (r < nr && i % (8 * NG) < nt && v != 0.0f) sm.a.flag[r] = 1;
-      }
-      __syncthreads();
-    }
-    // the open neurons, in order
-    if (warp == 0) {
-      int n = 0;
-      for (int i = lane; i < kRowsA; i += 32) {
-        const bool open = sm.a.flag[i] != 0;
-        const unsigned m = __ballot_sync(0xffffffffu, open);
-        if (open) sm.a.rows[n + __popc(m & lanemask_lt())] = jb + i;
-        n += __popc(m);
-      }
-      for (int i = n + lane; i < min(kRowsA, (n + 31) & ~31); i += 32) sm.a.rows[i] = -1;
-      if (lane == 0) sm.count = n;
-    }
-    // a closed neuron's h is 0 and is not read again: only its flag is written
-    // (unless another pass's tokens may open it)
-    for (int i = tid; i < nr; i += kMThreads)
-      if (!sm.a.flag[i]) {
-        if (!add) a.nz[(size_t)ai * a.d_ff + jb + i] = 0;
-        if (keep_zeros)
-          for (int c = 0; c < nt; ++c) __stcg(a.h + (size_t)(slot0 + c) * a.d_ff + jb + i, 0.0f);
-      }
-    __syncthreads();
-    const int n = sm.count;
-    for (int r0 = 0; r0 < n; r0 += 32) {
-      tile_dot<FP4, NG>(a.w2 + wo, FP4 ? a.s2 + so : nullptr, sm.a.rows + r0, a, sm.tok, sm.a.red, lane, warp);
-      __syncthreads();
-      // one neuron per 8 NG neighbouring threads
-      for (int i = tid; i < 32 * 8 * NG; i += kMThreads) {
-        const int r = r0 + i / (8 * NG), c = i % (8 * NG);
-        float h = 0.0f;
-        const int j = r < n ? sm.a.rows[r] : -1;
-        if (j >= 0 && c < nt) {
-          float v = 0.0f;
+  for (int n = 0; n < NG; ++n) {
+    const int t = sm.tok[n * 8 + g];
+    const __nv_bfloat16* px = a.x + (size_t)max(t, 0) * a.d_model + (size_t)P.part * P.per * 32 + q * 8;
+    const float up = FP4 && t >= 0 ? sm.xup[t] : 0.0f;
 #pragma unroll
-          for (int w = 0; w < kMWarps; ++w) v += sm.a.red[w * 32 * 8 * NG + i];
-          if (b2) v += b2[j];
-          if (a.drelu) v = relu_nan(v);
-          h = sm.a.first[(j - jb) * 8 * NG + c] * v;
-          __stcg(a.h + (size_t)(slot0 + c) * a.d_ff + j, h);
+    for (int i = 0; i < KU; ++i) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (t >= 0 && i < P.n) v = ld_x(px + i * 32);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      if constexpr (FP4) {
+        // values 0, 2, 4, 6 and 1, 3, 5, 7, as the codes come out of their words
+        uint32_t f[2][2] = {{0, 0}, {0, 0}};       // [part][even, odd]
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const float v0 = (o ? bf16hi(u[2 * j]) : bf16lo(u[2 * j])) * up;
+            const float v1 = (o ? bf16hi(u[2 * j + 1]) : bf16lo(u[2 * j + 1])) * up;
+            const uint32_t p = e4m3x2(v0, v1);
+            const float2 b = e4m3x2_back(p);
+            f[0][o] |= p << (16 * j);
+            f[1][o] |= e4m3x2((v0 - b.x) * 16.0f, (v1 - b.y) * 16.0f) << (16 * j);
+          }
         }
+        x.v[i][n][0] = f[0][0];
+        x.v[i][n][1] = f[1][0];
+        x.v[i][n][2] = f[0][1];
+        x.v[i][n][3] = f[1][1];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.v[i][n][j] = u[j];
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// n rows from the ring times the pass's tokens: sums of row r (of the batch) and
+// token t to red[part][r][t]
+template <bool FP4, int KU, int NG>
+__device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P,
+                                               const XFrag<KU, NG>& x, const uint8_t* sc, const int* list, int j0, int n,
+                                               int lane) {
+  const int g = lane >> 2, q = lane & 3;
+  float* red = sm.red + (size_t)P.part * kBatch * 8;     // kBatch x 8 = 32 x 16
+  // a lane's units lie apart by 64 or 16 bytes; the loads of those that the warp
+  // does not have repeat its first (x is 0 there)
+  const int first = P.n > 0 ? P.part * P.per : 0;
+  for (int i0 = 0; i0 < n; i0 += R.rps) {
+    const int nr = min(R.rps, n - i0);
+    ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
+    const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
+    for (int t0 = P.group * 8; t0 < nr; t0 += P.groups * 8) {
+      const unsigned char* row = stage + (t0 + g < nr ? t0 + g : t0) * R.pitch;
+      if constexpr (!FP4) {
+        // four sums in turn: one matrix instruction after the other into the
+        // same sum takes 20 to 32 cycles each
+        float acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+        constexpr int kAhead = NG == 1 && KU == 8 ? 8 : 4;      // loads before the first product
+#pragma unroll
+        for (int h = 0; h < KU; h += kAhead) {
+          uint4 w[kAhead];
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(row + (first + (h + i < P.n ? h + i : 0)) * 64 + q * 16);
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const uint32_t(&x0)[4] = x.v[h + i][0];
+            const uint32_t(&x1)[4] = x.v[h + i][NG - 1];
+            mma_bf16(acc[(2 * i) & 3], x0[0], NG > 1 ? x1[0] : 0u, x0[1], NG > 1 ? x1[1] : 0u, w[i].x, w[i].y);
+            mma_bf16(acc[(2 * i + 1) & 3], x0[2], NG > 1 ? x1[2] : 0u, x0[3], NG > 1 ? x1[3] : 0u, w[i].z, w[i].w);
+          }
+        }
+        // tokens g and g + 8, rows 2q and 2q + 1 of the tile
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rr = t0 + 2 * q + c;
+          if (rr < nr) {
+            red[(i0 + rr) * 8 * NG + g] = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
+            if constexpr (NG > 1)
+              red[(i0 + rr) * 8 * NG + 8 + g] = (acc[0][2 + c] + acc[1][2 + c]) + (acc[2][2 + c] + acc[3][2 + c]);
+          }
+        }
+      } else {
+        // a unit is one block: its sum times its scale.  Columns 2q and 2q + 1
+        // are the tile's rows 2q and 2q + 1.
+        const int c0 = min(t0 + 2 * q, nr - 1), c1 = min(t0 + 2 * q + 1, nr - 1);
+        uint32_t s[2][KU];
+        if (R.sb && KU == 8 && P.per == 8) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint2 v = *reinterpret_cast<const uint2*>(stage + (c ? c1 : c0) * R.pitch + R.rb + first);
+#pragma unroll
+            for (int i = 0; i < KU; ++i) s[c][i] = ((i < 4 ? v.x : v.y) >> (8 * (i & 3))) & 0xffu;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = c ? c1 : c0;
+            const uint8_t* p = R.sb ? stage + r * R.pitch + R.rb + first
+                                    : sc + (size_t)(list ? list[i0 + r] : j0 + i0 + r) * (a.d_model / 32) + first;
+#pragma unroll
+            for (int i = 0; i < KU; ++i) s[c][i] = R.sb ? p[i < P.n ? i : 0] : __ldg(p + (i < P.n ? i : 0));
+          }
+        }
+        uint32_t w[KU];
+#pragma unroll
+        for (int i = 0; i < KU; ++i) w[i] = *reinterpret_cast<const uint32_t*>(row + (first + (i < P.n ? i : 0)) * 16 + q * 4);
+        float acc[NG][4];
+#pragma unroll
+        for (int t = 0; t < NG; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < KU; ++i) {
+          const uint32_t even = ((w[i] * 4u) & 0x1c1c1c1cu) | ((w[i] * 16u) & 0x80808080u);
+          const uint32_t odd = ((w[i] >> 2) & 0x1c1c1c1cu) | (w[i] & 0x80808080u);
+          // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
+          // of its codes, all 0)
+          const float f0 = __uint_as_float(s[0][i] << 23), f1 = __uint_as_float(s[1][i] << 23);
+#pragma unroll
+          for (int t = 0; t < NG; ++t) {
+            float d[4];
+            mma_e4m3(d, x.v[i][t], even, odd);
+            acc[t][0] = fmaf(d[0], f0, acc[t][0]);
+            acc[t][1] = fmaf(d[1], f1, acc[t][1]);
+            acc[t][2] = fmaf(d[2], f0, acc[t][2]);
+            acc[t][3] = fmaf(d[3], f1, acc[t][3]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rr = t0 + 2 * q + c;
+          if (rr < nr)
+#pragma unroll
+            for (int t = 0; t < NG; ++t) red[(i0 + rr) * 8 * NG + t * 8 + g] = fmaf(acc[t][2 + c], 0.0625f, acc[t][c]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[at.sl]);
+    at.next(R);
+  }
+}
+
+// One token, d_model <= 4096: the CTA goes on to its neurons' down rows, 8
+// columns per thread.
+template <bool FP4>
+__device__ __forceinline__ void down_stage_rows(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const uint8_t* sc,
+                                                const int* list, const float* val, int n, float (&y)[8], int lane) {
+  const int tid = threadIdx.x;
+  const bool in = tid * 8 < a.d_model;
+  for (int i0 = 0; i0 < n; i0 += R.rps) {
+    const int nr = min(R.rps, n - i0);
+    ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 76);
+    const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
+    if (in) {
+      for (int r = 0; r < nr; ++r) {
+        const unsigned char* row = stage + r * R.pitch;
+        float h = val[i0 + r];
+        if constexpr (!FP4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + tid * 16);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[2 * c] = fmaf(h, bf16lo(u[c]), y[2 * c]);
+            y[2 * c + 1] = fmaf(h, bf16hi(u[c]), y[2 * c + 1]);
+          }
+        } else {
+          const uint32_t b = R.sb ? row[R.rb + tid / 4] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + tid / 4);
+          h *= e8m0_value(b);
+          uint32_t f[4];
+          e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + tid * 4), f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[c]));
+            y[2 * c] = fmaf(h, v.x, y[2 * c]);
+            y[2 * c + 1] = fmaf(h, v.y, y[2 * c + 1]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[at.sl]);
+    at.next(R);
+  }
+}
+
+// one token: the share of the choice whose slot this is
+__device__ __forceinline__ float choice_share(const MoeArgs& a, const Smem& sm, int slot) {
+  float p = 0.0f;
+  for (int j = 0; j < a.top_k; ++j)
+    if (sm.slot[j] == slot) p = sm.share[j];
+  return p;
+}
+
+// A run: neurons [j0, j1) of active expert ai for nt of its tokens, whose slots
+// start at slot0.  Both roles go through the same batches.
+struct Run {
+  int ai, e, slot0, nt, j0, j1, batch;
+  bool add;            // not the first pass over these neurons: flags are only set
+  bool keep_zeros;     // another pass may open a neuron that this one closes: its h is written too
+};
+
+struct ExpertMats {
+  const uint8_t *w1, *w2, *wd, *s1, *s2, *sd;
+};
+template <bool FP4>
+__device__ __forceinline__ ExpertMats expert_mats(const MoeArgs& a, int e) {
+  const size_t mat = (size_t)a.d_ff * a.d_model, wo = FP4 ? (size_t)e * (mat / 2) : (size_t)e * mat * 2;
+  const size_t so = FP4 ? (size_t)e * (mat / 32) : 0;
+  return ExpertMats{a.w1 + wo, a.w2 + wo, a.wd + wo, FP4 ? a.s1 + so : nullptr, FP4 ? a.s2 + so : nullptr,
+                    FP4 ? a.sd + so : nullptr};
+}
+
+template <bool FP4, bool ONE>
+__device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u, uint32_t& lists, int lane) {
+  const ExpertMats M = expert_mats<FP4>(a, u.e);
+  const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
+  for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
+    if (b < nb) {
+      const int jb = u.j0 + b * u.batch;
+      send_rows(R, at, sm, a.status, M.w1, M.s1, nullptr, jb, min(u.batch, u.j1 - jb), lane);
+    }
+    if (b >= 1 && b - 1 < nb) {
+      const int s = (b - 1) & 1;
+      ring_wait(&sm.open[s], (lists >> s) & 1u, sm, a.status, 77);
+      lists ^= 1u << s;
+      send_rows(R, at, sm, a.status, M.w2, M.s2, sm.rows[s], 0, *(volatile int*)&sm.nrows[s], lane);
+    }
+    if (ONE && b >= 2) {
+      const int s = b & 1;
+      ring_wait(&sm.down[s], (lists >> (2 + s)) & 1u, sm, a.status, 78);
+      lists ^= 4u << s;
+      send_rows(R, at, sm, a.status, M.wd, M.sd, sm.drows[s], 0, *(volatile int*)&sm.ndrows[s], lane);
+    }
+  }
+}
+
+// the sum at place i (row * 8 NG + token) over the warps that share the rows
+__device__ __forceinline__ float dot_sum(const Smem& sm, const Split& P, int i) {
+  float v = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < P.ks; ++k) v += sm.red[(size_t)k * kBatch * 8 + i];
+  return v;
+}
+
+template <bool FP4, int KU, int NG, bool ONE>
+__device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u, float (&y)[8],
+                                            int lane, int warp) {
+  const int tid = threadIdx.x;
+  const ExpertMats M = expert_mats<FP4>(a, u.e);
+  const float* b1 = a.b1 ? a.b1 + (size_t)u.e * a.d_ff : nullptr;
+  const float* b2 = a.b2 ? a.b2 + (size_t)u.e * a.d_ff : nullptr;
+  const Split P(a.d_model, KU, warp);
+  XFrag<KU, NG> x;
+  load_x<FP4, KU, NG>(a, sm, P, x, lane);
+  const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
+  // this thread's place in a batch's results: row tid / 8 NG, token tid % 8 NG
+  const int r = tid / (8 * NG), c = tid % (8 * NG);
+  constexpr int kRowsPerWarp = 32 / (8 * NG);
+  const float back = FP4 && c < u.nt ? 64.0f / sm.xup[sm.tok[c]] : 1.0f;
+  const float share = ONE ? choice_share(a, sm, u.slot0) : 0.0f;
+  for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
+    if (b < nb) {
+      // first factors of batch b, and its open neurons
+      const int s = b & 1, jb = u.j0 + b * u.batch, nr = min(u.batch, u.j1 - jb);
+      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, M.s1, nullptr, jb, nr, lane);
+      const float bias = b1 && r < nr ? b1[jb + r] : 0.0f;
+      csync();
+      float v = 0.0f;
+      if (r < nr && c < u.nt) {
+        v = dot_sum(sm, P, tid) * back;
+        v = relu_nan(v + bias);
+        if (!a.drelu) v *= v;
+      }
+      sm.first[s][tid] = v;
+      const unsigned any = __ballot_sync(0xffffffffu, v != 0.0f);
+      if (lane == 0) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i)
+          if ((any >> (i * 8 * NG)) & (8 * NG == 32 ? 0xffffffffu : (1u << (8 * NG & 31)) - 1u)) m |= 1u << i;
+        sm.mask[warp] = m;
+      }
+      csync();
+      if (tid < kBatch) {
+        // row tid of the batch (rows behind nr are closed)
+        uint64_t m = 0;
+#pragma unroll
+        for (int w = 0; w < kMWarps; ++w) m |= (uint64_t)sm.mask[w] << (w * kRowsPerWarp);
+        const bool open = (m >> tid) & 1u;
+        if (open) sm.rows[s][__popcll(m & ((1ull << tid) - 1ull))] = jb + tid;
+        if (tid == 0) sm.nrows[s] = __popcll(m);
+        mbar_arrive(&sm.open[s]);
+        if constexpr (!ONE) {
+          // a closed neuron's h is 0 and is not read again: only its flag is written
+          if (!open && tid < nr) {
+            if (!u.add) a.nz[(size_t)u.ai * a.d_ff + jb + tid] = 0;
+            if (u.keep_zeros)
+              for (int t = 0; t < u.nt; ++t) __stcg(a.h + (size_t)(u.slot0 + t) * a.d_ff + jb + tid, 0.0f);
+          }
+        }
+      }
+      csync();
+    }
+    if (b >= 1 && b - 1 < nb) {
+      // second factors of batch b - 1's open neurons, and h
+      const int s = (b - 1) & 1, jb = u.j0 + (b - 1) * u.batch, n = sm.nrows[s];
+      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, M.s2, sm.rows[s], 0, n, lane);
+      const int j = r < n ? sm.rows[s][r] : -1;
+      const float bias = b2 && j >= 0 ? b2[j] : 0.0f;
+      csync();
+      float h = 0.0f;
+      if (j >= 0 && c < u.nt) {
+        float v = dot_sum(sm, P, tid) * back + bias;
+        if (a.drelu) v = relu_nan(v);
+        h = sm.first[s][(j - jb) * 8 * NG + c] * v;
+        if constexpr (!ONE) __stcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j, h);
+      }
+      if constexpr (!ONE) {
         const unsigned any = __ballot_sync(0xffffffffu, h != 0.0f);
-        const unsigned mine = NG == 4 ? any : (any >> ((lane / (8 * NG)) * 8 * NG)) & ((1u << (8 * NG & 31)) - 1u);
+        const unsigned mine = (any >> ((lane / (8 * NG)) * 8 * NG)) & ((1u << (8 * NG & 31)) - 1u);
         if (j >= 0 && c == 0) {
-          uint8_t* f = a.nz + (size_t)ai * a.d_ff + j;
-          if (add) { if (mine) *f = 1; }
+          uint8_t* f = a.nz + (size_t)u.ai * a.d_ff + j;
+          if (u.add) { if (mine) *f = 1; }
           else *f = mine != 0;
         }
+        csync();
+      } else {
+        if (c == 0) sm.hval[r] = h;
+        csync();
+        if (tid < kBatch) {
+          // the neurons with h != 0, in order, and p h
+          const float hv = tid < n ? sm.hval[tid] : 0.0f;
+          const unsigned m = __ballot_sync(0xffffffffu, hv != 0.0f);
+          if (lane == 0) sm.scan[warp] = __popc(m);
+          asm volatile("bar.sync 2, 64;" ::: "memory");
+          if (hv != 0.0f) {
+            const int at2 = (warp ? sm.scan[0] : 0) + __popc(m & lanemask_lt());
+            sm.drows[s][at2] = sm.rows[s][tid];
+            sm.dval[s][at2] = hv * share;
+          }
+          if (tid == 0) sm.ndrows[s] = sm.scan[0] + sm.scan[1];
+          mbar_arrive(&sm.down[s]);
+        }
+        csync();
       }
-      __syncthreads();
+    }
+    if (ONE && b >= 2) {
+      const int s = b & 1;
+      down_stage_rows<FP4>(a, R, at, sm, M.sd, sm.drows[s], sm.dval[s], sm.ndrows[s], y, lane);
     }
   }
 }
 
-// The tokens of an active expert in passes of up to 32, each with the smallest
-// instance that holds it.
+// The runs of a hidden-layer item, in the order both roles take them: f(run).
 template <typename F>
-__device__ __forceinline__ void token_passes(const MoeArgs& a, Smem& sm, int first, int cnt, F&& f) {
-  for (int t0 = 0; t0 < cnt; t0 += 8 * kMaxNg) {
-    const int nt = min(8 * kMaxNg, cnt - t0);
-    __syncthreads();
-    if (threadIdx.x < 8 * kMaxNg)
-      sm.tok[threadIdx.x] = (int)threadIdx.x < nt ? __ldcg(a.table + kMtToken + first + t0 + threadIdx.x) : -1;
-    __syncthreads();
-    f(t0, nt);
+__device__ __forceinline__ void each_run(const MoeArgs& a, const Smem& sm, int item, int pass, F&& f) {
+  const long long N = (long long)sm.active * a.d_ff;
+  const long long n1 = N * (item + 1) / a.plan.hidden_items;
+  for (long long n0 = N * item / a.plan.hidden_items; n0 < n1;) {
+    Run u;
+    u.ai = (int)(n0 / a.d_ff);
+    u.j0 = (int)(n0 - (long long)u.ai * a.d_ff);
+    u.j1 = (int)min((long long)a.d_ff, (long long)u.j0 + (n1 - n0));
+    u.e = sm.expert[u.ai];
+    const int cnt = sm.count[u.ai], first = sm.firsts[u.ai];
+    // (every pass over a batch's worth of neurons before the next, so that the
+    // second pass finds the rows in L2)
+    const int step = cnt > pass ? 2 * kBatch : u.j1 - u.j0;
+    const int end = u.j1;
+    for (int j = u.j0; j < end; j += step)
+      for (int t0 = 0; t0 < cnt; t0 += pass) {
+        Run v = u;
+        v.j0 = j;
+        v.j1 = min(end, j + step);
+        v.slot0 = first + t0;
+        v.nt = min(pass, cnt - t0);
+        v.batch = v.nt > 8 ? kBatch / 2 : kBatch;
+        v.add = t0 > 0;
+        v.keep_zeros = cnt > pass;
+        f(v);
+      }
+    n0 += end - u.j0;
   }
 }
 
-template <bool FP4>
-__device__ void hidden_item(const MoeArgs& a, Smem& sm, int item, int lane, int warp) {
-  const int A = __ldcg(a.table);
-  const long long N = (long long)A * a.d_ff;
-  long long n0 = N * item / a.plan.hidden_items;
-  const long long n1 = N * (item + 1) / a.plan.hidden_items;
-  while (n0 < n1) {
-    const int ai = (int)(n0 / a.d_ff), j0 = (int)(n0 - (long long)ai * a.d_ff);
-    const int j1 = (int)min((long long)a.d_ff, (long long)j0 + (n1 - n0));
-    const int e = __ldcg(a.table + kMtExpert + ai), first = __ldcg(a.table + kMtFirst + ai), cnt = __ldcg(a.table + kMtCount + ai);
-    token_passes(a, sm, first, cnt, [&](int t0, int nt) {
-      if (nt <= 8) hidden_rows<FP4, 1>(a, sm, ai, e, first + t0, nt, j0, j1, t0 > 0, cnt > 8 * kMaxNg, lane, warp);
-      else if (nt <= 16) hidden_rows<FP4, 2>(a, sm, ai, e, first + t0, nt, j0, j1, t0 > 0, cnt > 8 * kMaxNg, lane, warp);
-      else hidden_rows<FP4, 4>(a, sm, ai, e, first + t0, nt, j0, j1, t0 > 0, cnt > 8 * kMaxNg, lane, warp);
-    });
-    n0 += j1 - j0;
+// tokens of a run into sm.tok (computing warps)
+__device__ __forceinline__ void run_tokens(Smem& sm, const Run& u) {
+  csync();
+  if (threadIdx.x < 8 * kMaxNg) sm.tok[threadIdx.x] = (int)threadIdx.x < u.nt ? sm.token[u.slot0 + threadIdx.x] : -1;
+  csync();
+}
+
+// (a function of its own per instance: inlined together they share the
+// registers of the largest and spill)
+template <bool FP4, int KU, int NG>
+__device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingAt& at, const Run& u, int lane, int warp) {
+  Smem& sm = smem();
+  float none[8];
+  RingAt here = at;                     // in registers
+  const Ring ring = R;
+  const Run run = u;
+  compute_run<FP4, KU, NG, false>(a, ring, here, sm, run, none, lane, warp);
+  at = here;
+}
+
+template <bool FP4, bool ONE>
+__device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, int item, uint32_t& lists,
+                                            int lane, int warp) {
+  // tokens per pass: two groups of 8 where x of both fits the registers
+  const int pass = a.d_model <= 4096 ? 16 : 8;
+  if (warp == kMWarps) {
+    each_run(a, sm, item, pass, [&](const Run& u) { send_run<FP4, ONE>(a, R, at, sm, u, lists, lane); });
+    return;
+  }
+  float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  each_run(a, sm, item, pass, [&](const Run& u) {
+    run_tokens(sm, u);
+    if constexpr (ONE) {
+      compute_run<FP4, 8, 1, true>(a, R, at, sm, u, y, lane, warp);
+    } else {
+      if (a.d_model > 4096) compute_pass<FP4, 16, 1>(a, R, at, u, lane, warp);
+      else if (u.nt <= 8) compute_pass<FP4, 8, 1>(a, R, at, u, lane, warp);
+      else compute_pass<FP4, 8, 2>(a, R, at, u, lane, warp);
+    }
+  });
+  if (ONE && threadIdx.x * 8 < a.d_model) {
+    float* o = a.parts + (size_t)item * a.d_model + threadIdx.x * 8;
+    __stcg(reinterpret_cast<float4*>(o), make_float4(y[0], y[1], y[2], y[3]));
+    __stcg(reinterpret_cast<float4*>(o + 4), make_float4(y[4], y[5], y[6], y[7]));
   }
 }
 
 // ---- down projection ---------------------------------------------------------
 // a strip of 64 (bf16) or 128 (4-bit) columns per warp; the CTA's flagged
 // neurons of [j0, j1) are listed once and their h staged as three bf16 parts
-template <bool FP4, int NG>
-__device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, int nt, int j0, int j1, int strip,
+template <bool FP4, int NG, int STR>
+__device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot0, int nt, int j0, int j1, int strip, int gap,
                           int split, int lane, int warp) {
+  Smem& sm = smem();
   constexpr int kCols = FP4 ? 16 : 8;                // columns of a lane
   constexpr int kMma = kCols / 2;                    // MMAs per 16 neurons and token group
   const int g = lane >> 2, q = lane & 3, tid = threadIdx.x;
-  const int col = strip * (8 * kCols) + g * kCols;
   // the matrix instructions need whole warps: a strip takes part when its first
   // column exists, a lane loads and stores when its own do (d_model is a
   // multiple of 32, a lane's columns divide that)
   const bool works = strip >= 0 && strip * (8 * kCols) < a.d_model;
-  const bool in = works && col < a.d_model;
+  int col[STR];
+  bool in[STR];
+#pragma unroll
+  for (int x = 0; x < STR; ++x) {
+    col[x] = (strip + x * gap) * (8 * kCols) + g * kCols;
+    in[x] = works && col[x] < a.d_model;
+    if (!in[x]) col[x] = 0;
+  }
   const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;
   const int sb = a.d_model / 32;
-  const uint8_t* w = a.wd + (size_t)e * a.d_ff * rb + (FP4 ? col / 2 : col * 2);
-  const uint8_t* sc = FP4 ? a.sd + (size_t)e * a.d_ff * sb + col / 32 : nullptr;
-  float acc[kMma][NG][4];
+  const uint8_t* w = a.wd + (size_t)e * a.d_ff * rb;
+  const uint8_t* sc = FP4 ? a.sd + (size_t)e * a.d_ff * sb : nullptr;
+  float acc[STR][kMma][NG][4];
 #pragma unroll
-  for (int m = 0; m < kMma; ++m)
+  for (int x = 0; x < STR; ++x)
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
+    for (int m = 0; m < kMma; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[x][m][n][i] = 0.0f;
 
   for (int jl = j0; jl < j1; jl += kListD) {
     // list the flagged neurons of [jl, je), in order
     const int je = min(j1, jl + kListD);
     int total = 0;
-    __syncthreads();
+    csync();
     for (int jb = jl; jb < je; jb += kMThreads) {
       const int j = jb + tid;
       const bool f = j < je && __ldcg(a.nz + (size_t)ai * a.d_ff + j) != 0;
       const unsigned m = __ballot_sync(0xffffffffu, f);
       if (lane == 0) sm.scan[warp] = __popc(m);
-      __syncthreads();
+      csync();
       int at = total, sum = 0;
 #pragma unroll
       for (int v = 0; v < kMWarps; ++v) {
@@ -570,7 +1037,7 @@ __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, 
       }
       if (f) sm.d.list[at + __popc(m & lanemask_lt())] = (uint16_t)(j - jl);
       total += sum;
-      __syncthreads();
+      csync();
     }
     for (int l0 = 0; l0 < total; l0 += kRowsD) {
       const int n = min(kRowsD, total - l0), np = (n + 15) & ~15;
@@ -588,35 +1055,42 @@ __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, 
           h = finite ? h - __bfloat162float(b) : 0.0f;
         }
       }
-      __syncthreads();
+      csync();
       if (works) {
         using Vec = typename std::conditional<FP4, uint2, uint4>::type;
-        auto load = [&](int st, Vec (&v)[4], uint32_t (&s)[4]) {
+        auto load = [&](int st, Vec (&v)[STR][4], uint32_t (&s)[STR][4]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = st * 16 + 4 * q + i;
-            const bool ok = in && r < n;
+            const bool ok = r < n;
             const size_t j = ok ? (size_t)(jl + sm.d.list[l0 + r]) : 0;
-            if constexpr (FP4) {
-              v[i] = ok ? ld_w8(w + j * rb) : make_uint2(0, 0);
-              s[i] = ok ? (uint32_t)__ldg(sc + j * sb) : 0u;
-            } else {
-              v[i] = ok ? ld_w(w + j * rb) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < STR; ++x) {
+              if constexpr (FP4) {
+                v[x][i] = ok && in[x] ? ld_w8(w + j * rb + col[x] / 2) : make_uint2(0, 0);
+                s[x][i] = ok && in[x] ? (uint32_t)__ldg(sc + j * sb + col[x] / 32) : 0u;
+              } else {
+                v[x][i] = ok && in[x] ? ld_w(w + j * rb + col[x] * 2) : make_uint4(0, 0, 0, 0);
+              }
             }
           }
         };
-        auto step = [&](int st, const Vec (&v)[4], const uint32_t (&s)[4]) {
+        auto step = [&](int st, const Vec (&vv)[STR][4], const uint32_t (&ss)[STR][4]) {
           uint2 b[NG][3];
 #pragma unroll
           for (int t = 0; t < NG; ++t)
 #pragma unroll
             for (int v = 0; v < 3; ++v)
               b[t][v] = *reinterpret_cast<const uint2*>(sm.d.h[v] + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
+#pragma unroll
+          for (int x = 0; x < STR; ++x) {
+          const Vec (&v)[4] = vv[x];
+          const uint32_t (&s)[4] = ss[x];
           auto mmas = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int t = 0; t < NG; ++t) {
 #pragma unroll
-              for (int v = 0; v < 3; ++v) mma_bf16(acc[m][t], a0, a1, a2, a3, b[t][v].x, b[t][v].y);
+              for (int v = 0; v < 3; ++v) mma_bf16(acc[x][m][t], a0, a1, a2, a3, b[t][v].x, b[t][v].y);
             }
           };
           if constexpr (!FP4) {
@@ -644,42 +1118,68 @@ __device__ void down_rows(const MoeArgs& a, Smem& sm, int ai, int e, int slot0, 
                    weight_pair<2>(p23, lo23, hi23, b23), weight_pair<3>(p23, lo23, hi23, b23));
             }
           }
+          }
         };
         const int nst = np / 16;
-        Vec v0[4], v1[4], v2[4];
-        uint32_t s0[4], s1[4], s2[4];
+        // one step ahead with two strips (their registers), two with one
+        Vec v0[STR][4], v1[STR][4];
+        uint32_t s0[STR][4], s1[STR][4];
         load(0, v0, s0);
-        load(1, v1, s1);
-        for (int st = 0; st < nst; st += 3) {          // two steps ahead
-          load(st + 2, v2, s2);
-          step(st, v0, s0);
-          if (st + 1 >= nst) break;
-          load(st + 3, v0, s0);
-          step(st + 1, v1, s1);
-          if (st + 2 >= nst) break;
-          load(st + 4, v1, s1);
-          step(st + 2, v2, s2);
+        if constexpr (STR > 1) {
+          for (int st = 0; st < nst; st += 2) {
+            load(st + 1, v1, s1);
+            step(st, v0, s0);
+            if (st + 1 >= nst) break;
+            load(st + 2, v0, s0);
+            step(st + 1, v1, s1);
+          }
+        } else {
+          Vec v2[STR][4];
+          uint32_t s2[STR][4];
+          load(1, v1, s1);
+          for (int st = 0; st < nst; st += 3) {
+            load(st + 2, v2, s2);
+            step(st, v0, s0);
+            if (st + 1 >= nst) break;
+            load(st + 3, v0, s0);
+            step(st + 1, v1, s1);
+            if (st + 2 >= nst) break;
+            load(st + 4, v1, s1);
+            step(st + 2, v2, s2);
+          }
         }
       }
-      __syncthreads();
+      csync();
     }
   }
-  if (in) {
-    const size_t slots = (size_t)a.T * a.top_k;
+  const size_t slots = (size_t)a.T * a.top_k;
+#pragma unroll
+  for (int x = 0; x < STR; ++x) {
+    if (!in[x]) continue;
 #pragma unroll
     for (int t = 0; t < NG; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int n = t * 8 + 2 * q + c;
         if (n < nt) {
-          float* o = a.parts + ((size_t)split * slots + slot0 + n) * a.d_model + col;
+          float* o = a.parts + ((size_t)split * slots + slot0 + n) * a.d_model + col[x];
 #pragma unroll
           for (int m = 0; m < kMma; m += 2)
             __stcg(reinterpret_cast<float4*>(o + 2 * m),
-                   make_float4(acc[m][t][c], acc[m][t][2 + c], acc[m + 1][t][c], acc[m + 1][t][2 + c]));
+                   make_float4(acc[x][m][t][c], acc[x][m][t][2 + c], acc[x][m + 1][t][c], acc[x][m + 1][t][2 + c]));
         }
       }
   }
+}
+
+template <bool FP4>
+constexpr int kStrips = FP4 ? 1 : 2;
+
+// an expert's tokens in passes of up to 16: f(first slot, tokens)
+template <typename F>
+__device__ __forceinline__ void each_pass(const Smem& sm, int ai, F&& f) {
+  const int first = sm.firsts[ai], cnt = sm.count[ai];
+  for (int t0 = 0; t0 < cnt; t0 += 8 * kMaxNg) f(first + t0, min(8 * kMaxNg, cnt - t0));
 }
 
 // splits of an expert's neurons: about one item per CTA in all
@@ -691,100 +1191,178 @@ __device__ __forceinline__ int down_splits(const MoeArgs& a, int A) {
 template <bool FP4>
 __device__ void down_item(const MoeArgs& a, Smem& sm, int item, int A, int S, int lane, int warp) {
   const int ct = item % a.plan.col_tiles, rest = item / a.plan.col_tiles, s = rest % S, ai = rest / S;
-  const int e = __ldcg(a.table + kMtExpert + ai), first = __ldcg(a.table + kMtFirst + ai), cnt = __ldcg(a.table + kMtCount + ai);
+  const int e = sm.expert[ai];
   const int j0 = (int)((long long)a.d_ff * s / S), j1 = (int)((long long)a.d_ff * (s + 1) / S);
-  const int strip = warp < a.plan.tile_warps ? ct * a.plan.tile_warps + warp : -1;
-  token_passes(a, sm, first, cnt, [&](int t0, int nt) {
-    // the 4-bit form has twice the columns, and half the tokens, per warp
-    if (nt <= 8) down_rows<FP4, 1>(a, sm, ai, e, first + t0, nt, j0, j1, strip, s, lane, warp);
-    else if (nt <= 16) down_rows<FP4, 2>(a, sm, ai, e, first + t0, nt, j0, j1, strip, s, lane, warp);
-    else if constexpr (!FP4) down_rows<FP4, 4>(a, sm, ai, e, first + t0, nt, j0, j1, strip, s, lane, warp);
-    else {
-      down_rows<FP4, 2>(a, sm, ai, e, first + t0, 16, j0, j1, strip, s, lane, warp);
-      down_rows<FP4, 2>(a, sm, ai, e, first + t0 + 16, nt - 16, j0, j1, strip, s, lane, warp);
+  const int tw = a.plan.tile_warps;
+  const int strip = warp < tw ? ct * tw * kStrips<FP4> + warp : -1;
+  each_pass(sm, ai, [&](int slot0, int nt) {
+    if constexpr (FP4) {
+      if (nt <= 8) down_rows<true, 1, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+      else down_rows<true, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+    } else {
+      if (nt <= 8) {
+        down_rows<false, 1, 2>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+      } else {      // the strips one after the other: their sums share the registers
+        down_rows<false, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+        down_rows<false, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip < 0 ? -1 : strip + tw, tw, s, lane, warp);
+      }
     }
   });
 }
 
 // ---- sums ----------------------------------------------------------------------
-__device__ void sum_item(const MoeArgs& a, int item, int S) {
-  const int n4 = a.d_model / 4;
-  const long long i = (long long)item * kMThreads + threadIdx.x;
-  if (i >= (long long)a.T * n4) return;
-  const int t = (int)(i / n4), c = (int)(i - (long long)t * n4) * 4;
+// 16 vectors of 4 outputs per item; 32 threads share the partial sums of each
+// (every 32nd in turn), so that their loads are all in flight at once
+__device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
+  const int n4 = a.d_model / 4, tid = threadIdx.x, vec = tid & 15, part = tid >> 4;
+  for (long long i0 = (long long)item * 16; i0 < (long long)a.T * n4; i0 += (long long)a.plan.out_items * 16) {
+  const long long i = i0 + vec;
+  const bool ok = i < (long long)a.T * n4;
+  const int t = ok ? (int)(i / n4) : 0, c = ok ? (int)(i - (long long)t * n4) * 4 : 0;
   const size_t slots = (size_t)a.T * a.top_k;
   float4 y = make_float4(0, 0, 0, 0);
-  for (int j = 0; j < a.top_k; ++j) {
-    const int slot = __ldcg(a.table + kMtSlot + t * a.top_k + j);
-    const float p = __ldcg(a.share + t * a.top_k + j);
-    const float* src = a.parts + (size_t)slot * a.d_model + c;
-    float4 v = make_float4(0, 0, 0, 0);
+  if (ok) {
+    if (a.plan.one_token) {
+      const float* src = a.parts + c;
 #pragma unroll 8
-    for (int s = 0; s < S; ++s) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * slots * a.d_model));
-      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      for (int s = part; s < a.plan.hidden_items; s += 32) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * a.d_model));
+        y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
+      }
+    } else {
+      const int n = a.top_k * S;
+#pragma unroll 4
+      for (int k = part; k < n; k += 32) {
+        const int j = k / S, s = k - j * S;
+        const float p = sm.share[t * a.top_k + j];
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(
+            a.parts + ((size_t)s * slots + sm.slot[t * a.top_k + j]) * a.d_model + c));
+        y.x = fmaf(p, u.x, y.x), y.y = fmaf(p, u.y, y.y), y.z = fmaf(p, u.z, y.z), y.w = fmaf(p, u.w, y.w);
+      }
     }
-    y.x = fmaf(p, v.x, y.x), y.y = fmaf(p, v.y, y.y), y.z = fmaf(p, v.z, y.z), y.w = fmaf(p, v.w, y.w);
   }
-  const size_t o = (size_t)t * a.d_model + c;
-  if (a.y_bf16) {
-    uint2 b;
-    b.x = (uint32_t)f32_to_bf16_bits(y.x) | ((uint32_t)f32_to_bf16_bits(y.y) << 16);
-    b.y = (uint32_t)f32_to_bf16_bits(y.z) | ((uint32_t)f32_to_bf16_bits(y.w) << 16);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.y) + o) = b;
-  } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + o) = y;
+  float4* red = reinterpret_cast<float4*>(sm.red);
+  csync();
+  red[tid] = y;
+  csync();
+  if (part == 0 && ok) {
+    for (int k = 1; k < 32; ++k) {
+      const float4 u = red[k * 16 + vec];
+      y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
+    }
+    const size_t o = (size_t)t * a.d_model + c;
+    if (a.y_bf16) {
+      uint2 b;
+      b.x = (uint32_t)f32_to_bf16_bits(y.x) | ((uint32_t)f32_to_bf16_bits(y.y) << 16);
+      b.y = (uint32_t)f32_to_bf16_bits(y.z) | ((uint32_t)f32_to_bf16_bits(y.w) << 16);
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.y) + o) = b;
+    } else {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + o) = y;
+    }
+  }
   }
 }
 
-template <bool FP4>
-__global__ void __launch_bounds__(kMThreads, 2) moe_kernel(MoeArgs a) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+template <bool FP4, bool ONE>
+__global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeArgs a) {
+  Smem& sm = smem();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_begin();
+  const bool computes = warp < kMWarps;
   const MoePlan& P = a.plan;
-  int A = 0, S = 1, nD = 0;             // known once the experts are selected
+  const Ring R{P.row_bytes, P.scale_bytes, P.pitch, P.stage_rows, P.stages};
+  RingAt at;
+  uint32_t lists = 0;                   // the copying warp: phases of the lists' barriers
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R.stages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], kMWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.open[i], kBatch);
+      mbar_init(&sm.down[i], kBatch);
+    }
+    mbar_fence_init();
+    sm.abort = 0;
+  }
+  pdl_begin();
+  int S = 1, nD = 0;                    // known once the experts are
+  bool routed = false;
   if (threadIdx.x == 0) sm.item = atomicAdd(a.ctl + MC_QUEUE, 1);
   __syncthreads();
   for (;;) {
     const int item = sm.item;
     __syncthreads();
-    int next = 0;
-    if (threadIdx.x == 0) next = atomicAdd(a.ctl + MC_QUEUE, 1);   // asked for early, used at the end
     int i = item;
     if (i < P.router_items) {
-      router_item(a, i, lane, warp);
-      if (finish(a.ctl + MC_ROUTED, sm) == P.router_items - 1) {
-        __threadfence();
-        select_experts(a, sm, lane, warp);
-        finish(a.ctl + MC_READY, sm);
+      if (computes) {
+        if (i < P.router_items - P.x_items) {
+          router_item(a, i, lane, warp);
+        } else {
+          const int t = (i - (P.router_items - P.x_items)) * kMWarps + warp;
+          if (t < a.T) {
+            const float u = x_power(a.x + (size_t)t * a.d_model, a.d_model, lane);
+            if (lane == 0) __stcg(a.xup + t, u);
+          }
+        }
+        if (finish(a.ctl + MC_ROUTED, sm) == P.router_items - 1) {
+          __threadfence();
+          select_experts<false>(a, a.logits, true, lane, warp);
+          publish_routing(a, sm);
+          finish(a.ctl + MC_READY, sm);
+        }
       }
     } else {
       i -= P.router_items;
-      if (A == 0) {
-        if (!wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) break;   // no tables to go by
-        A = __ldcg(a.table);
-        S = down_splits(a, A);
-        nD = A * S * P.col_tiles;
+      if (!routed) {
+        if (computes) {
+          if (P.local) {
+            route_here(a, item == 0, lane, warp);
+          } else if (wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) {
+            fetch_routing(a, sm);
+          } else if (threadIdx.x == 0) {
+            sm.active = 0;              // no tables to go by
+          }
+        }
+        __syncthreads();
+        if (sm.active == 0) break;
+        routed = true;
+        if constexpr (!ONE) {
+          S = down_splits(a, sm.active);
+          nD = sm.active * S * P.col_tiles;
+        }
       }
       if (i < P.hidden_items) {
-        hidden_item<FP4>(a, sm, i, lane, warp);
-        finish(a.ctl + MC_HIDDEN, sm);
+        hidden_item<FP4, ONE>(a, R, at, sm, i, lists, lane, warp);
+        if (computes) finish(a.ctl + MC_HIDDEN, sm);
       } else if ((i -= P.hidden_items) < nD) {
-        wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
-        down_item<FP4>(a, sm, i, A, S, lane, warp);
-        finish(a.ctl + MC_DOWN, sm);
+        if constexpr (!ONE) {
+          if (computes) {
+            wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
+            down_item<FP4>(a, sm, i, sm.active, S, lane, warp);
+            finish(a.ctl + MC_DOWN, sm);
+          }
+        }
       } else if ((i -= nD) < P.out_items) {
-        wait_for(a.ctl + MC_DOWN, nD, a.status, 72, sm);
-        sum_item(a, i, S);
+        if (computes) {
+          if (ONE) wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 72, sm);
+          else wait_for(a.ctl + MC_DOWN, nD, a.status, 73, sm);
+          sum_item(a, sm, i, S);
+        }
       } else {
         break;
       }
     }
-    if (threadIdx.x == 0) sm.item = next;
+    // (drawn when the item is done: a CTA that holds its next item beforehand
+    // takes two of the hidden layer's equal shares while another takes none)
+    if (threadIdx.x == 0) sm.item = atomicAdd(a.ctl + MC_QUEUE, 1);
     __syncthreads();
   }
+  // after a wait that gave up, copies may still be in flight
+  if (warp == kMWarps && lane == 0 && *(volatile int*)&sm.abort)
+    for (int k = 1; k <= R.stages && k <= at.issued; ++k) {
+      const int g = at.issued - k;
+      mbar_wait(&sm.full[g % R.stages], (uint32_t)(g / R.stages) & 1u);
+    }
   // the last CTA to leave clears the counters for the next call
   if (threadIdx.x == 0) {
     __threadfence();
@@ -798,13 +1376,30 @@ __global__ void __launch_bounds__(kMThreads, 2) moe_kernel(MoeArgs a) {
 MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4) {
   (void)d_ff;
   MoePlan p;
-  p.grid = 2 * kNumSMs;
-  p.router_items = (n_experts + kMWarps - 1) / kMWarps * ((T + 7) / 8);
+  p.grid = kNumSMs;
+  p.local = T <= 32 && n_experts <= 64 && n_experts * d_model <= 65536 && T * n_experts * d_model <= kMoeLocalWork;
+  p.x_items = (!p.local && fp4) ? (T + kMWarps - 1) / kMWarps : 0;
+  p.router_tokens = (long)T * n_experts <= kNumSMs * kMWarps ? 1 : 4;
+  p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
+  p.one_token = T == 1 && d_model <= 4096;
   p.hidden_items = p.grid;
-  const int strips = (d_model + (fp4 ? 127 : 63)) / (fp4 ? 128 : 64);
-  p.col_tiles = (strips + kMWarps - 1) / kMWarps;
-  p.tile_warps = (strips + p.col_tiles - 1) / p.col_tiles;
-  p.out_items = (int)(((long long)T * (d_model / 4) + kMThreads - 1) / kMThreads);
+  // the ring: stages of about 36 KB, whole tiles of 8 rows where rows are short;
+  // a row's scales travel with it where bulk copies can take them
+  p.row_bytes = fp4 ? d_model / 2 : d_model * 2;
+  p.scale_bytes = fp4 && d_model % 512 == 0 ? d_model / 32 : 0;
+  // eight rows' loads of 64 or 16 bytes each do not meet in a bank
+  const int apart = fp4 ? 16 : 64;
+  p.pitch = (p.row_bytes + p.scale_bytes + 127 - apart) / 128 * 128 + apart;
+  p.stage_rows = 36 * 1024 / p.pitch;
+  if (p.stage_rows < 1) p.stage_rows = 1;
+  if (p.stage_rows > 8) p.stage_rows = p.stage_rows > 64 ? 64 : p.stage_rows / 8 * 8;
+  p.stages = kRing / (p.stage_rows * p.pitch);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  const int strips = (d_model + (fp4 ? 127 : 63)) / (fp4 ? 128 : 64), per = fp4 ? kStrips<true> : kStrips<false>;
+  p.col_tiles = (strips + kMWarps * per - 1) / (kMWarps * per);
+  p.tile_warps = (strips + p.col_tiles * per - 1) / (p.col_tiles * per);
+  const long vecs = ((long)T * (d_model / 4) + 15) / 16;
+  p.out_items = (int)(vecs < p.grid ? vecs : p.grid);
   p.max_splits = kMoePartRows / (T * top_k);
   if (p.max_splits < 1) p.max_splits = 1;
   if (p.max_splits > p.grid) p.max_splits = p.grid;
@@ -812,11 +1407,13 @@ MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4
 }
 
 cudaError_t launch_moe(const MoeArgs& a, cudaStream_t s) {
-  static unsigned done[2] = {0, 0};
-  auto k = a.fp4 ? moe_kernel<true> : moe_kernel<false>;
-  cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[a.fp4 ? 1 : 0]);
+  static unsigned done[4] = {0, 0, 0, 0};
+  const bool one = a.plan.one_token != 0;
+  auto k = a.fp4 ? (one ? moe_kernel<true, true> : moe_kernel<true, false>)
+                 : (one ? moe_kernel<false, true> : moe_kernel<false, false>);
+  cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[(a.fp4 ? 2 : 0) + (one ? 1 : 0)]);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kMThreads), sizeof(Smem), s, a);
+  e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -6,6 +6,8 @@
 namespace qs {
 
 constexpr int kMoeMaxT = 64;          // tokens per launch
+constexpr int kMoeLocalWork = 524288; // local routing: products that each CTA does for itself
+constexpr int kMoeMaxModel = QS_MOE_MAX_MODEL;
 constexpr int kMoePartRows = 1024;    // rows of partial sums (splits x tokens x experts per token)
 
 // counters, zero between calls
@@ -13,11 +15,16 @@ enum MoeCtl { MC_QUEUE = 0, MC_ROUTED = 1, MC_READY = 2, MC_HIDDEN = 3, MC_DOWN 
 
 struct MoePlan {
   int grid = 0;
+  int local = 0;            // every CTA evaluates the router for itself
+  int one_token = 0;        // a CTA goes on from its neurons to their down rows
+  int router_tokens = 1;    // tokens of a router task
   int router_items = 0;     // queue items of the router
+  int x_items = 0;          // ... of which look for x's powers (4-bit weights)
   int hidden_items = 0;     // ... of the hidden layer
   int out_items = 0;        // ... of the final sums
   int col_tiles = 0;        // column tiles of the down projection
-  int tile_warps = 0;       // warps of a tile (each a strip of columns)
+  int tile_warps = 0;       // warps of a tile (each one or two strips of columns)
+  int row_bytes = 0, scale_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
 };
 MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4);
@@ -47,6 +54,7 @@ struct MoeArgs {
   float* logits = nullptr;                // [T, E]
   int32_t* table = nullptr;               // routing tables (see moe.cu)
   float* share = nullptr;                 // [T, top_k]
+  float* xup = nullptr;                   // [T] power of two that takes x to float16 (4-bit weights)
   float* h = nullptr;                     // [T * top_k, d_ff]
   uint8_t* nz = nullptr;                  // [min(E, T * top_k), d_ff]
   float* parts = nullptr;                 // [splits][T * top_k][d_model]

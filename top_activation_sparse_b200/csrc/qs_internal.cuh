@@ -226,6 +226,7 @@ struct WsLayout {
   size_t moe_logits = 0;      // [Tc, experts] f32 (mixture of experts)
   size_t moe_table = 0;       // routing tables, int32
   size_t moe_share = 0;       // [Tc, top_k] f32
+  size_t moe_xup = 0;         // [Tc] f32, 4-bit weights
   size_t moe_nz = 0;          // [active experts, d_ff] flags
   size_t alpha_parts = 0;     // f64 partial sums (ternary pack)
   size_t alpha = 0;           // f32 (ternary pack)
