@@ -36,7 +36,7 @@
 //
 // Products run on mma.sync m16n8k16 (16 tokens x 8 neurons; 16 columns x 8
 // tokens in the down projection): with weights read once, a few tokens stay
-// bound by bytes.  x stays in registers: each of 16 warps holds its part of
+// bound by bytes.  x stays in registers: each of 8 warps holds its part of
 // d_model for all tokens of the pass.  The sum over k may be permuted freely as
 // long as both operands agree; a lane's 16 bytes are its k values.  x and bf16
 // weights enter exactly; h enters as the sum of three bf16 numbers (relative
@@ -47,7 +47,8 @@
 namespace qs {
 namespace {
 
-constexpr int kMWarps = 16;            // warps that compute
+constexpr int kMWarps = 8;             // warps that compute (168 registers each: a spill would go to L2, the
+                                       // ring leaves no L1)
 constexpr int kMThreads = kMWarps * 32;
 constexpr int kThreads = kMThreads + 32;   // and one that copies
 constexpr int kMaxNg = 2;              // groups of 8 tokens per pass
@@ -61,7 +62,7 @@ constexpr int kMaxStages = 8;
 struct Smem {
   unsigned char ring[kRing];
   union {
-    float red[kMWarps * kBatch * 8];             // 32 KB: the warps' sums
+    float red[kMWarps * kBatch * 8];             // 16 KB: the warps' sums
     struct {
       __nv_bfloat16 h[3][8 * kMaxNg * kHPitch];
       uint16_t list[kListD];
@@ -75,7 +76,7 @@ struct Smem {
   float dval[2][kBatch];
   int ndrows[2];
   float hval[kBatch];
-  uint32_t mask[kMWarps];
+  uint32_t mask[kBatch / 4];
   // this call's routing
   int16_t expert[kMoeMaxE], firsts[kMoeMaxE], count[kMoeMaxE];
   int16_t token[kMoeMaxSlots], slot[kMoeMaxSlots];
@@ -98,7 +99,7 @@ __device__ __forceinline__ Smem& smem() {
 }
 
 // the computing warps' barrier
-__device__ __forceinline__ void csync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void csync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 ld_w(const uint8_t* p) {
   uint4 r;
@@ -205,7 +206,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* b, uint32_t parity, Smem& sm
 }
 
 // ---- router ------------------------------------------------------------------
-// item: 16 tasks, one per warp, of one expert and router_tokens tokens
+// item: 8 tasks, one per warp, of one expert and router_tokens tokens
 __device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
   const int nt = a.plan.router_tokens, groups = (a.T + nt - 1) / nt;
   const int task = item * kMWarps + warp;
@@ -243,7 +244,7 @@ __device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, i
   }
 }
 
-// The power of two that brings a token's largest |x| into [2^7, 2^8).
+// The power of two that brings a token's largest |x| into [2^14, 2^15).
 __device__ __forceinline__ float x_power(const __nv_bfloat16* x, int d, int lane) {
   uint32_t m = 0;
 #pragma unroll 4
@@ -258,7 +259,7 @@ __device__ __forceinline__ float x_power(const __nv_bfloat16* x, int d, int lane
   const int e = (int)(m >> 7);                      // biased exponent of the largest
   // (nothing but subnormal numbers, or a non-finite one: no useful power);
   // at most 2^126, so that its reciprocal is a normal number
-  const int up = e == 0 || e == 255 ? 0 : min(126, 127 + 7 - e);
+  const int up = e == 0 || e == 255 ? 0 : min(126, 127 + 14 - e);
   return __uint_as_float((uint32_t)(up + 127) << 23);
 }
 
@@ -494,20 +495,20 @@ __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, D
 // Up to KU units of 32 values of each row per warp, NG groups of 8 tokens; four
 // registers per unit and group.
 //   bf16 weights: a lane's 8 values of x (16 bytes), in order.
-//   4-bit weights: the products run on e4m3 x e4m3 -> float32 (m16n8k32), whose
-//   sums are correctly rounded float32.  A code's bits, moved to the low
-//   exponent and the high mantissa bit of e4m3, are its value times 2^-6
-//   (subnormals included): no conversion.  x, times the power of two that
-//   brings its token's largest into [2^7, 2^8), is the sum of two e4m3 numbers,
-//   the second times 2^-4: exact for bf16 down to 2^-14 of the largest, and
-//   within 2^-22 of it below that.  The two parts are two rows of the matrix.
+//   4-bit weights: a code's bits, moved to the lowest exponent bits and the
+//   highest mantissa bit of float16, are its value times 2^-14 (subnormals
+//   included): no conversion, four operations a pair.  (The conversion
+//   instruction takes as long, at a quarter of the rate; matrix instructions of
+//   e4m3, into which a code goes as easily, were three times slower than those
+//   of float16.)  x, times the power of two that brings its token's largest into
+//   [2^14, 2^15), is float16, exact down to 2^-39 of that largest.
 template <int KU, int NG>
 struct XFrag {
   uint32_t v[KU][NG][4];
 };
 
-// KS warps share the rows' length, 16 / KS groups take the 8-row tiles of a
-// stage in turn.
+// KS warps share the rows' length, 8 / KS groups take the tiles of a stage (8
+// rows, 16 of 4-bit weights) in turn.
 struct Split {
   int units, ks, groups, part, group, per, n;      // units of this warp: part * per .. + n
   __device__ Split(int d, int ku, int warp) {
@@ -522,15 +523,12 @@ struct Split {
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_back(uint32_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// bits 4c..4c+3 of each half of p (a code each) -> a pair of float16, times 2^-14
+template <int C>
+__device__ __forceinline__ uint32_t half_pair(uint32_t p) {
+  const uint32_t m = C == 3 ? p >> 3 : p << (9 - 4 * C);
+  const uint32_t s = C == 3 ? p : p << (12 - 4 * C);
+  return (m & 0x0e000e00u) | (s & 0x80008000u);
 }
 
 template <bool FP4, int KU, int NG>
@@ -547,24 +545,14 @@ __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const S
       if (t >= 0 && i < P.n) v = ld_x(px + i * 32);
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
       if constexpr (FP4) {
-        // values 0, 2, 4, 6 and 1, 3, 5, 7, as the codes come out of their words
-        uint32_t f[2][2] = {{0, 0}, {0, 0}};       // [part][even, odd]
+        // values c and c + 4, as the codes come out of their words
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const float v0 = (o ? bf16hi(u[2 * j]) : bf16lo(u[2 * j])) * up;
-            const float v1 = (o ? bf16hi(u[2 * j + 1]) : bf16lo(u[2 * j + 1])) * up;
-            const uint32_t p = e4m3x2(v0, v1);
-            const float2 b = e4m3x2_back(p);
-            f[0][o] |= p << (16 * j);
-            f[1][o] |= e4m3x2((v0 - b.x) * 16.0f, (v1 - b.y) * 16.0f) << (16 * j);
-          }
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t lo = u[c >> 1], hi = u[2 + (c >> 1)];
+          const __half2 h = c & 1 ? __floats2half2_rn(bf16hi(lo) * up, bf16hi(hi) * up)
+                                  : __floats2half2_rn(bf16lo(lo) * up, bf16lo(hi) * up);
+          x.v[i][n][c] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        x.v[i][n][0] = f[0][0];
-        x.v[i][n][1] = f[1][0];
-        x.v[i][n][2] = f[0][1];
-        x.v[i][n][3] = f[1][1];
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) x.v[i][n][j] = u[j];
@@ -573,11 +561,12 @@ __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const S
   }
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&x)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1), "f"(0.0f));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // n rows from the ring times the pass's tokens: sums of row r (of the batch) and
@@ -595,8 +584,10 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
     const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
-    for (int t0 = P.group * 8; t0 < nr; t0 += P.groups * 8) {
-      const unsigned char* row = stage + (t0 + g < nr ? t0 + g : t0) * R.pitch;
+    constexpr int kTile = FP4 ? 16 : 8;
+    for (int t0 = P.group * kTile; t0 < nr; t0 += P.groups * kTile) {
+      const int ra = t0 + g < nr ? t0 + g : t0;
+      const unsigned char* row = stage + ra * R.pitch;
       if constexpr (!FP4) {
         // four sums in turn: one matrix instruction after the other into the
         // same sum takes 20 to 32 cycles each
@@ -605,7 +596,7 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        constexpr int kAhead = NG == 1 && KU == 8 ? 8 : 4;      // loads before the first product
+        constexpr int kAhead = KU * NG <= 16 ? 8 : 4;      // loads before the first product
 #pragma unroll
         for (int h = 0; h < KU; h += kAhead) {
           uint4 w[kAhead];
@@ -631,58 +622,74 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
           }
         }
       } else {
-        // a unit is one block: its sum times its scale.  Columns 2q and 2q + 1
-        // are the tile's rows 2q and 2q + 1.
-        const int c0 = min(t0 + 2 * q, nr - 1), c1 = min(t0 + 2 * q + 1, nr - 1);
-        uint32_t s[2][KU];
-        if (R.sb && KU == 8 && P.per == 8) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint2 v = *reinterpret_cast<const uint2*>(stage + (c ? c1 : c0) * R.pitch + R.rb + first);
-#pragma unroll
-            for (int i = 0; i < KU; ++i) s[c][i] = ((i < 4 ? v.x : v.y) >> (8 * (i & 3))) & 0xffu;
-          }
+        // the neurons are the matrix's 16 rows, the tokens its 8 columns; a unit
+        // is one block: its sum times its scale
+        const int rb2 = t0 + 8 + g < nr ? t0 + 8 + g : t0;
+        const unsigned char* row2 = stage + rb2 * R.pitch;
+        const uint8_t *p0, *p1;
+        if (R.sb) {
+          p0 = row + R.rb + first;
+          p1 = row2 + R.rb + first;
         } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int r = c ? c1 : c0;
-            const uint8_t* p = R.sb ? stage + r * R.pitch + R.rb + first
-                                    : sc + (size_t)(list ? list[i0 + r] : j0 + i0 + r) * (a.d_model / 32) + first;
-#pragma unroll
-            for (int i = 0; i < KU; ++i) s[c][i] = R.sb ? p[i < P.n ? i : 0] : __ldg(p + (i < P.n ? i : 0));
-          }
+          p0 = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * (a.d_model / 32) + first;
+          p1 = sc + (size_t)(list ? list[i0 + rb2] : j0 + i0 + rb2) * (a.d_model / 32) + first;
         }
-        uint32_t w[KU];
-#pragma unroll
-        for (int i = 0; i < KU; ++i) w[i] = *reinterpret_cast<const uint32_t*>(row + (first + (i < P.n ? i : 0)) * 16 + q * 4);
         float acc[NG][4];
 #pragma unroll
         for (int t = 0; t < NG; ++t)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < KU; ++i) {
-          const uint32_t even = ((w[i] * 4u) & 0x1c1c1c1cu) | ((w[i] * 16u) & 0x80808080u);
-          const uint32_t odd = ((w[i] >> 2) & 0x1c1c1c1cu) | (w[i] & 0x80808080u);
-          // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
-          // of its codes, all 0)
-          const float f0 = __uint_as_float(s[0][i] << 23), f1 = __uint_as_float(s[1][i] << 23);
+        for (int h = 0; h < KU; h += 8) {             // eight units at a time
+          uint32_t s[2][8], w[2][8];
+          if (R.sb && P.per % 8 == 0) {
+            const uint2 v0 = *reinterpret_cast<const uint2*>(p0 + h), v1 = *reinterpret_cast<const uint2*>(p1 + h);
 #pragma unroll
-          for (int t = 0; t < NG; ++t) {
-            float d[4];
-            mma_e4m3(d, x.v[i][t], even, odd);
-            acc[t][0] = fmaf(d[0], f0, acc[t][0]);
-            acc[t][1] = fmaf(d[1], f1, acc[t][1]);
-            acc[t][2] = fmaf(d[2], f0, acc[t][2]);
-            acc[t][3] = fmaf(d[3], f1, acc[t][3]);
+            for (int i = 0; i < 8; ++i) {
+              s[0][i] = ((i < 4 ? v0.x : v0.y) >> (8 * (i & 3))) & 0xffu;
+              s[1][i] = ((i < 4 ? v1.x : v1.y) >> (8 * (i & 3))) & 0xffu;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int at2 = h + i < P.n ? h + i : 0;
+              s[0][i] = R.sb ? p0[at2] : __ldg(p0 + at2);
+              s[1][i] = R.sb ? p1[at2] : __ldg(p1 + at2);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int at2 = (first + (h + i < P.n ? h + i : 0)) * 16 + q * 4;
+            w[0][i] = *reinterpret_cast<const uint32_t*>(row + at2);
+            w[1][i] = *reinterpret_cast<const uint32_t*>(row2 + at2);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
+            // of its codes, all 0)
+            const float f0 = __uint_as_float(s[0][i] << 23), f1 = __uint_as_float(s[1][i] << 23);
+            const uint32_t a0 = half_pair<0>(w[0][i]), a1 = half_pair<0>(w[1][i]), a2 = half_pair<1>(w[0][i]),
+                           a3 = half_pair<1>(w[1][i]);
+            const uint32_t c0 = half_pair<2>(w[0][i]), c1 = half_pair<2>(w[1][i]), c2 = half_pair<3>(w[0][i]),
+                           c3 = half_pair<3>(w[1][i]);
+#pragma unroll
+            for (int t = 0; t < NG; ++t) {
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma_f16(d, a0, a1, a2, a3, x.v[h + i][t][0], x.v[h + i][t][1]);
+              mma_f16(d, c0, c1, c2, c3, x.v[h + i][t][2], x.v[h + i][t][3]);
+              acc[t][0] = fmaf(d[0], f0, acc[t][0]);
+              acc[t][1] = fmaf(d[1], f0, acc[t][1]);
+              acc[t][2] = fmaf(d[2], f1, acc[t][2]);
+              acc[t][3] = fmaf(d[3], f1, acc[t][3]);
+            }
           }
         }
+        // rows g and g + 8 of the tile, tokens 2q and 2q + 1
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rr = t0 + 2 * q + c;
-          if (rr < nr)
-#pragma unroll
-            for (int t = 0; t < NG; ++t) red[(i0 + rr) * 8 * NG + t * 8 + g] = fmaf(acc[t][2 + c], 0.0625f, acc[t][c]);
+        for (int t = 0; t < NG; ++t) {
+          float* o = red + (size_t)(i0 + t0 + g) * 8 * NG + t * 8 + 2 * q;
+          if (t0 + g < nr) *reinterpret_cast<float2*>(o) = make_float2(acc[t][0], acc[t][1]);
+          if (t0 + 8 + g < nr) *reinterpret_cast<float2*>(o + 64 * NG) = make_float2(acc[t][2], acc[t][3]);
         }
       }
     }
@@ -692,39 +699,43 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
   }
 }
 
-// One token, d_model <= 4096: the CTA goes on to its neurons' down rows, 8
-// columns per thread.
+// One token, d_model <= 4096: the CTA goes on to its neurons' down rows, 16
+// columns per thread (two vectors of 8: 8 tid and 2048 + 8 tid).
 template <bool FP4>
 __device__ __forceinline__ void down_stage_rows(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const uint8_t* sc,
-                                                const int* list, const float* val, int n, float (&y)[8], int lane) {
+                                                const int* list, const float* val, int n, float (&y)[2][8], int lane) {
   const int tid = threadIdx.x;
-  const bool in = tid * 8 < a.d_model;
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 76);
     const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
-    if (in) {
-      for (int r = 0; r < nr; ++r) {
-        const unsigned char* row = stage + r * R.pitch;
-        float h = val[i0 + r];
-        if constexpr (!FP4) {
-          const uint4 w = *reinterpret_cast<const uint4*>(row + tid * 16);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll 2
+    for (int r = 0; r < nr; ++r) {
+      const unsigned char* row = stage + r * R.pitch;
+      const float h = val[i0 + r];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            y[2 * c] = fmaf(h, bf16lo(u[c]), y[2 * c]);
-            y[2 * c + 1] = fmaf(h, bf16hi(u[c]), y[2 * c + 1]);
-          }
-        } else {
-          const uint32_t b = R.sb ? row[R.rb + tid / 4] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + tid / 4);
-          h *= e8m0_value(b);
-          uint32_t f[4];
-          e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + tid * 4), f);
+      for (int v = 0; v < 2; ++v) {
+        const int col = v * 2048 + tid * 8;
+        if (col < a.d_model) {
+          if constexpr (!FP4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(row + col * 2);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f[c]));
-            y[2 * c] = fmaf(h, v.x, y[2 * c]);
-            y[2 * c + 1] = fmaf(h, v.y, y[2 * c + 1]);
+            for (int c = 0; c < 4; ++c) {
+              y[v][2 * c] = fmaf(h, bf16lo(u[c]), y[v][2 * c]);
+              y[v][2 * c + 1] = fmaf(h, bf16hi(u[c]), y[v][2 * c + 1]);
+            }
+          } else {
+            const uint32_t b = R.sb ? row[R.rb + col / 32] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + col / 32);
+            const float hs = h * e8m0_value(b);
+            uint32_t f[4];
+            e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + col / 2), f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[c]));
+              y[v][2 * c] = fmaf(hs, e.x, y[v][2 * c]);
+              y[v][2 * c + 1] = fmaf(hs, e.y, y[v][2 * c + 1]);
+            }
           }
         }
       }
@@ -795,8 +806,8 @@ __device__ __forceinline__ float dot_sum(const Smem& sm, const Split& P, int i) 
 }
 
 template <bool FP4, int KU, int NG, bool ONE>
-__device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u, float (&y)[8],
-                                            int lane, int warp) {
+__device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u,
+                                            float (&y)[2][8], int lane, int warp) {
   const int tid = threadIdx.x;
   const ExpertMats M = expert_mats<FP4>(a, u.e);
   const float* b1 = a.b1 ? a.b1 + (size_t)u.e * a.d_ff : nullptr;
@@ -805,80 +816,100 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
   XFrag<KU, NG> x;
   load_x<FP4, KU, NG>(a, sm, P, x, lane);
   const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
-  // this thread's place in a batch's results: row tid / 8 NG, token tid % 8 NG
-  const int r = tid / (8 * NG), c = tid % (8 * NG);
-  constexpr int kRowsPerWarp = 32 / (8 * NG);
-  const float back = FP4 && c < u.nt ? 64.0f / sm.xup[sm.tok[c]] : 1.0f;
+  // this thread's places in a batch's results: i = tid and tid + 256, row
+  // i / 8 NG, token i % 8 NG (the same for both)
+  constexpr int kPer = kBatch * 8 / kMThreads, kTok = 8 * NG, kRowsPerWarp = 32 / kTok;
+  const int c = tid % kTok, r0 = tid / kTok;
+  constexpr int kStep = kMThreads / kTok;                // rows between a thread's places
+  const float back = FP4 && c < u.nt ? 16384.0f / sm.xup[sm.tok[c]] : 1.0f;
   const float share = ONE ? choice_share(a, sm, u.slot0) : 0.0f;
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
-    if (b < nb) {
-      // first factors of batch b, and its open neurons
-      const int s = b & 1, jb = u.j0 + b * u.batch, nr = min(u.batch, u.j1 - jb);
-      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, M.s1, nullptr, jb, nr, lane);
-      const float bias = b1 && r < nr ? b1[jb + r] : 0.0f;
-      csync();
-      float v = 0.0f;
-      if (r < nr && c < u.nt) {
-        v = dot_sum(sm, P, tid) * back;
-        v = relu_nan(v + bias);
-        if (!a.drelu) v *= v;
-      }
-      sm.first[s][tid] = v;
-      const unsigned any = __ballot_sync(0xffffffffu, v != 0.0f);
-      if (lane == 0) {
-        uint32_t m = 0;
+    // (one body for both factors: the code of two does not stay in the
+    // instruction cache)
+#pragma unroll 1
+    for (int second = 0; second < 2; ++second) {
+      const int bb = b - second;
+      if (bb < 0 || bb >= nb) continue;
+      const int s = bb & 1, jb = u.j0 + bb * u.batch;
+      const int n = second ? sm.nrows[s] : min(u.batch, u.j1 - jb);
+      const int* list = second ? sm.rows[s] : nullptr;
+      const float* bs = second ? b2 : b1;
+      int j[kPer];
+      float bias[kPer];
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i)
-          if ((any >> (i * 8 * NG)) & (8 * NG == 32 ? 0xffffffffu : (1u << (8 * NG & 31)) - 1u)) m |= 1u << i;
-        sm.mask[warp] = m;
+      for (int k = 0; k < kPer; ++k) {
+        const int r = r0 + k * kStep;
+        j[k] = r < n ? (list ? list[r] : jb + r) : -1;
+        bias[k] = bs && j[k] >= 0 ? __ldg(bs + j[k]) : 0.0f;
       }
+      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, second ? M.s2 : M.s1, list, jb, n, lane);
       csync();
-      if (tid < kBatch) {
-        // row tid of the batch (rows behind nr are closed)
-        uint64_t m = 0;
+      if (!second) {
+        // first factors of batch b, and its open neurons
 #pragma unroll
-        for (int w = 0; w < kMWarps; ++w) m |= (uint64_t)sm.mask[w] << (w * kRowsPerWarp);
-        const bool open = (m >> tid) & 1u;
-        if (open) sm.rows[s][__popcll(m & ((1ull << tid) - 1ull))] = jb + tid;
-        if (tid == 0) sm.nrows[s] = __popcll(m);
-        mbar_arrive(&sm.open[s]);
-        if constexpr (!ONE) {
-          // a closed neuron's h is 0 and is not read again: only its flag is written
-          if (!open && tid < nr) {
-            if (!u.add) a.nz[(size_t)u.ai * a.d_ff + jb + tid] = 0;
-            if (u.keep_zeros)
-              for (int t = 0; t < u.nt; ++t) __stcg(a.h + (size_t)(u.slot0 + t) * a.d_ff + jb + tid, 0.0f);
+        for (int k = 0; k < kPer; ++k) {
+          float v = 0.0f;
+          if (j[k] >= 0 && c < u.nt) {
+            v = relu_nan(dot_sum(sm, P, tid + k * kMThreads) * back + bias[k]);
+            if (!a.drelu) v *= v;
+          }
+          sm.first[s][tid + k * kMThreads] = v;
+          const unsigned any = __ballot_sync(0xffffffffu, v != 0.0f);
+          if (lane == 0) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kRowsPerWarp; ++i)
+              if ((any >> (i * kTok)) & ((1u << kTok) - 1u)) m |= 1u << i;
+            sm.mask[k * kMWarps + warp] = m;
           }
         }
-      }
-      csync();
-    }
-    if (b >= 1 && b - 1 < nb) {
-      // second factors of batch b - 1's open neurons, and h
-      const int s = (b - 1) & 1, jb = u.j0 + (b - 1) * u.batch, n = sm.nrows[s];
-      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, M.s2, sm.rows[s], 0, n, lane);
-      const int j = r < n ? sm.rows[s][r] : -1;
-      const float bias = b2 && j >= 0 ? b2[j] : 0.0f;
-      csync();
-      float h = 0.0f;
-      if (j >= 0 && c < u.nt) {
-        float v = dot_sum(sm, P, tid) * back + bias;
-        if (a.drelu) v = relu_nan(v);
-        h = sm.first[s][(j - jb) * 8 * NG + c] * v;
-        if constexpr (!ONE) __stcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j, h);
-      }
-      if constexpr (!ONE) {
-        const unsigned any = __ballot_sync(0xffffffffu, h != 0.0f);
-        const unsigned mine = (any >> ((lane / (8 * NG)) * 8 * NG)) & ((1u << (8 * NG & 31)) - 1u);
-        if (j >= 0 && c == 0) {
-          uint8_t* f = a.nz + (size_t)u.ai * a.d_ff + j;
-          if (u.add) { if (mine) *f = 1; }
-          else *f = mine != 0;
+        csync();
+        if (tid < kBatch) {
+          // row tid of the batch (rows behind n are closed)
+          uint64_t m = 0;
+#pragma unroll
+          for (int w = 0; w < kPer * kMWarps; ++w) m |= (uint64_t)sm.mask[w] << (w * kRowsPerWarp);
+          const bool open = (m >> tid) & 1u;
+          if (open) sm.rows[s][__popcll(m & ((1ull << tid) - 1ull))] = jb + tid;
+          if (tid == 0) sm.nrows[s] = __popcll(m);
+          mbar_arrive(&sm.open[s]);
+          if constexpr (!ONE) {
+            // a closed neuron's h is 0 and is not read again: only its flag is
+            // written (unless another pass's tokens may open it)
+            if (!open && tid < n) {
+              if (!u.add) a.nz[(size_t)u.ai * a.d_ff + jb + tid] = 0;
+              if (u.keep_zeros)
+                for (int t = 0; t < u.nt; ++t) __stcg(a.h + (size_t)(u.slot0 + t) * a.d_ff + jb + tid, 0.0f);
+            }
+          }
         }
         csync();
-      } else {
-        if (c == 0) sm.hval[r] = h;
-        csync();
+        continue;
+      }
+      // second factors of the open neurons, and h
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        float h = 0.0f;
+        if (j[k] >= 0 && c < u.nt) {
+          float v = dot_sum(sm, P, tid + k * kMThreads) * back + bias[k];
+          if (a.drelu) v = relu_nan(v);
+          h = sm.first[s][(j[k] - jb) * kTok + c] * v;
+          if constexpr (!ONE) __stcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j[k], h);
+        }
+        if constexpr (!ONE) {
+          const unsigned any = __ballot_sync(0xffffffffu, h != 0.0f);
+          const unsigned mine = (any >> (lane / kTok * kTok)) & ((1u << kTok) - 1u);
+          if (j[k] >= 0 && c == 0) {
+            uint8_t* f = a.nz + (size_t)u.ai * a.d_ff + j[k];
+            if (u.add) { if (mine) *f = 1; }
+            else *f = mine != 0;
+          }
+        } else if (c == 0) {
+          sm.hval[r0 + k * kStep] = h;
+        }
+      }
+      csync();
+      if constexpr (ONE) {
         if (tid < kBatch) {
           // the neurons with h != 0, in order, and p h
           const float hv = tid < n ? sm.hval[tid] : 0.0f;
@@ -947,7 +978,7 @@ __device__ __forceinline__ void run_tokens(Smem& sm, const Run& u) {
 template <bool FP4, int KU, int NG>
 __device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingAt& at, const Run& u, int lane, int warp) {
   Smem& sm = smem();
-  float none[8];
+  float none[2][8];
   RingAt here = at;                     // in registers
   const Ring ring = R;
   const Run run = u;
@@ -964,21 +995,31 @@ __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, Rin
     each_run(a, sm, item, pass, [&](const Run& u) { send_run<FP4, ONE>(a, R, at, sm, u, lists, lane); });
     return;
   }
-  float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  float y[2][8];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[0][i] = y[1][i] = 0.0f;
+  }
   each_run(a, sm, item, pass, [&](const Run& u) {
     run_tokens(sm, u);
     if constexpr (ONE) {
-      compute_run<FP4, 8, 1, true>(a, R, at, sm, u, y, lane, warp);
+      compute_run<FP4, 16, 1, true>(a, R, at, sm, u, y, lane, warp);
     } else {
-      if (a.d_model > 4096) compute_pass<FP4, 16, 1>(a, R, at, u, lane, warp);
-      else if (u.nt <= 8) compute_pass<FP4, 8, 1>(a, R, at, u, lane, warp);
-      else compute_pass<FP4, 8, 2>(a, R, at, u, lane, warp);
+      if (a.d_model > 4096) compute_pass<FP4, 32, 1>(a, R, at, u, lane, warp);
+      else if (u.nt <= 8) compute_pass<FP4, 16, 1>(a, R, at, u, lane, warp);
+      else compute_pass<FP4, 16, 2>(a, R, at, u, lane, warp);
     }
   });
-  if (ONE && threadIdx.x * 8 < a.d_model) {
-    float* o = a.parts + (size_t)item * a.d_model + threadIdx.x * 8;
-    __stcg(reinterpret_cast<float4*>(o), make_float4(y[0], y[1], y[2], y[3]));
-    __stcg(reinterpret_cast<float4*>(o + 4), make_float4(y[4], y[5], y[6], y[7]));
+  if constexpr (ONE) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int col = v * 2048 + threadIdx.x * 8;
+      if (col < a.d_model) {
+        float* o = a.parts + (size_t)item * a.d_model + col;
+        __stcg(reinterpret_cast<float4*>(o), make_float4(y[v][0], y[v][1], y[v][2], y[v][3]));
+        __stcg(reinterpret_cast<float4*>(o + 4), make_float4(y[v][4], y[v][5], y[v][6], y[v][7]));
+      }
+    }
   }
 }
 
@@ -1058,24 +1099,22 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
       csync();
       if (works) {
         using Vec = typename std::conditional<FP4, uint2, uint4>::type;
-        auto load = [&](int st, Vec (&v)[STR][4], uint32_t (&s)[STR][4]) {
+        const int nst = np / 16;
+        auto load = [&](int st, int x, Vec (&v)[4], uint32_t (&s)[4]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int r = st * 16 + 4 * q + i;
-            const bool ok = r < n;
-            const size_t j = ok ? (size_t)(jl + sm.d.list[l0 + r]) : 0;
-#pragma unroll
-            for (int x = 0; x < STR; ++x) {
-              if constexpr (FP4) {
-                v[x][i] = ok && in[x] ? ld_w8(w + j * rb + col[x] / 2) : make_uint2(0, 0);
-                s[x][i] = ok && in[x] ? (uint32_t)__ldg(sc + j * sb + col[x] / 32) : 0u;
-              } else {
-                v[x][i] = ok && in[x] ? ld_w(w + j * rb + col[x] * 2) : make_uint4(0, 0, 0, 0);
-              }
+            const bool ok = r < n && in[x];
+            const size_t j = r < n ? (size_t)(jl + sm.d.list[l0 + r]) : 0;
+            if constexpr (FP4) {
+              v[i] = ok ? ld_w8(w + j * rb + col[x] / 2) : make_uint2(0, 0);
+              s[i] = ok ? (uint32_t)__ldg(sc + j * sb + col[x] / 32) : 0u;
+            } else {
+              v[i] = ok ? ld_w(w + j * rb + col[x] * 2) : make_uint4(0, 0, 0, 0);
             }
           }
         };
-        auto step = [&](int st, const Vec (&vv)[STR][4], const uint32_t (&ss)[STR][4]) {
+        auto step = [&](int st, Vec (&vv)[STR][4], uint32_t (&ss)[STR][4]) {
           uint2 b[NG][3];
 #pragma unroll
           for (int t = 0; t < NG; ++t)
@@ -1118,36 +1157,15 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
                    weight_pair<2>(p23, lo23, hi23, b23), weight_pair<3>(p23, lo23, hi23, b23));
             }
           }
+          if (st + 1 < nst) load(st + 1, x, vv[x], ss[x]);
           }
         };
-        const int nst = np / 16;
-        // one step ahead with two strips (their registers), two with one
-        Vec v0[STR][4], v1[STR][4];
-        uint32_t s0[STR][4], s1[STR][4];
-        load(0, v0, s0);
-        if constexpr (STR > 1) {
-          for (int st = 0; st < nst; st += 2) {
-            load(st + 1, v1, s1);
-            step(st, v0, s0);
-            if (st + 1 >= nst) break;
-            load(st + 2, v0, s0);
-            step(st + 1, v1, s1);
-          }
-        } else {
-          Vec v2[STR][4];
-          uint32_t s2[STR][4];
-          load(1, v1, s1);
-          for (int st = 0; st < nst; st += 3) {
-            load(st + 2, v2, s2);
-            step(st, v0, s0);
-            if (st + 1 >= nst) break;
-            load(st + 3, v0, s0);
-            step(st + 1, v1, s1);
-            if (st + 2 >= nst) break;
-            load(st + 4, v1, s1);
-            step(st + 2, v2, s2);
-          }
-        }
+        // a strip's next rows are asked for as soon as its registers are free
+        Vec v[STR][4];
+        uint32_t sv[STR][4];
+#pragma unroll
+        for (int x = 0; x < STR; ++x) load(0, x, v[x], sv[x]);
+        for (int st = 0; st < nst; ++st) step(st, v, sv);
       }
       csync();
     }
@@ -1173,7 +1191,7 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
 }
 
 template <bool FP4>
-constexpr int kStrips = FP4 ? 1 : 2;
+constexpr int kStrips = FP4 ? 2 : 4;
 
 // an expert's tokens in passes of up to 16: f(first slot, tokens)
 template <typename F>
@@ -1196,23 +1214,21 @@ __device__ void down_item(const MoeArgs& a, Smem& sm, int item, int A, int S, in
   const int tw = a.plan.tile_warps;
   const int strip = warp < tw ? ct * tw * kStrips<FP4> + warp : -1;
   each_pass(sm, ai, [&](int slot0, int nt) {
-    if constexpr (FP4) {
-      if (nt <= 8) down_rows<true, 1, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
-      else down_rows<true, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+    // (two groups of tokens: half of the strips after the other, their sums
+    // share the registers)
+    constexpr int kAll = kStrips<FP4>;
+    if (nt <= 8) {
+      down_rows<FP4, 1, kAll>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
     } else {
-      if (nt <= 8) {
-        down_rows<false, 1, 2>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
-      } else {      // the strips one after the other: their sums share the registers
-        down_rows<false, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
-        down_rows<false, 2, 1>(a, ai, e, slot0, nt, j0, j1, strip < 0 ? -1 : strip + tw, tw, s, lane, warp);
-      }
+      down_rows<FP4, 2, kAll / 2>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
+      down_rows<FP4, 2, kAll / 2>(a, ai, e, slot0, nt, j0, j1, strip < 0 ? -1 : strip + kAll / 2 * tw, tw, s, lane, warp);
     }
   });
 }
 
 // ---- sums ----------------------------------------------------------------------
-// 16 vectors of 4 outputs per item; 32 threads share the partial sums of each
-// (every 32nd in turn), so that their loads are all in flight at once
+// 16 vectors of 4 outputs per item; 16 threads share the partial sums of each
+// (every 16th in turn), so that their loads are all in flight at once
 __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
   const int n4 = a.d_model / 4, tid = threadIdx.x, vec = tid & 15, part = tid >> 4;
   for (long long i0 = (long long)item * 16; i0 < (long long)a.T * n4; i0 += (long long)a.plan.out_items * 16) {
@@ -1225,14 +1241,14 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
     if (a.plan.one_token) {
       const float* src = a.parts + c;
 #pragma unroll 8
-      for (int s = part; s < a.plan.hidden_items; s += 32) {
+      for (int s = part; s < a.plan.hidden_items; s += 16) {
         const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * a.d_model));
         y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
       }
     } else {
       const int n = a.top_k * S;
 #pragma unroll 4
-      for (int k = part; k < n; k += 32) {
+      for (int k = part; k < n; k += 16) {
         const int j = k / S, s = k - j * S;
         const float p = sm.share[t * a.top_k + j];
         const float4 u = __ldcg(reinterpret_cast<const float4*>(
@@ -1246,7 +1262,7 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
   red[tid] = y;
   csync();
   if (part == 0 && ok) {
-    for (int k = 1; k < 32; ++k) {
+    for (int k = 1; k < 16; ++k) {
       const float4 u = red[k * 16 + vec];
       y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
     }
