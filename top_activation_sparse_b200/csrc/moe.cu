@@ -86,8 +86,10 @@ struct Smem {
   int tok[8 * kMaxNg];                           // the pass's tokens (-1: none)
   int scan[kMWarps];
   int item, last, abort;
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t open[2], down[2];                     // lists of rows ready for the copying warp
+  uint64_t full[kMaxStages], empty[kMaxStages], dfull[kMaxStages], dempty[kMaxStages];
+  // lists of rows: written for the copying warp, read by it (0, 1: open neurons;
+  // 2, 3: down rows)
+  uint64_t listed[4], taken[4];
 };
 static_assert(sizeof(Smem) <= 227 * 1024 - 1024, "shared memory");
 
@@ -101,18 +103,6 @@ __device__ __forceinline__ Smem& smem() {
 // the computing warps' barrier
 __device__ __forceinline__ void csync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__device__ __forceinline__ uint4 ld_w(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint2 ld_w8(const uint8_t* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
 __device__ __forceinline__ uint4 ld_x(const __nv_bfloat16* p) {
   uint4 r;
   asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -291,6 +281,7 @@ __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logit
       uint64_t key = 0;                       // order, then the lower expert
 #pragma unroll
       for (int i = 0; i < kMoeMaxE / 32; ++i) {
+        if (32 * i >= a.E) break;
         const int e = lane + 32 * i;
         if (e < a.E && !((taken >> i) & 1u)) {
           const uint64_t k = ((uint64_t)order_key(v[i]) << 32) | (uint32_t)(kMoeMaxE - e);
@@ -331,6 +322,7 @@ __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logit
   // thread e: its tokens in order; experts without tokens drop out
   int cnt = 0;
   if (e < a.E)
+#pragma unroll 8
     for (int i = 0; i < n; ++i) cnt += sm.sel[i] == e;
   const int act = cnt > 0;
   // sums over the experts: (active experts, slots), both below 2^16
@@ -399,44 +391,30 @@ __device__ void fetch_routing(const MoeArgs& a, Smem& sm) {
   csync();
 }
 
-// Local routing: few tokens and a small router (at most 128 KB, from L2), which
-// every CTA evaluates for itself: less time than handing the result over.  A
-// warp's task is four (expert, token) pairs, whose loads overlap, over a slice
-// of d_model where there are few pairs.
+// Local routing: at most 8 tokens and a small router (at most 64 experts and 128
+// KB, from L2), which every CTA evaluates for itself: less time than handing
+// the result over.  The warps share d_model; 16 experts x 8 tokens per matrix
+// instruction.
 __device__ __noinline__ void route_here(const MoeArgs& a, bool publish, int lane, int warp) {
   Smem& sm = smem();
-  const int pairs = a.E * a.T, quads = (pairs + 3) / 4;
-  const int slices = quads >= kMWarps ? 1 : min(8, kMWarps / quads);
-  float* part = sm.red;                             // [slices][pairs], at most 2048
-  for (int task = warp; task < quads * slices; task += kMWarps) {
-    const int i0 = (task % quads) * 4, slice = task / quads;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const __nv_bfloat16 *pw[4], *px[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = min(i0 + i, pairs - 1);
-      pw[i] = a.router + (size_t)(at % a.E) * a.d_model;
-      px[i] = a.x + (size_t)(at / a.E) * a.d_model;
+  const int g = lane >> 2, q = lane & 3, units = a.d_model / 32, pairs = a.E * a.T;
+  float* part = sm.red;                             // [warp][expert][8 tokens]: 64 x 8 x 8 at most
+  for (int e0 = 0; e0 < a.E; e0 += 16) {
+    const bool ok0 = e0 + g < a.E, ok1 = e0 + 8 + g < a.E;
+    const __nv_bfloat16* w0 = a.router + (size_t)(ok0 ? e0 + g : 0) * a.d_model + q * 8;
+    const __nv_bfloat16* w1 = a.router + (size_t)(ok1 ? e0 + 8 + g : 0) * a.d_model + q * 8;
+    const __nv_bfloat16* x = a.x + (size_t)(g < a.T ? g : 0) * a.d_model + q * 8;
+    float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int u = warp; u < units; u += kMWarps) {
+      const uint4 v0 = ok0 ? ld_x(w0 + u * 32) : z, v1 = ok1 ? ld_x(w1 + u * 32) : z, b = g < a.T ? ld_x(x + u * 32) : z;
+      mma_bf16(acc[0], v0.x, v1.x, v0.y, v1.y, b.x, b.y);
+      mma_bf16(acc[1], v0.z, v1.z, v0.w, v1.w, b.z, b.w);
     }
-#pragma unroll 2
-    for (int k = slice * 256 + lane * 8; k < a.d_model; k += 256 * slices) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 w = ld_x(pw[i] + k), x = ld_x(px[i] + k);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, xx[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          v[i] = fmaf(bf16lo(ww[c]), bf16lo(xx[c]), v[i]);
-          v[i] = fmaf(bf16hi(ww[c]), bf16hi(xx[c]), v[i]);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-      if (lane == 0 && i0 + i < pairs) part[slice * pairs + i0 + i] = v[i];
-    }
+    float* o = part + warp * 512 + (e0 + g) * 8 + 2 * q;
+    *reinterpret_cast<float2*>(o) = make_float2(acc[0][0] + acc[1][0], acc[0][1] + acc[1][1]);
+    *reinterpret_cast<float2*>(o + 64) = make_float2(acc[0][2] + acc[1][2], acc[0][3] + acc[1][3]);
   }
   if (a.fp4)
     for (int t = warp; t < a.T; t += kMWarps) {
@@ -444,9 +422,18 @@ __device__ __noinline__ void route_here(const MoeArgs& a, bool publish, int lane
       if (lane == 0) sm.xup[t] = u;
     }
   csync();
-  // [T, E]; each place is read and written by one thread
-  for (int i = threadIdx.x; i < pairs && slices > 1; i += kMThreads)
-    for (int k = 1; k < slices; ++k) part[i] += part[k * pairs + i];
+  float v[2] = {0.0f, 0.0f};                        // pairs <= 512
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = threadIdx.x + k * kMThreads;      // token i / E, expert i % E
+    if (i < pairs)
+#pragma unroll
+      for (int w = 0; w < kMWarps; ++w) v[k] += part[w * 512 + (i % a.E) * 8 + i / a.E];
+  }
+  csync();
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if ((int)threadIdx.x + k * kMThreads < pairs) part[threadIdx.x + k * kMThreads] = v[k];
   csync();
   select_experts<true>(a, part, publish, lane, warp);
 }
@@ -466,10 +453,32 @@ struct Ring {
 struct RingAt {
   int sl = 0, issued = 0;
   uint32_t ph = 0;
-  __device__ __forceinline__ void next(const Ring& R) {
-    if (++sl == R.stages) sl = 0, ph ^= 1u;
+  uint32_t lists = 0;                    // phases of the lists' barriers (the hidden layer's place keeps them)
+  __device__ __forceinline__ void next(const Ring& R) { next(R.stages); }
+  __device__ __forceinline__ void next(int stages) {
+    if (++sl == stages) sl = 0, ph ^= 1u;
   }
+
 };
+
+// A list changes hands both ways: it is written again only after the copying
+// warp has read it (a list may be empty, and then nothing else holds the
+// computing warps back).
+__device__ __forceinline__ void list_free(Smem& sm, const RingAt& at, int i, DevStatus* st) {
+  ring_wait(&sm.taken[i], ((at.lists >> i) & 1u) ^ 1u, sm, st, 82);
+}
+__device__ __forceinline__ void list_written(Smem& sm, RingAt& at, int i) {     // computing warps
+  if (threadIdx.x < kBatch) mbar_arrive(&sm.listed[i]);
+  at.lists ^= 1u << i;
+}
+__device__ __forceinline__ void list_wait(Smem& sm, const RingAt& at, int i, DevStatus* st) {
+  ring_wait(&sm.listed[i], (at.lists >> i) & 1u, sm, st, 77);
+}
+__device__ __forceinline__ void list_taken(Smem& sm, RingAt& at, int i, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.taken[i]);
+  at.lists ^= 1u << i;
+}
 
 // the copying warp: rows list[0..n), or j0 + i without a list, of matrix w
 __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, DevStatus* st, const uint8_t* w, const uint8_t* sc,
@@ -774,7 +783,7 @@ __device__ __forceinline__ ExpertMats expert_mats(const MoeArgs& a, int e) {
 }
 
 template <bool FP4, bool ONE>
-__device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u, uint32_t& lists, int lane) {
+__device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u, int lane) {
   const ExpertMats M = expert_mats<FP4>(a, u.e);
   const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
@@ -784,15 +793,15 @@ __device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, 
     }
     if (b >= 1 && b - 1 < nb) {
       const int s = (b - 1) & 1;
-      ring_wait(&sm.open[s], (lists >> s) & 1u, sm, a.status, 77);
-      lists ^= 1u << s;
+      list_wait(sm, at, s, a.status);
       send_rows(R, at, sm, a.status, M.w2, M.s2, sm.rows[s], 0, *(volatile int*)&sm.nrows[s], lane);
+      list_taken(sm, at, s, lane);
     }
     if (ONE && b >= 2) {
       const int s = b & 1;
-      ring_wait(&sm.down[s], (lists >> (2 + s)) & 1u, sm, a.status, 78);
-      lists ^= 4u << s;
+      list_wait(sm, at, 2 + s, a.status);
       send_rows(R, at, sm, a.status, M.wd, M.sd, sm.drows[s], 0, *(volatile int*)&sm.ndrows[s], lane);
+      list_taken(sm, at, 2 + s, lane);
     }
   }
 }
@@ -864,6 +873,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
           }
         }
         csync();
+        list_free(sm, at, s, a.status);
         if (tid < kBatch) {
           // row tid of the batch (rows behind n are closed)
           uint64_t m = 0;
@@ -872,7 +882,6 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
           const bool open = (m >> tid) & 1u;
           if (open) sm.rows[s][__popcll(m & ((1ull << tid) - 1ull))] = jb + tid;
           if (tid == 0) sm.nrows[s] = __popcll(m);
-          mbar_arrive(&sm.open[s]);
           if constexpr (!ONE) {
             // a closed neuron's h is 0 and is not read again: only its flag is
             // written (unless another pass's tokens may open it)
@@ -883,6 +892,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
             }
           }
         }
+        list_written(sm, at, s);
         csync();
         continue;
       }
@@ -910,6 +920,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
       }
       csync();
       if constexpr (ONE) {
+        list_free(sm, at, 2 + s, a.status);
         if (tid < kBatch) {
           // the neurons with h != 0, in order, and p h
           const float hv = tid < n ? sm.hval[tid] : 0.0f;
@@ -922,8 +933,8 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
             sm.dval[s][at2] = hv * share;
           }
           if (tid == 0) sm.ndrows[s] = sm.scan[0] + sm.scan[1];
-          mbar_arrive(&sm.down[s]);
         }
+        list_written(sm, at, 2 + s);
         csync();
       }
     }
@@ -957,7 +968,9 @@ __device__ __forceinline__ void each_run(const MoeArgs& a, const Smem& sm, int i
         v.j1 = min(end, j + step);
         v.slot0 = first + t0;
         v.nt = min(pass, cnt - t0);
-        v.batch = v.nt > 8 ? kBatch / 2 : kBatch;
+        // batches of about the same size, whole tiles of 16
+        const int most = v.nt > 8 ? kBatch / 2 : kBatch, n = v.j1 - v.j0, nb = (n + most - 1) / most;
+        v.batch = min(most, ((n + nb - 1) / nb + 15) / 16 * 16);
         v.add = t0 > 0;
         v.keep_zeros = cnt > pass;
         f(v);
@@ -987,12 +1000,12 @@ __device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingA
 }
 
 template <bool FP4, bool ONE>
-__device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, int item, uint32_t& lists,
-                                            int lane, int warp) {
+__device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, int item, int lane,
+                                            int warp) {
   // tokens per pass: two groups of 8 where x of both fits the registers
   const int pass = a.d_model <= 4096 ? 16 : 8;
   if (warp == kMWarps) {
-    each_run(a, sm, item, pass, [&](const Run& u) { send_run<FP4, ONE>(a, R, at, sm, u, lists, lane); });
+    each_run(a, sm, item, pass, [&](const Run& u) { send_run<FP4, ONE>(a, R, at, sm, u, lane); });
     return;
   }
   float y[2][8];
@@ -1024,31 +1037,90 @@ __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, Rin
 }
 
 // ---- down projection ---------------------------------------------------------
-// a strip of 64 (bf16) or 128 (4-bit) columns per warp; the CTA's flagged
-// neurons of [j0, j1) are listed once and their h staged as three bf16 parts
+// Item: (expert, column tile, range of neurons).  The range's flagged neurons
+// are listed, 2048 neurons at a time; the tile's piece of their down rows comes
+// through the ring 16 neurons per stage (one step of the matrix instructions);
+// their h is staged as three bf16 numbers, 128 neurons at a time.  A warp has
+// STR strips of 64 columns (4-bit weights: 128), every eighth of the tile.
+struct DownItem {
+  int ai, e, ct, s, j0, j1, c0, cw;      // columns [c0, c0 + cw)
+};
+// Its stages are others than the hidden layer's, in the same memory, with
+// barriers of their own (an item begins and ends with every stage free).
+struct DownRing {
+  int pb, sb;                            // bytes of a piece, of its scales (0: not in the ring)
+  int pitch, stages;
+};
+constexpr int kRowsStage = 16;
+
+template <bool FP4>
+__device__ __forceinline__ DownItem down_place(const MoeArgs& a, const Smem& sm, int item, int S) {
+  DownItem d;
+  d.ct = item % a.plan.col_tiles;
+  const int rest = item / a.plan.col_tiles;
+  d.s = rest % S;
+  d.ai = rest / S;
+  d.e = sm.expert[d.ai];
+  // whole groups of 8 neurons (their flags are read 8 at a time)
+  d.j0 = (int)((long long)(a.d_ff / 8) * d.s / S) * 8;
+  d.j1 = (int)((long long)(a.d_ff / 8) * (d.s + 1) / S) * 8;
+  d.c0 = d.ct * a.plan.tile_cols;
+  d.cw = min(a.plan.tile_cols, a.d_model - d.c0);
+  return d;
+}
+template <bool FP4>
+__device__ __forceinline__ DownRing down_ring(const MoeArgs& a, const DownItem& d) {
+  DownRing r;
+  r.pb = FP4 ? d.cw / 2 : d.cw * 2;
+  r.sb = FP4 && a.plan.scale_bytes && d.cw % 512 == 0 && d.c0 % 512 == 0 ? d.cw / 32 : 0;
+  r.pitch = a.plan.down_pitch;
+  r.stages = a.plan.down_stages;
+  return r;
+}
+
+template <bool FP4>
+__device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem& d, int passes, int lane) {
+  const DownRing R = down_ring<FP4>(a, d);
+  const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;
+  const uint8_t* w = a.wd + (size_t)d.e * a.d_ff * rb + (FP4 ? d.c0 / 2 : d.c0 * 2);
+  const uint8_t* sc = FP4 ? a.sd + (size_t)d.e * a.d_ff * (a.d_model / 32) + d.c0 / 32 : nullptr;
+  for (int p = 0; p < passes; ++p)
+    for (int jl = d.j0; jl < d.j1; jl += kListD) {
+      list_wait(sm, at, 2, a.status);
+      const int total = *(volatile int*)&sm.ndrows[0];
+      for (int i0 = 0; i0 < total; i0 += kRowsStage) {
+        const int nr = min(kRowsStage, total - i0);
+        const bool ok = ring_wait(&sm.dempty[at.sl], at.ph ^ 1u, sm, a.status, 80);
+        if (__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) mbar_arrive_expect_tx(&sm.dfull[at.sl], (uint32_t)(nr * (R.pb + R.sb)));
+          __syncwarp();
+          unsigned char* dst = sm.ring + (size_t)at.sl * kRowsStage * R.pitch;
+          if (lane < nr) {
+            const size_t j = (size_t)(jl + sm.d.list[i0 + lane]);
+            bulk_g2s(dst + lane * R.pitch, w + j * rb, (uint32_t)R.pb, &sm.dfull[at.sl]);
+            if (R.sb) bulk_g2s(dst + lane * R.pitch + R.pb, sc + j * (a.d_model / 32), (uint32_t)R.sb, &sm.dfull[at.sl]);
+          }
+          ++at.issued;
+        }
+        at.next(R.stages);
+      }
+      list_taken(sm, at, 2, lane);
+    }
+}
+
 template <bool FP4, int NG, int STR>
-__device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot0, int nt, int j0, int j1, int strip, int gap,
-                          int split, int lane, int warp) {
+__device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const DownItem& d_, int slot0, int nt, int lane, int warp) {
   Smem& sm = smem();
+  RingAt at = at_;
+  const DownItem d = d_;
+  const DownRing R = down_ring<FP4>(a, d);
   constexpr int kCols = FP4 ? 16 : 8;                // columns of a lane
   constexpr int kMma = kCols / 2;                    // MMAs per 16 neurons and token group
   const int g = lane >> 2, q = lane & 3, tid = threadIdx.x;
-  // the matrix instructions need whole warps: a strip takes part when its first
-  // column exists, a lane loads and stores when its own do (d_model is a
-  // multiple of 32, a lane's columns divide that)
-  const bool works = strip >= 0 && strip * (8 * kCols) < a.d_model;
   int col[STR];
-  bool in[STR];
 #pragma unroll
-  for (int x = 0; x < STR; ++x) {
-    col[x] = (strip + x * gap) * (8 * kCols) + g * kCols;
-    in[x] = works && col[x] < a.d_model;
-    if (!in[x]) col[x] = 0;
-  }
-  const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;
-  const int sb = a.d_model / 32;
-  const uint8_t* w = a.wd + (size_t)e * a.d_ff * rb;
-  const uint8_t* sc = FP4 ? a.sd + (size_t)e * a.d_ff * sb : nullptr;
+  for (int x = 0; x < STR; ++x) col[x] = (x * kMWarps + warp) * (8 * kCols) + g * kCols;
+  const uint8_t* sc = FP4 ? a.sd + (size_t)d.e * a.d_ff * (a.d_model / 32) + d.c0 / 32 : nullptr;
   float acc[STR][kMma][NG][4];
 #pragma unroll
   for (int x = 0; x < STR; ++x)
@@ -1059,89 +1131,101 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[x][m][n][i] = 0.0f;
 
-  for (int jl = j0; jl < j1; jl += kListD) {
-    // list the flagged neurons of [jl, je), in order
-    const int je = min(j1, jl + kListD);
-    int total = 0;
-    csync();
-    for (int jb = jl; jb < je; jb += kMThreads) {
-      const int j = jb + tid;
-      const bool f = j < je && __ldcg(a.nz + (size_t)ai * a.d_ff + j) != 0;
-      const unsigned m = __ballot_sync(0xffffffffu, f);
-      if (lane == 0) sm.scan[warp] = __popc(m);
-      csync();
-      int at = total, sum = 0;
+  for (int jl = d.j0; jl < d.j1; jl += kListD) {
+    // list the flagged neurons of this round, in order: 8 flags per thread
+    const int jt = jl + tid * 8;
+    uint2 f8 = make_uint2(0, 0);
+    if (jt < min(d.j1, jl + kListD)) f8 = __ldcg(reinterpret_cast<const uint2*>(a.nz + (size_t)d.ai * a.d_ff + jt));
+    uint32_t bits8 = 0;
 #pragma unroll
-      for (int v = 0; v < kMWarps; ++v) {
-        if (v < warp) at += sm.scan[v];
-        sum += sm.scan[v];
-      }
-      if (f) sm.d.list[at + __popc(m & lanemask_lt())] = (uint16_t)(j - jl);
-      total += sum;
-      csync();
+    for (int i = 0; i < 8; ++i) bits8 |= (((i < 4 ? f8.x : f8.y) >> (8 * (i & 3))) & 1u) << i;
+    const int cnt = __popc(bits8);
+    int inc = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
     }
+    list_free(sm, at, 2, a.status);
+    csync();                                         // the previous round's list and h are read
+    if (lane == 31) sm.scan[warp] = inc;
+    csync();
+    int at2 = inc - cnt, total = 0;
+#pragma unroll
+    for (int v = 0; v < kMWarps; ++v) {
+      if (v < warp) at2 += sm.scan[v];
+      total += sm.scan[v];
+    }
+    for (uint32_t m = bits8; m; m &= m - 1u) sm.d.list[at2++] = (uint16_t)(tid * 8 + __ffs((int)m) - 1);
+    if (tid == 0) sm.ndrows[0] = total;
+    csync();
+    list_written(sm, at, 2);
     for (int l0 = 0; l0 < total; l0 += kRowsD) {
       const int n = min(kRowsD, total - l0), np = (n + 15) & ~15;
-      // h of these neurons as three bf16 numbers
+      if (l0) csync();                               // the previous neurons' h is read
+      // h of these neurons as three bf16 numbers; neuron r of a step of 16 is
+      // lane quarter r % 4's r / 4-th
       for (int i = tid; i < np * 8 * NG; i += kMThreads) {
         const int r = i % np, c = i / np;
         float h = 0.0f;
         if (r < n && c < nt) h = __ldcg(a.h + (size_t)(slot0 + c) * a.d_ff + jl + sm.d.list[l0 + r]);
         // (an infinity or a NaN has no rest)
         const bool finite = fabsf(h) <= 3.0e38f;
+        const int to = c * kHPitch + (r & ~15) + (r & 3) * 4 + ((r & 15) >> 2);
 #pragma unroll
         for (int v = 0; v < 3; ++v) {
           const __nv_bfloat16 b = __float2bfloat16_rn(h);
-          sm.d.h[v][c * kHPitch + r] = b;
+          sm.d.h[v][to] = b;
           h = finite ? h - __bfloat162float(b) : 0.0f;
         }
       }
       csync();
-      if (works) {
-        using Vec = typename std::conditional<FP4, uint2, uint4>::type;
-        const int nst = np / 16;
-        auto load = [&](int st, int x, Vec (&v)[4], uint32_t (&s)[4]) {
+      for (int st = 0; st < np / 16; ++st) {
+        const int nr = min(kRowsStage, n - st * 16);
+        ring_wait(&sm.dfull[at.sl], at.ph, sm, a.status, 81);
+        const unsigned char* stage = sm.ring + (size_t)at.sl * kRowsStage * R.pitch;
+        // this lane's rows 4 i + q (rows that the stage does not have repeat the
+        // first: their h is 0)
+        const unsigned char* row[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = st * 16 + 4 * q + i;
-            const bool ok = r < n && in[x];
-            const size_t j = r < n ? (size_t)(jl + sm.d.list[l0 + r]) : 0;
-            if constexpr (FP4) {
-              v[i] = ok ? ld_w8(w + j * rb + col[x] / 2) : make_uint2(0, 0);
-              s[i] = ok ? (uint32_t)__ldg(sc + j * sb + col[x] / 32) : 0u;
-            } else {
-              v[i] = ok ? ld_w(w + j * rb + col[x] * 2) : make_uint4(0, 0, 0, 0);
-            }
-          }
-        };
-        auto step = [&](int st, Vec (&vv)[STR][4], uint32_t (&ss)[STR][4]) {
-          uint2 b[NG][3];
+        for (int i = 0; i < 4; ++i) row[i] = stage + (4 * i + q < nr ? 4 * i + q : 0) * R.pitch;
+        uint2 b[NG][3];
 #pragma unroll
-          for (int t = 0; t < NG; ++t)
+        for (int t = 0; t < NG; ++t)
 #pragma unroll
-            for (int v = 0; v < 3; ++v)
-              b[t][v] = *reinterpret_cast<const uint2*>(sm.d.h[v] + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
+          for (int v = 0; v < 3; ++v)
+            b[t][v] = *reinterpret_cast<const uint2*>(sm.d.h[v] + (t * 8 + g) * kHPitch + st * 16 + 4 * q);
 #pragma unroll
-          for (int x = 0; x < STR; ++x) {
-          const Vec (&v)[4] = vv[x];
-          const uint32_t (&s)[4] = ss[x];
+        for (int x = 0; x < STR; ++x) {
+          if ((x * kMWarps + warp) * (8 * kCols) >= d.cw) break;          // whole warps: the strip does not exist
+          const int cl = col[x] < d.cw ? col[x] : 0;
           auto mmas = [&](int m, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-            for (int t = 0; t < NG; ++t) {
+            for (int t = 0; t < NG; ++t)
 #pragma unroll
               for (int v = 0; v < 3; ++v) mma_bf16(acc[x][m][t], a0, a1, a2, a3, b[t][v].x, b[t][v].y);
-            }
           };
           if constexpr (!FP4) {
-            const uint32_t* u0 = reinterpret_cast<const uint32_t*>(&v[0]);
-            const uint32_t* u1 = reinterpret_cast<const uint32_t*>(&v[1]);
-            const uint32_t* u2 = reinterpret_cast<const uint32_t*>(&v[2]);
-            const uint32_t* u3 = reinterpret_cast<const uint32_t*>(&v[3]);
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(row[i] + cl * 2);
+            const uint32_t* u0 = reinterpret_cast<const uint32_t*>(&u[0]);
+            const uint32_t* u1 = reinterpret_cast<const uint32_t*>(&u[1]);
+            const uint32_t* u2 = reinterpret_cast<const uint32_t*>(&u[2]);
+            const uint32_t* u3 = reinterpret_cast<const uint32_t*>(&u[3]);
 #pragma unroll
             for (int m = 0; m < kMma; ++m)
               mmas(m, __byte_perm(u0[m], u1[m], 0x5410), __byte_perm(u0[m], u1[m], 0x7632),
                    __byte_perm(u2[m], u3[m], 0x5410), __byte_perm(u2[m], u3[m], 0x7632));
           } else {
+            uint2 v[4];
+            uint32_t s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[i] = *reinterpret_cast<const uint2*>(row[i] + cl / 2);
+              s[i] = R.sb ? row[i][R.pb + cl / 32]
+                          : __ldg(sc + (size_t)(jl + sm.d.list[l0 + st * 16 + (4 * i + q < nr ? 4 * i + q : 0)]) * (a.d_model / 32) + cl / 32);
+            }
             // pairs of neurons (0, 1) and (2, 3), one code of each per half
             const uint32_t lo01 = scale_lo(s[0]) | (scale_lo(s[1]) << 16), lo23 = scale_lo(s[2]) | (scale_lo(s[3]) << 16);
             const uint32_t hi01 = scale_hi(s[0]) | (scale_hi(s[1]) << 16), hi23 = scale_hi(s[2]) | (scale_hi(s[3]) << 16);
@@ -1157,30 +1241,24 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
                    weight_pair<2>(p23, lo23, hi23, b23), weight_pair<3>(p23, lo23, hi23, b23));
             }
           }
-          if (st + 1 < nst) load(st + 1, x, vv[x], ss[x]);
-          }
-        };
-        // a strip's next rows are asked for as soon as its registers are free
-        Vec v[STR][4];
-        uint32_t sv[STR][4];
-#pragma unroll
-        for (int x = 0; x < STR; ++x) load(0, x, v[x], sv[x]);
-        for (int st = 0; st < nst; ++st) step(st, v, sv);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.dempty[at.sl]);
+        at.next(R.stages);
       }
-      csync();
     }
   }
   const size_t slots = (size_t)a.T * a.top_k;
 #pragma unroll
   for (int x = 0; x < STR; ++x) {
-    if (!in[x]) continue;
+    if (col[x] >= d.cw) continue;
 #pragma unroll
     for (int t = 0; t < NG; ++t)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int n = t * 8 + 2 * q + c;
         if (n < nt) {
-          float* o = a.parts + ((size_t)split * slots + slot0 + n) * a.d_model + col[x];
+          float* o = a.parts + ((size_t)d.s * slots + slot0 + n) * a.d_model + d.c0 + col[x];
 #pragma unroll
           for (int m = 0; m < kMma; m += 2)
             __stcg(reinterpret_cast<float4*>(o + 2 * m),
@@ -1188,17 +1266,13 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, int ai, int e, int slot
         }
       }
   }
+  at_ = at;
 }
 
+// strips per warp: with at most 8 tokens their sums take 64 registers, with 16
+// (bf16; the 4-bit form takes 8 tokens at a time) half the strips do
 template <bool FP4>
 constexpr int kStrips = FP4 ? 2 : 4;
-
-// an expert's tokens in passes of up to 16: f(first slot, tokens)
-template <typename F>
-__device__ __forceinline__ void each_pass(const Smem& sm, int ai, F&& f) {
-  const int first = sm.firsts[ai], cnt = sm.count[ai];
-  for (int t0 = 0; t0 < cnt; t0 += 8 * kMaxNg) f(first + t0, min(8 * kMaxNg, cnt - t0));
-}
 
 // splits of an expert's neurons: about one item per CTA in all
 __device__ __forceinline__ int down_splits(const MoeArgs& a, int A) {
@@ -1207,23 +1281,19 @@ __device__ __forceinline__ int down_splits(const MoeArgs& a, int A) {
 }
 
 template <bool FP4>
-__device__ void down_item(const MoeArgs& a, Smem& sm, int item, int A, int S, int lane, int warp) {
-  const int ct = item % a.plan.col_tiles, rest = item / a.plan.col_tiles, s = rest % S, ai = rest / S;
-  const int e = sm.expert[ai];
-  const int j0 = (int)((long long)a.d_ff * s / S), j1 = (int)((long long)a.d_ff * (s + 1) / S);
-  const int tw = a.plan.tile_warps;
-  const int strip = warp < tw ? ct * tw * kStrips<FP4> + warp : -1;
-  each_pass(sm, ai, [&](int slot0, int nt) {
-    // (two groups of tokens: half of the strips after the other, their sums
-    // share the registers)
-    constexpr int kAll = kStrips<FP4>;
-    if (nt <= 8) {
-      down_rows<FP4, 1, kAll>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
-    } else {
-      down_rows<FP4, 2, kAll / 2>(a, ai, e, slot0, nt, j0, j1, strip, tw, s, lane, warp);
-      down_rows<FP4, 2, kAll / 2>(a, ai, e, slot0, nt, j0, j1, strip < 0 ? -1 : strip + kAll / 2 * tw, tw, s, lane, warp);
-    }
-  });
+__device__ void down_item(const MoeArgs& a, RingAt& at, Smem& sm, int item, int S, int lane, int warp) {
+  const DownItem d = down_place<FP4>(a, sm, item, S);
+  const int first = sm.firsts[d.ai], cnt = sm.count[d.ai], pass = a.plan.down_tokens;
+  if (warp == kMWarps) {
+    send_down<FP4>(a, at, sm, d, (cnt + pass - 1) / pass, lane);
+    return;
+  }
+  for (int t0 = 0; t0 < cnt; t0 += pass) {
+    const int nt = min(pass, cnt - t0);
+    if (FP4 || pass == 8) down_rows<FP4, 1, kStrips<FP4>>(a, at, d, first + t0, nt, lane, warp);
+    else if (nt <= 8) down_rows<FP4, 1, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
+    else down_rows<FP4, 2, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
+  }
 }
 
 // ---- sums ----------------------------------------------------------------------
@@ -1286,16 +1356,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const bool computes = warp < kMWarps;
   const MoePlan& P = a.plan;
   const Ring R{P.row_bytes, P.scale_bytes, P.pitch, P.stage_rows, P.stages};
-  RingAt at;
-  uint32_t lists = 0;                   // the copying warp: phases of the lists' barriers
+  RingAt at, atd;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R.stages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], kMWarps);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.open[i], kBatch);
-      mbar_init(&sm.down[i], kBatch);
+    for (int i = 0; i < P.down_stages; ++i) {
+      mbar_init(&sm.dfull[i], 1);
+      mbar_init(&sm.dempty[i], kMWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.listed[i], kBatch);
+      mbar_init(&sm.taken[i], 1);
     }
     mbar_fence_init();
     sm.abort = 0;
@@ -1348,15 +1421,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         }
       }
       if (i < P.hidden_items) {
-        hidden_item<FP4, ONE>(a, R, at, sm, i, lists, lane, warp);
+        hidden_item<FP4, ONE>(a, R, at, sm, i, lane, warp);
         if (computes) finish(a.ctl + MC_HIDDEN, sm);
       } else if ((i -= P.hidden_items) < nD) {
         if constexpr (!ONE) {
-          if (computes) {
-            wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
-            down_item<FP4>(a, sm, i, sm.active, S, lane, warp);
-            finish(a.ctl + MC_DOWN, sm);
-          }
+          if (computes) wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
+          // (the copying warp waits for the first list of rows)
+          down_item<FP4>(a, atd, sm, i, S, lane, warp);
+          if (computes) finish(a.ctl + MC_DOWN, sm);
         }
       } else if ((i -= nD) < P.out_items) {
         if (computes) {
@@ -1374,11 +1446,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
     __syncthreads();
   }
   // after a wait that gave up, copies may still be in flight
-  if (warp == kMWarps && lane == 0 && *(volatile int*)&sm.abort)
+  if (warp == kMWarps && lane == 0 && *(volatile int*)&sm.abort) {
     for (int k = 1; k <= R.stages && k <= at.issued; ++k) {
       const int g = at.issued - k;
       mbar_wait(&sm.full[g % R.stages], (uint32_t)(g / R.stages) & 1u);
     }
+    for (int k = 1; k <= P.down_stages && k <= atd.issued; ++k) {
+      const int g = atd.issued - k;
+      mbar_wait(&sm.dfull[g % P.down_stages], (uint32_t)(g / P.down_stages) & 1u);
+    }
+  }
   // the last CTA to leave clears the counters for the next call
   if (threadIdx.x == 0) {
     __threadfence();
@@ -1393,7 +1470,7 @@ MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4
   (void)d_ff;
   MoePlan p;
   p.grid = kNumSMs;
-  p.local = T <= 32 && n_experts <= 64 && n_experts * d_model <= 65536 && T * n_experts * d_model <= kMoeLocalWork;
+  p.local = T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
   p.x_items = (!p.local && fp4) ? (T + kMWarps - 1) / kMWarps : 0;
   p.router_tokens = (long)T * n_experts <= kNumSMs * kMWarps ? 1 : 4;
   p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
@@ -1411,9 +1488,16 @@ MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4
   if (p.stage_rows > 8) p.stage_rows = p.stage_rows > 64 ? 64 : p.stage_rows / 8 * 8;
   p.stages = kRing / (p.stage_rows * p.pitch);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int strips = (d_model + (fp4 ? 127 : 63)) / (fp4 ? 128 : 64), per = fp4 ? kStrips<true> : kStrips<false>;
-  p.col_tiles = (strips + kMWarps * per - 1) / (kMWarps * per);
-  p.tile_warps = (strips + p.col_tiles * per - 1) / (p.col_tiles * per);
+  // the down projection: tiles of up to 8 warps' strips
+  p.down_tokens = fp4 || T <= 8 ? 8 : 16;
+  const int strips = fp4 ? kStrips<true> : (p.down_tokens == 8 ? kStrips<false> : kStrips<false> / 2);
+  p.tile_cols = kMWarps * strips * (fp4 ? 128 : 64);
+  if (p.tile_cols > d_model) p.tile_cols = d_model;
+  p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
+  // 32 mod 128: four rows' loads do not meet in a bank
+  p.down_pitch = ((fp4 ? p.tile_cols / 2 + p.tile_cols / 32 : p.tile_cols * 2) + 95) / 128 * 128 + 32;
+  p.down_stages = kRing / (kRowsStage * p.down_pitch);
+  if (p.down_stages > kMaxStages) p.down_stages = kMaxStages;
   const long vecs = ((long)T * (d_model / 4) + 15) / 16;
   p.out_items = (int)(vecs < p.grid ? vecs : p.grid);
   p.max_splits = kMoePartRows / (T * top_k);

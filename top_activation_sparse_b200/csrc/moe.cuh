@@ -6,7 +6,6 @@
 namespace qs {
 
 constexpr int kMoeMaxT = 64;          // tokens per launch
-constexpr int kMoeLocalWork = 524288; // local routing: products that each CTA does for itself
 constexpr int kMoeMaxModel = QS_MOE_MAX_MODEL;
 constexpr int kMoePartRows = 1024;    // rows of partial sums (splits x tokens x experts per token)
 
@@ -23,7 +22,9 @@ struct MoePlan {
   int hidden_items = 0;     // ... of the hidden layer
   int out_items = 0;        // ... of the final sums
   int col_tiles = 0;        // column tiles of the down projection
-  int tile_warps = 0;       // warps of a tile (each one or two strips of columns)
+  int tile_cols = 0;        // ... of this many columns
+  int down_tokens = 0;      // tokens per pass of the down projection
+  int down_pitch = 0, down_stages = 0;
   int row_bytes = 0, scale_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
 };
