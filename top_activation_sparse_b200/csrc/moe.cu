@@ -111,7 +111,7 @@ __device__ __forceinline__ uint4 ld_x(const __nv_bfloat16* p) {
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -572,7 +572,7 @@ __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const S
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -672,24 +672,39 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
             w[0][i] = *reinterpret_cast<const uint32_t*>(row + at2);
             w[1][i] = *reinterpret_cast<const uint32_t*>(row2 + at2);
           }
+          // four blocks at a time: a block's second product waits for its first
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
-            // of its codes, all 0)
-            const float f0 = __uint_as_float(s[0][i] << 23), f1 = __uint_as_float(s[1][i] << 23);
-            const uint32_t a0 = half_pair<0>(w[0][i]), a1 = half_pair<0>(w[1][i]), a2 = half_pair<1>(w[0][i]),
-                           a3 = half_pair<1>(w[1][i]);
-            const uint32_t c0 = half_pair<2>(w[0][i]), c1 = half_pair<2>(w[1][i]), c2 = half_pair<3>(w[0][i]),
-                           c3 = half_pair<3>(w[1][i]);
+          for (int i0u = 0; i0u < 8; i0u += 4) {
+            float d[4][NG][4];
+            uint32_t c[4][4];
 #pragma unroll
-            for (int t = 0; t < NG; ++t) {
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma_f16(d, a0, a1, a2, a3, x.v[h + i][t][0], x.v[h + i][t][1]);
-              mma_f16(d, c0, c1, c2, c3, x.v[h + i][t][2], x.v[h + i][t][3]);
-              acc[t][0] = fmaf(d[0], f0, acc[t][0]);
-              acc[t][1] = fmaf(d[1], f0, acc[t][1]);
-              acc[t][2] = fmaf(d[2], f1, acc[t][2]);
-              acc[t][3] = fmaf(d[3], f1, acc[t][3]);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t wa = w[0][i0u + i], wb = w[1][i0u + i];
+              const uint32_t a0 = half_pair<0>(wa), a1 = half_pair<0>(wb), a2 = half_pair<1>(wa), a3 = half_pair<1>(wb);
+              c[i][0] = half_pair<2>(wa), c[i][1] = half_pair<2>(wb), c[i][2] = half_pair<3>(wa), c[i][3] = half_pair<3>(wb);
+#pragma unroll
+              for (int t = 0; t < NG; ++t) {
+                d[i][t][0] = d[i][t][1] = d[i][t][2] = d[i][t][3] = 0.0f;
+                mma_f16(d[i][t], a0, a1, a2, a3, x.v[h + i0u + i][t][0], x.v[h + i0u + i][t][1]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int t = 0; t < NG; ++t)
+                mma_f16(d[i][t], c[i][0], c[i][1], c[i][2], c[i][3], x.v[h + i0u + i][t][2], x.v[h + i0u + i][t][3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a
+              // NaN of its codes, all 0)
+              const float f0 = __uint_as_float(s[0][i0u + i] << 23), f1 = __uint_as_float(s[1][i0u + i] << 23);
+#pragma unroll
+              for (int t = 0; t < NG; ++t) {
+                acc[t][0] = fmaf(d[i][t][0], f0, acc[t][0]);
+                acc[t][1] = fmaf(d[i][t][1], f0, acc[t][1]);
+                acc[t][2] = fmaf(d[i][t][2], f1, acc[t][2]);
+                acc[t][3] = fmaf(d[i][t][3], f1, acc[t][3]);
+              }
             }
           }
         }
