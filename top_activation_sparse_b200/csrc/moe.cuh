@@ -1,4 +1,4 @@
-// Mixture-of-experts FFN layer for a few tokens (moe.cu): arguments and plan.
+// Mixture-of-experts FFN layer for a few tokens (moe_kernel.cuh): arguments and plan.
 #pragma once
 
 #include "qs_internal.cuh"
@@ -25,10 +25,13 @@ struct MoePlan {
   int tile_cols = 0;        // ... of this many columns
   int down_tokens = 0;      // tokens per pass of the down projection
   int down_pitch = 0, down_stages = 0;
+  int hidden_tokens = 0;    // tokens per pass of the hidden layer
+  int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
 };
-MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4);
+MoePlan plan_moe_bf16(int T, int d_model, int n_experts, int top_k);
+MoePlan plan_moe_fp4(int T, int d_model, int n_experts, int top_k);
 
 struct MoeArgs {
   const __nv_bfloat16* x = nullptr;       // [T, d_model]
@@ -53,7 +56,7 @@ struct MoeArgs {
   // workspace
   int32_t* ctl = nullptr;                 // MC_COUNT counters
   float* logits = nullptr;                // [T, E]
-  int32_t* table = nullptr;               // routing tables (see moe.cu)
+  int32_t* table = nullptr;               // routing tables (see below)
   float* share = nullptr;                 // [T, top_k]
   float* xup = nullptr;                   // [T] power of two that takes x to float16 (4-bit weights)
   float* h = nullptr;                     // [T * top_k, d_ff]
@@ -62,7 +65,8 @@ struct MoeArgs {
   DevStatus* status = nullptr;
   MoePlan plan{};
 };
-cudaError_t launch_moe(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
 
 // routing tables, int32: [0] active experts A, then per active expert its
 // number, first slot and number of tokens, then per slot its token, then per

@@ -1,0 +1,13 @@
+// The mixture-of-experts layer with bf16 expert weights.
+namespace qs {
+namespace {
+constexpr bool kFp4 = false;
+}
+}  // namespace qs
+
+#include "moe_kernel.cuh"
+
+namespace qs {
+MoePlan plan_moe_bf16(int T, int d_model, int n_experts, int top_k) { return make_plan(T, d_model, n_experts, top_k); }
+cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s) { return launch(a, s); }
+}  // namespace qs

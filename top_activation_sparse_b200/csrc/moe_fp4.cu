@@ -1,0 +1,13 @@
+// The mixture-of-experts layer with 4-bit expert weights.
+namespace qs {
+namespace {
+constexpr bool kFp4 = true;
+}
+}  // namespace qs
+
+#include "moe_kernel.cuh"
+
+namespace qs {
+MoePlan plan_moe_fp4(int T, int d_model, int n_experts, int top_k) { return make_plan(T, d_model, n_experts, top_k); }
+cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s) { return launch(a, s); }
+}  // namespace qs

@@ -1,4 +1,5 @@
 // A whole mixture-of-experts FFN layer for up to 64 tokens in one kernel.
+// Included by moe_bf16.cu and moe_fp4.cu, which say with what weights (kFp4).
 //
 //   logits = x W_r^T;  each token's top_k largest (ties: lower expert) are its
 //   experts, p = softmax over them;  for each (token, expert e):
@@ -36,33 +37,40 @@
 //
 // Products run on mma.sync m16n8k16 (16 tokens x 8 neurons; 16 columns x 8
 // tokens in the down projection): with weights read once, a few tokens stay
-// bound by bytes.  x stays in registers: each of 8 warps holds its part of
-// d_model for all tokens of the pass.  The sum over k may be permuted freely as
+// bound by bytes.  x stays in registers: with bf16 weights in registers, each
+// warp holding its part of d_model for all tokens of the pass, with 4-bit
+// weights (whose expansion needs the registers) in shared memory.  The sum over k may be permuted freely as
 // long as both operands agree; a lane's 16 bytes are its k values.  x and bf16
 // weights enter exactly; h enters as the sum of three bf16 numbers (relative
 // error below 2^-24).  4-bit weights are expanded in registers, exactly.
+#pragma once
+
 #include "fp4.cuh"
 #include "moe.cuh"
 
 namespace qs {
 namespace {
 
-constexpr int kMWarps = 8;             // warps that compute (168 registers each: a spill would go to L2, the
-                                       // ring leaves no L1)
+// Warps that compute.  bf16 rows: 8, with 168 registers, in which x and a strip of
+// columns fit (16 warps with 96: 521 against 447 us for 8 tokens, 8 experts of
+// 4096 x 11008; a spill goes to L2, the ring leaves no L1).  4-bit rows, whose
+// expansion waits for results at every step: 16 (67 against 79 us for one token,
+// 4096 x 14336).
+constexpr int kMWarps = kFp4 ? 16 : 8;
 constexpr int kMThreads = kMWarps * 32;
 constexpr int kThreads = kMThreads + 32;   // and one that copies
 constexpr int kMaxNg = 2;              // groups of 8 tokens per pass
 constexpr int kBatch = 64;             // neurons per batch (32 with two groups of tokens)
-constexpr int kListD = 2048;           // neurons per round of the down projection
+constexpr int kListD = 8 * kMThreads;  // neurons per round of the down projection
 constexpr int kRowsD = 128;            // flagged neurons whose h is staged at a time
 constexpr int kHPitch = kRowsD + 16;   // bf16 entries per token (pitch = 32 bytes mod 128)
-constexpr int kRing = 165 * 1024;      // ring of rows
+constexpr int kTail = 176 * 1024;      // x (4-bit weights), then the ring of rows
 constexpr int kMaxStages = 8;
 
 struct Smem {
-  unsigned char ring[kRing];
+  unsigned char tail[kTail];
   union {
-    float red[kMWarps * kBatch * 8];             // 16 KB: the warps' sums
+    float red[kMWarps * kBatch * 8];             // the warps' sums
     struct {
       __nv_bfloat16 h[3][8 * kMaxNg * kHPitch];
       uint16_t list[kListD];
@@ -101,7 +109,7 @@ __device__ __forceinline__ Smem& smem() {
 }
 
 // the computing warps' barrier
-__device__ __forceinline__ void csync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void csync() { asm volatile("bar.sync 1, %0;" ::"n"(kMThreads) : "memory"); }
 
 __device__ __forceinline__ uint4 ld_x(const __nv_bfloat16* p) {
   uint4 r;
@@ -196,7 +204,7 @@ __device__ __forceinline__ bool ring_wait(uint64_t* b, uint32_t parity, Smem& sm
 }
 
 // ---- router ------------------------------------------------------------------
-// item: 8 tasks, one per warp, of one expert and router_tokens tokens
+// item: a task per warp, of one expert and router_tokens tokens
 __device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
   const int nt = a.plan.router_tokens, groups = (a.T + nt - 1) / nt;
   const int task = item * kMWarps + warp;
@@ -447,6 +455,7 @@ struct Ring {
   int pitch;           // bytes between rows
   int rps;             // rows per stage
   int stages;
+  int off;             // where it starts in the tail
 };
 
 // The place in the ring, kept by each role across all its rows.
@@ -489,7 +498,7 @@ __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, D
     if (__all_sync(0xffffffffu, ok)) {
       if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.sl], (uint32_t)(nr * (R.rb + R.sb)));
       __syncwarp();
-      unsigned char* dst = sm.ring + (size_t)at.sl * R.rps * R.pitch;
+      unsigned char* dst = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
       for (int r = lane; r < nr; r += 32) {
         const size_t j = (size_t)(list ? list[i0 + r] : j0 + i0 + r);
         bulk_g2s(dst + r * R.pitch, w + j * R.rb, (uint32_t)R.rb, &sm.full[at.sl]);
@@ -501,29 +510,21 @@ __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, D
   }
 }
 
-// Up to KU units of 32 values of each row per warp, NG groups of 8 tokens; four
-// registers per unit and group.
-//   bf16 weights: a lane's 8 values of x (16 bytes), in order.
-//   4-bit weights: a code's bits, moved to the lowest exponent bits and the
-//   highest mantissa bit of float16, are its value times 2^-14 (subnormals
-//   included): no conversion, four operations a pair.  (The conversion
-//   instruction takes as long, at a quarter of the rate; matrix instructions of
-//   e4m3, into which a code goes as easily, were three times slower than those
-//   of float16.)  x, times the power of two that brings its token's largest into
-//   [2^14, 2^15), is float16, exact down to 2^-39 of that largest.
+// bf16 weights: x of up to KU units of 32 values per warp and NG groups of 8
+// tokens, four registers per unit and group (a lane's 8 values, in order).
 template <int KU, int NG>
 struct XFrag {
   uint32_t v[KU][NG][4];
 };
 
-// KS warps share the rows' length, 8 / KS groups take the tiles of a stage (8
-// rows, 16 of 4-bit weights) in turn.
+// KS warps share the rows' length, the kMWarps / KS groups take the tiles (8 rows, 16 of
+// 4-bit weights) in turn.  ku: units of 32 values per warp.
 struct Split {
-  int units, ks, groups, part, group, per, n;      // units of this warp: part * per .. + n
+  int ks, groups, part, group, per, n;             // units of this warp: part * per .. + n
   __device__ Split(int d, int ku, int warp) {
-    units = d / 32;
+    const int units = d / 32;
     ks = 1;
-    while (ks * ku < units) ks *= 2;
+    while (ks * ku < units && ks < kMWarps) ks *= 2;
     groups = kMWarps / ks;
     part = warp % ks;
     group = warp / ks;
@@ -540,33 +541,47 @@ __device__ __forceinline__ uint32_t half_pair(uint32_t p) {
   return (m & 0x0e000e00u) | (s & 0x80008000u);
 }
 
-template <bool FP4, int KU, int NG>
+template <int KU, int NG>
 __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const Split& P, XFrag<KU, NG>& x, int lane) {
   const int g = lane >> 2, q = lane & 3;
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
     const int t = sm.tok[n * 8 + g];
     const __nv_bfloat16* px = a.x + (size_t)max(t, 0) * a.d_model + (size_t)P.part * P.per * 32 + q * 8;
-    const float up = FP4 && t >= 0 ? sm.xup[t] : 0.0f;
 #pragma unroll
     for (int i = 0; i < KU; ++i) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (t >= 0 && i < P.n) v = ld_x(px + i * 32);
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-      if constexpr (FP4) {
-        // values c and c + 4, as the codes come out of their words
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t lo = u[c >> 1], hi = u[2 + (c >> 1)];
-          const __half2 h = c & 1 ? __floats2half2_rn(bf16hi(lo) * up, bf16hi(hi) * up)
-                                  : __floats2half2_rn(bf16lo(lo) * up, bf16lo(hi) * up);
-          x.v[i][n][c] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x.v[i][n][j] = u[j];
-      }
+      x.v[i][n][0] = v.x, x.v[i][n][1] = v.y, x.v[i][n][2] = v.z, x.v[i][n][3] = v.w;
     }
+  }
+}
+
+// 4-bit weights: a code's bits, moved to the lowest exponent bits and the
+// highest mantissa bit of float16, are its value times 2^-14 (subnormals
+// included): no conversion, four operations a pair.  (The conversion instruction
+// takes as long, at a quarter of the rate; matrix instructions of e4m3, into
+// which a code goes as easily, were three times slower than those of float16.)
+// x, times the power of two that brings its token's largest into [2^14, 2^15), is
+// float16, exact down to 2^-39 of that largest.  Each 8 values lie in the order
+// 0, 4, 1, 5, 2, 6, 3, 7, in which the codes come out of their words.
+__device__ __forceinline__ int x_pitch(int d) { return (d * 2 + 63) / 128 * 128 + 64; }   // 64 mod 128
+__device__ __forceinline__ void stage_x(const MoeArgs& a, Smem& sm, int nt) {
+  const int per = a.d_model / 8, pitch = x_pitch(a.d_model);
+  for (int i = threadIdx.x; i < nt * per; i += kMThreads) {
+    const int n = i / per, k = (i - n * per) * 8, t = sm.tok[n];
+    const uint4 v = ld_x(a.x + (size_t)t * a.d_model + k);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    const float up = sm.xup[t];
+    uint32_t r[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t lo = u[c >> 1], hi = u[2 + (c >> 1)];
+      const __half2 h = c & 1 ? __floats2half2_rn(bf16hi(lo) * up, bf16hi(hi) * up)
+                              : __floats2half2_rn(bf16lo(lo) * up, bf16lo(hi) * up);
+      r[c] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(sm.tail + n * pitch + k * 2) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -579,141 +594,52 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 
 // n rows from the ring times the pass's tokens: sums of row r (of the batch) and
-// token t to red[part][r][t]
-template <bool FP4, int KU, int NG>
-__device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P,
-                                               const XFrag<KU, NG>& x, const uint8_t* sc, const int* list, int j0, int n,
-                                               int lane) {
+// token t to red[part][r][t].
+template <int KU, int NG>
+__device__ __forceinline__ void dot_rows_bf16(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P,
+                                              const XFrag<KU, NG>& x, int n, int lane) {
   const int g = lane >> 2, q = lane & 3;
   float* red = sm.red + (size_t)P.part * kBatch * 8;     // kBatch x 8 = 32 x 16
-  // a lane's units lie apart by 64 or 16 bytes; the loads of those that the warp
-  // does not have repeat its first (x is 0 there)
+  // the loads of units that the warp does not have repeat its first (x is 0 there)
   const int first = P.n > 0 ? P.part * P.per : 0;
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
-    const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
-    constexpr int kTile = FP4 ? 16 : 8;
-    for (int t0 = P.group * kTile; t0 < nr; t0 += P.groups * kTile) {
-      const int ra = t0 + g < nr ? t0 + g : t0;
-      const unsigned char* row = stage + ra * R.pitch;
-      if constexpr (!FP4) {
-        // four sums in turn: one matrix instruction after the other into the
-        // same sum takes 20 to 32 cycles each
-        float acc[4][4];
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+    for (int t0 = P.group * 8; t0 < nr; t0 += P.groups * 8) {
+      const unsigned char* row = stage + (t0 + g < nr ? t0 + g : t0) * R.pitch + first * 64 + q * 16;
+      // four sums in turn: one matrix instruction after the other into the
+      // same sum takes 20 to 32 cycles each
+      constexpr int kSums = 4, kAhead = NG > 1 || KU > 16 ? 4 : 8;
+      float acc[kSums][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kSums; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        constexpr int kAhead = KU * NG <= 16 ? 8 : 4;      // loads before the first product
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 #pragma unroll
-        for (int h = 0; h < KU; h += kAhead) {
-          uint4 w[kAhead];
+      for (int h = 0; h < KU; h += kAhead) {          // kAhead loads before the first product
+        uint4 w[kAhead];
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-            w[i] = *reinterpret_cast<const uint4*>(row + (first + (h + i < P.n ? h + i : 0)) * 64 + q * 16);
+        for (int i = 0; i < kAhead; ++i) w[i] = *reinterpret_cast<const uint4*>(row + (h + i < P.n ? h + i : 0) * 64);
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            const uint32_t(&x0)[4] = x.v[h + i][0];
-            const uint32_t(&x1)[4] = x.v[h + i][NG - 1];
-            mma_bf16(acc[(2 * i) & 3], x0[0], NG > 1 ? x1[0] : 0u, x0[1], NG > 1 ? x1[1] : 0u, w[i].x, w[i].y);
-            mma_bf16(acc[(2 * i + 1) & 3], x0[2], NG > 1 ? x1[2] : 0u, x0[3], NG > 1 ? x1[3] : 0u, w[i].z, w[i].w);
-          }
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t(&x0)[4] = x.v[h + i][0];
+          const uint32_t(&x1)[4] = x.v[h + i][NG - 1];
+          mma_bf16(acc[(2 * i) % kSums], x0[0], NG > 1 ? x1[0] : 0u, x0[1], NG > 1 ? x1[1] : 0u, w[i].x, w[i].y);
+          mma_bf16(acc[(2 * i + 1) % kSums], x0[2], NG > 1 ? x1[2] : 0u, x0[3], NG > 1 ? x1[3] : 0u, w[i].z, w[i].w);
         }
-        // tokens g and g + 8, rows 2q and 2q + 1 of the tile
+      }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int rr = t0 + 2 * q + c;
-          if (rr < nr) {
-            red[(i0 + rr) * 8 * NG + g] = (acc[0][c] + acc[1][c]) + (acc[2][c] + acc[3][c]);
-            if constexpr (NG > 1)
-              red[(i0 + rr) * 8 * NG + 8 + g] = (acc[0][2 + c] + acc[1][2 + c]) + (acc[2][2 + c] + acc[3][2 + c]);
-          }
-        }
-      } else {
-        // the neurons are the matrix's 16 rows, the tokens its 8 columns; a unit
-        // is one block: its sum times its scale
-        const int rb2 = t0 + 8 + g < nr ? t0 + 8 + g : t0;
-        const unsigned char* row2 = stage + rb2 * R.pitch;
-        const uint8_t *p0, *p1;
-        if (R.sb) {
-          p0 = row + R.rb + first;
-          p1 = row2 + R.rb + first;
-        } else {
-          p0 = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * (a.d_model / 32) + first;
-          p1 = sc + (size_t)(list ? list[i0 + rb2] : j0 + i0 + rb2) * (a.d_model / 32) + first;
-        }
-        float acc[NG][4];
+      for (int i = 1; i < kSums; ++i)
 #pragma unroll
-        for (int t = 0; t < NG; ++t)
+        for (int j = 0; j < 4; ++j) acc[0][j] += acc[i][j];
+      // tokens g and g + 8, rows 2q and 2q + 1 of the tile
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[t][j] = 0.0f;
-#pragma unroll
-        for (int h = 0; h < KU; h += 8) {             // eight units at a time
-          uint32_t s[2][8], w[2][8];
-          if (R.sb && P.per % 8 == 0) {
-            const uint2 v0 = *reinterpret_cast<const uint2*>(p0 + h), v1 = *reinterpret_cast<const uint2*>(p1 + h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              s[0][i] = ((i < 4 ? v0.x : v0.y) >> (8 * (i & 3))) & 0xffu;
-              s[1][i] = ((i < 4 ? v1.x : v1.y) >> (8 * (i & 3))) & 0xffu;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int at2 = h + i < P.n ? h + i : 0;
-              s[0][i] = R.sb ? p0[at2] : __ldg(p0 + at2);
-              s[1][i] = R.sb ? p1[at2] : __ldg(p1 + at2);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int at2 = (first + (h + i < P.n ? h + i : 0)) * 16 + q * 4;
-            w[0][i] = *reinterpret_cast<const uint32_t*>(row + at2);
-            w[1][i] = *reinterpret_cast<const uint32_t*>(row2 + at2);
-          }
-          // four blocks at a time: a block's second product waits for its first
-#pragma unroll
-          for (int i0u = 0; i0u < 8; i0u += 4) {
-            float d[4][NG][4];
-            uint32_t c[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t wa = w[0][i0u + i], wb = w[1][i0u + i];
-              const uint32_t a0 = half_pair<0>(wa), a1 = half_pair<0>(wb), a2 = half_pair<1>(wa), a3 = half_pair<1>(wb);
-              c[i][0] = half_pair<2>(wa), c[i][1] = half_pair<2>(wb), c[i][2] = half_pair<3>(wa), c[i][3] = half_pair<3>(wb);
-#pragma unroll
-              for (int t = 0; t < NG; ++t) {
-                d[i][t][0] = d[i][t][1] = d[i][t][2] = d[i][t][3] = 0.0f;
-                mma_f16(d[i][t], a0, a1, a2, a3, x.v[h + i0u + i][t][0], x.v[h + i0u + i][t][1]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int t = 0; t < NG; ++t)
-                mma_f16(d[i][t], c[i][0], c[i][1], c[i][2], c[i][3], x.v[h + i0u + i][t][2], x.v[h + i0u + i][t][3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a
-              // NaN of its codes, all 0)
-              const float f0 = __uint_as_float(s[0][i0u + i] << 23), f1 = __uint_as_float(s[1][i0u + i] << 23);
-#pragma unroll
-              for (int t = 0; t < NG; ++t) {
-                acc[t][0] = fmaf(d[i][t][0], f0, acc[t][0]);
-                acc[t][1] = fmaf(d[i][t][1], f0, acc[t][1]);
-                acc[t][2] = fmaf(d[i][t][2], f1, acc[t][2]);
-                acc[t][3] = fmaf(d[i][t][3], f1, acc[t][3]);
-              }
-            }
-          }
-        }
-        // rows g and g + 8 of the tile, tokens 2q and 2q + 1
-#pragma unroll
-        for (int t = 0; t < NG; ++t) {
-          float* o = red + (size_t)(i0 + t0 + g) * 8 * NG + t * 8 + 2 * q;
-          if (t0 + g < nr) *reinterpret_cast<float2*>(o) = make_float2(acc[t][0], acc[t][1]);
-          if (t0 + 8 + g < nr) *reinterpret_cast<float2*>(o + 64 * NG) = make_float2(acc[t][2], acc[t][3]);
+      for (int c = 0; c < 2; ++c) {
+        const int rr = t0 + 2 * q + c;
+        if (rr < nr) {
+          red[(i0 + rr) * 8 * NG + g] = acc[0][c];
+          if constexpr (NG > 1) red[(i0 + rr) * 8 * NG + 8 + g] = acc[0][2 + c];
         }
       }
     }
@@ -723,43 +649,126 @@ __device__ __forceinline__ void dot_stage_rows(const MoeArgs& a, const Ring& R, 
   }
 }
 
-// One token, d_model <= 4096: the CTA goes on to its neurons' down rows, 16
-// columns per thread (two vectors of 8: 8 tid and 2048 + 8 tid).
+// 4-bit weights: the neurons are the matrix's 16 rows, the tokens its 8 columns;
+// a unit is one block of 32: its sum times its scale, four blocks at a time (a
+// block's second product waits for its first).
+__device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P, int nt,
+                                             const uint8_t* sc, const int* list, int j0, int n, int lane) {
+  const int g = lane >> 2, q = lane & 3, first = P.part * P.per;
+  float* red = sm.red + (size_t)P.part * kBatch * 8;
+  const unsigned char* xs = sm.tail + (g < nt ? g : 0) * x_pitch(a.d_model) + first * 64 + q * 16;
+  const bool has = g < nt;
+  int tile = 0;
+  for (int i0 = 0; i0 < n; i0 += R.rps) {
+    const int nr = min(R.rps, n - i0);
+    ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+    for (int t0 = 0; t0 < nr; t0 += 16, ++tile) {
+      if ((tile & (P.groups - 1)) != P.group) continue;
+      const int ra = t0 + g < nr ? t0 + g : t0, rc = t0 + 8 + g < nr ? t0 + 8 + g : t0;
+      const unsigned char* wa = stage + ra * R.pitch + first * 16 + q * 4;
+      const unsigned char* wb = stage + rc * R.pitch + first * 16 + q * 4;
+      const uint8_t *pa, *pb;                         // the blocks' scales
+      if (R.sb) {
+        pa = stage + ra * R.pitch + R.rb + first;
+        pb = stage + rc * R.pitch + R.rb + first;
+      } else {
+        pa = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * (a.d_model / 32) + first;
+        pb = sc + (size_t)(list ? list[i0 + rc] : j0 + i0 + rc) * (a.d_model / 32) + first;
+      }
+      const bool words = R.sb && P.per % 4 == 0;      // scales in whole words
+      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+      for (int h = 0; h < P.n; h += 4) {
+        uint32_t sa, sb, va[4], vb[4];
+        uint4 x[4];
+        if (words) {
+          sa = *reinterpret_cast<const uint32_t*>(pa + h);
+          sb = *reinterpret_cast<const uint32_t*>(pb + h);
+        } else {
+          sa = sb = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (h + i < P.n) {
+              sa |= (uint32_t)(R.sb ? pa[h + i] : __ldg(pa + h + i)) << (8 * i);
+              sb |= (uint32_t)(R.sb ? pb[h + i] : __ldg(pb + h + i)) << (8 * i);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                 // (units behind the warp's last have x = 0)
+          const int k = h + i < P.n ? h + i : h;
+          va[i] = *reinterpret_cast<const uint32_t*>(wa + k * 16);
+          vb[i] = *reinterpret_cast<const uint32_t*>(wb + k * 16);
+          x[i] = has && h + i < P.n ? *reinterpret_cast<const uint4*>(xs + k * 64) : make_uint4(0, 0, 0, 0);
+        }
+        float d[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
+          mma_f16(d[i], half_pair<0>(va[i]), half_pair<0>(vb[i]), half_pair<1>(va[i]), half_pair<1>(vb[i]), x[i].x, x[i].y);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_f16(d[i], half_pair<2>(va[i]), half_pair<2>(vb[i]), half_pair<3>(va[i]), half_pair<3>(vb[i]), x[i].z, x[i].w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
+          // of its codes, all 0)
+          const float f0 = __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), f1 = __uint_as_float(((sb >> (8 * i)) & 0xffu) << 23);
+          acc[0] = fmaf(d[i][0], f0, acc[0]);
+          acc[1] = fmaf(d[i][1], f0, acc[1]);
+          acc[2] = fmaf(d[i][2], f1, acc[2]);
+          acc[3] = fmaf(d[i][3], f1, acc[3]);
+        }
+      }
+      // rows g and g + 8 of the tile, tokens 2q and 2q + 1
+      float* o = red + (size_t)(i0 + t0 + g) * 8 + 2 * q;
+      if (t0 + g < nr) *reinterpret_cast<float2*>(o) = make_float2(acc[0], acc[1]);
+      if (t0 + 8 + g < nr) *reinterpret_cast<float2*>(o + 64) = make_float2(acc[2], acc[3]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[at.sl]);
+    at.next(R);
+  }
+}
+
+// One token, d_model <= 4096: the CTA goes on to its neurons' down rows, kVec
+// vectors of 8 columns per thread.
+constexpr int kVec = 4096 / (kMThreads * 8);
 template <bool FP4>
 __device__ __forceinline__ void down_stage_rows(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const uint8_t* sc,
-                                                const int* list, const float* val, int n, float (&y)[2][8], int lane) {
+                                                const int* list, const float* val, int n, float (&y)[kVec][8], int lane) {
   const int tid = threadIdx.x;
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 76);
-    const unsigned char* stage = sm.ring + (size_t)at.sl * R.rps * R.pitch;
-#pragma unroll 2
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+#pragma unroll 4
     for (int r = 0; r < nr; ++r) {
       const unsigned char* row = stage + r * R.pitch;
       const float h = val[i0 + r];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int col = v * 2048 + tid * 8;
-        if (col < a.d_model) {
-          if constexpr (!FP4) {
-            const uint4 w = *reinterpret_cast<const uint4*>(row + col * 2);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int v = 0; v < kVec; ++v) {
+        const int col = (v * kMThreads + tid) * 8;
+        if (col >= a.d_model) break;
+        if constexpr (!FP4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + col * 2);
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              y[v][2 * c] = fmaf(h, bf16lo(u[c]), y[v][2 * c]);
-              y[v][2 * c + 1] = fmaf(h, bf16hi(u[c]), y[v][2 * c + 1]);
-            }
-          } else {
-            const uint32_t b = R.sb ? row[R.rb + col / 32] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + col / 32);
-            const float hs = h * e8m0_value(b);
-            uint32_t f[4];
-            e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + col / 2), f);
+          for (int c = 0; c < 4; ++c) {
+            y[v][2 * c] = fmaf(h, bf16lo(u[c]), y[v][2 * c]);
+            y[v][2 * c + 1] = fmaf(h, bf16hi(u[c]), y[v][2 * c + 1]);
+          }
+        } else {
+          const uint32_t b = R.sb ? row[R.rb + col / 32] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + col / 32);
+          const float hs = h * e8m0_value(b);
+          uint32_t f[4];
+          e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + col / 2), f);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[c]));
-              y[v][2 * c] = fmaf(hs, e.x, y[v][2 * c]);
-              y[v][2 * c + 1] = fmaf(hs, e.y, y[v][2 * c + 1]);
-            }
+          for (int c = 0; c < 4; ++c) {
+            const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[c]));
+            y[v][2 * c] = fmaf(hs, e.x, y[v][2 * c]);
+            y[v][2 * c + 1] = fmaf(hs, e.y, y[v][2 * c + 1]);
           }
         }
       }
@@ -831,14 +840,19 @@ __device__ __forceinline__ float dot_sum(const Smem& sm, const Split& P, int i) 
 
 template <bool FP4, int KU, int NG, bool ONE>
 __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Run& u,
-                                            float (&y)[2][8], int lane, int warp) {
+                                            float (&y)[kVec][8], int lane, int warp) {
   const int tid = threadIdx.x;
   const ExpertMats M = expert_mats<FP4>(a, u.e);
   const float* b1 = a.b1 ? a.b1 + (size_t)u.e * a.d_ff : nullptr;
   const float* b2 = a.b2 ? a.b2 + (size_t)u.e * a.d_ff : nullptr;
   const Split P(a.d_model, KU, warp);
-  XFrag<KU, NG> x;
-  load_x<FP4, KU, NG>(a, sm, P, x, lane);
+  XFrag<FP4 ? 1 : KU, NG> x;
+  if constexpr (FP4) {
+    stage_x(a, sm, u.nt);
+    csync();
+  } else {
+    load_x<KU, NG>(a, sm, P, x, lane);
+  }
   const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
   // this thread's places in a batch's results: i = tid and tid + 256, row
   // i / 8 NG, token i % 8 NG (the same for both)
@@ -866,7 +880,8 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         j[k] = r < n ? (list ? list[r] : jb + r) : -1;
         bias[k] = bs && j[k] >= 0 ? __ldg(bs + j[k]) : 0.0f;
       }
-      dot_stage_rows<FP4, KU, NG>(a, R, at, sm, P, x, second ? M.s2 : M.s1, list, jb, n, lane);
+      if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
+      else dot_rows_bf16<KU, NG>(a, R, at, sm, P, x, n, lane);
       csync();
       if (!second) {
         // first factors of batch b, and its open neurons
@@ -1006,7 +1021,7 @@ __device__ __forceinline__ void run_tokens(Smem& sm, const Run& u) {
 template <bool FP4, int KU, int NG>
 __device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingAt& at, const Run& u, int lane, int warp) {
   Smem& sm = smem();
-  float none[2][8];
+  float none[kVec][8];
   RingAt here = at;                     // in registers
   const Ring ring = R;
   const Run run = u;
@@ -1014,34 +1029,42 @@ __device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingA
   at = here;
 }
 
+// units of 32 values per warp: bf16, d_model <= 4096: all of them in registers
+constexpr int kUnits = 16;
+
 template <bool FP4, bool ONE>
 __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, int item, int lane,
                                             int warp) {
-  // tokens per pass: two groups of 8 where x of both fits the registers
-  const int pass = a.d_model <= 4096 ? 16 : 8;
+  const int pass = a.plan.hidden_tokens;
   if (warp == kMWarps) {
     each_run(a, sm, item, pass, [&](const Run& u) { send_run<FP4, ONE>(a, R, at, sm, u, lane); });
     return;
   }
-  float y[2][8];
+  float y[kVec][8];
   if constexpr (ONE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[0][i] = y[1][i] = 0.0f;
+    for (int v = 0; v < kVec; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[v][i] = 0.0f;
   }
   each_run(a, sm, item, pass, [&](const Run& u) {
     run_tokens(sm, u);
     if constexpr (ONE) {
-      compute_run<FP4, 16, 1, true>(a, R, at, sm, u, y, lane, warp);
+      compute_run<FP4, kUnits, 1, true>(a, R, at, sm, u, y, lane, warp);
     } else {
-      if (a.d_model > 4096) compute_pass<FP4, 32, 1>(a, R, at, u, lane, warp);
-      else if (u.nt <= 8) compute_pass<FP4, 16, 1>(a, R, at, u, lane, warp);
-      else compute_pass<FP4, 16, 2>(a, R, at, u, lane, warp);
+      if constexpr (FP4) {
+        compute_pass<true, kUnits, 1>(a, R, at, u, lane, warp);
+      } else {
+        if (a.d_model > 4096) compute_pass<false, 2 * kUnits, 1>(a, R, at, u, lane, warp);
+        else if (u.nt <= 8) compute_pass<false, kUnits, 1>(a, R, at, u, lane, warp);
+        else compute_pass<false, kUnits, 2>(a, R, at, u, lane, warp);
+      }
     }
   });
   if constexpr (ONE) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int col = v * 2048 + threadIdx.x * 8;
+    for (int v = 0; v < kVec; ++v) {
+      const int col = (v * kMThreads + threadIdx.x) * 8;
       if (col < a.d_model) {
         float* o = a.parts + (size_t)item * a.d_model + col;
         __stcg(reinterpret_cast<float4*>(o), make_float4(y[v][0], y[v][1], y[v][2], y[v][3]));
@@ -1053,10 +1076,10 @@ __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, Rin
 
 // ---- down projection ---------------------------------------------------------
 // Item: (expert, column tile, range of neurons).  The range's flagged neurons
-// are listed, 2048 neurons at a time; the tile's piece of their down rows comes
+// are listed, 8 per thread at a time; the tile's piece of their down rows comes
 // through the ring 16 neurons per stage (one step of the matrix instructions);
 // their h is staged as three bf16 numbers, 128 neurons at a time.  A warp has
-// STR strips of 64 columns (4-bit weights: 128), every eighth of the tile.
+// STR strips of 64 columns (4-bit weights: 128), in turn over the warps.
 struct DownItem {
   int ai, e, ct, s, j0, j1, c0, cw;      // columns [c0, c0 + cw)
 };
@@ -1064,7 +1087,7 @@ struct DownItem {
 // barriers of their own (an item begins and ends with every stage free).
 struct DownRing {
   int pb, sb;                            // bytes of a piece, of its scales (0: not in the ring)
-  int pitch, stages;
+  int pitch, stages, off;
 };
 constexpr int kRowsStage = 16;
 
@@ -1090,6 +1113,7 @@ __device__ __forceinline__ DownRing down_ring(const MoeArgs& a, const DownItem& 
   r.sb = FP4 && a.plan.scale_bytes && d.cw % 512 == 0 && d.c0 % 512 == 0 ? d.cw / 32 : 0;
   r.pitch = a.plan.down_pitch;
   r.stages = a.plan.down_stages;
+  r.off = 0;
   return r;
 }
 
@@ -1109,7 +1133,7 @@ __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem
         if (__all_sync(0xffffffffu, ok)) {
           if (lane == 0) mbar_arrive_expect_tx(&sm.dfull[at.sl], (uint32_t)(nr * (R.pb + R.sb)));
           __syncwarp();
-          unsigned char* dst = sm.ring + (size_t)at.sl * kRowsStage * R.pitch;
+          unsigned char* dst = sm.tail + R.off + (size_t)at.sl * kRowsStage * R.pitch;
           if (lane < nr) {
             const size_t j = (size_t)(jl + sm.d.list[i0 + lane]);
             bulk_g2s(dst + lane * R.pitch, w + j * rb, (uint32_t)R.pb, &sm.dfull[at.sl]);
@@ -1198,7 +1222,7 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
       for (int st = 0; st < np / 16; ++st) {
         const int nr = min(kRowsStage, n - st * 16);
         ring_wait(&sm.dfull[at.sl], at.ph, sm, a.status, 81);
-        const unsigned char* stage = sm.ring + (size_t)at.sl * kRowsStage * R.pitch;
+        const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * kRowsStage * R.pitch;
         // this lane's rows 4 i + q (rows that the stage does not have repeat the
         // first: their h is 0)
         const unsigned char* row[4];
@@ -1284,10 +1308,10 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
   at_ = at;
 }
 
-// strips per warp: with at most 8 tokens their sums take 64 registers, with 16
+// strips per warp: with at most 8 tokens their sums take 64 or 32 registers, with 16
 // (bf16; the 4-bit form takes 8 tokens at a time) half the strips do
 template <bool FP4>
-constexpr int kStrips = FP4 ? 2 : 4;
+constexpr int kStrips = FP4 ? 1 : 4;
 
 // splits of an expert's neurons: about one item per CTA in all
 __device__ __forceinline__ int down_splits(const MoeArgs& a, int A) {
@@ -1306,14 +1330,16 @@ __device__ void down_item(const MoeArgs& a, RingAt& at, Smem& sm, int item, int 
   for (int t0 = 0; t0 < cnt; t0 += pass) {
     const int nt = min(pass, cnt - t0);
     if (FP4 || pass == 8) down_rows<FP4, 1, kStrips<FP4>>(a, at, d, first + t0, nt, lane, warp);
-    else if (nt <= 8) down_rows<FP4, 1, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
-    else down_rows<FP4, 2, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
+    else if constexpr (!FP4) {
+      if (nt <= 8) down_rows<FP4, 1, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
+      else down_rows<FP4, 2, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
+    }
   }
 }
 
 // ---- sums ----------------------------------------------------------------------
-// 16 vectors of 4 outputs per item; 16 threads share the partial sums of each
-// (every 16th in turn), so that their loads are all in flight at once
+// 16 vectors of 4 outputs per item; kMThreads / 16
+// threads share the partial sums of each (in turn), so that their loads are all in flight at once
 __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
   const int n4 = a.d_model / 4, tid = threadIdx.x, vec = tid & 15, part = tid >> 4;
   for (long long i0 = (long long)item * 16; i0 < (long long)a.T * n4; i0 += (long long)a.plan.out_items * 16) {
@@ -1326,14 +1352,14 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
     if (a.plan.one_token) {
       const float* src = a.parts + c;
 #pragma unroll 8
-      for (int s = part; s < a.plan.hidden_items; s += 16) {
+      for (int s = part; s < a.plan.hidden_items; s += kMThreads / 16) {
         const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * a.d_model));
         y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
       }
     } else {
       const int n = a.top_k * S;
 #pragma unroll 4
-      for (int k = part; k < n; k += 16) {
+      for (int k = part; k < n; k += kMThreads / 16) {
         const int j = k / S, s = k - j * S;
         const float p = sm.share[t * a.top_k + j];
         const float4 u = __ldcg(reinterpret_cast<const float4*>(
@@ -1347,7 +1373,7 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
   red[tid] = y;
   csync();
   if (part == 0 && ok) {
-    for (int k = 1; k < 16; ++k) {
+    for (int k = 1; k < kMThreads / 16; ++k) {
       const float4 u = red[k * 16 + vec];
       y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
     }
@@ -1370,7 +1396,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool computes = warp < kMWarps;
   const MoePlan& P = a.plan;
-  const Ring R{P.row_bytes, P.scale_bytes, P.pitch, P.stage_rows, P.stages};
+  const Ring R{P.row_bytes, P.scale_bytes, P.pitch, P.stage_rows, P.stages, P.x_bytes};
   RingAt at, atd;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R.stages; ++i) {
@@ -1441,7 +1467,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       } else if ((i -= P.hidden_items) < nD) {
         if constexpr (!ONE) {
           if (computes) wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
-          // (the copying warp waits for the first list of rows)
+          // (the copying warp waits for the first list of rows; with 4-bit weights
+          // its copies go where x lay)
+          if (FP4 && computes) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           down_item<FP4>(a, atd, sm, i, S, lane, warp);
           if (computes) finish(a.ctl + MC_DOWN, sm);
         }
@@ -1479,10 +1507,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
 }
 
-}  // namespace
-
-MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4) {
-  (void)d_ff;
+MoePlan make_plan(int T, int d_model, int n_experts, int top_k) {
+  constexpr bool fp4 = kFp4;
   MoePlan p;
   p.grid = kNumSMs;
   p.local = T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
@@ -1491,27 +1517,32 @@ MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4
   p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
   p.one_token = T == 1 && d_model <= 4096;
   p.hidden_items = p.grid;
-  // the ring: stages of about 36 KB, whole tiles of 8 rows where rows are short;
-  // a row's scales travel with it where bulk copies can take them
+  // tokens per pass: two groups of 8 where x of both fits the registers; with
+  // 4-bit weights as many as fit 64 KB of shared memory
+  p.hidden_tokens = fp4 ? (d_model <= 4096 ? 8 : 4) : (d_model <= 4096 ? 16 : 8);
+  p.x_bytes = fp4 ? (T < p.hidden_tokens ? T : p.hidden_tokens) * ((d_model * 2 + 63) / 128 * 128 + 64) : 0;
+  p.x_bytes = (p.x_bytes + 127) / 128 * 128;
+  // the ring: stages of about 36 KB, whole tiles of 8 or 16 rows where rows are
+  // short; a row's scales travel with it where bulk copies can take them
   p.row_bytes = fp4 ? d_model / 2 : d_model * 2;
   p.scale_bytes = fp4 && d_model % 512 == 0 ? d_model / 32 : 0;
   // eight rows' loads of 64 or 16 bytes each do not meet in a bank
-  const int apart = fp4 ? 16 : 64;
+  const int apart = fp4 ? 16 : 64, tile = fp4 ? 16 : 8;
   p.pitch = (p.row_bytes + p.scale_bytes + 127 - apart) / 128 * 128 + apart;
   p.stage_rows = 36 * 1024 / p.pitch;
   if (p.stage_rows < 1) p.stage_rows = 1;
-  if (p.stage_rows > 8) p.stage_rows = p.stage_rows > 64 ? 64 : p.stage_rows / 8 * 8;
-  p.stages = kRing / (p.stage_rows * p.pitch);
+  if (p.stage_rows > tile) p.stage_rows = p.stage_rows > 64 ? 64 : p.stage_rows / tile * tile;
+  p.stages = (kTail - p.x_bytes) / (p.stage_rows * p.pitch);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  // the down projection: tiles of up to 8 warps' strips
+  // the down projection: tiles of the warps' strips
   p.down_tokens = fp4 || T <= 8 ? 8 : 16;
-  const int strips = fp4 ? kStrips<true> : (p.down_tokens == 8 ? kStrips<false> : kStrips<false> / 2);
+  const int strips = p.down_tokens == 8 ? kStrips<fp4> : kStrips<fp4> / 2;
   p.tile_cols = kMWarps * strips * (fp4 ? 128 : 64);
   if (p.tile_cols > d_model) p.tile_cols = d_model;
   p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
   // 32 mod 128: four rows' loads do not meet in a bank
   p.down_pitch = ((fp4 ? p.tile_cols / 2 + p.tile_cols / 32 : p.tile_cols * 2) + 95) / 128 * 128 + 32;
-  p.down_stages = kRing / (kRowsStage * p.down_pitch);
+  p.down_stages = kTail / (kRowsStage * p.down_pitch);
   if (p.down_stages > kMaxStages) p.down_stages = kMaxStages;
   const long vecs = ((long)T * (d_model / 4) + 15) / 16;
   p.out_items = (int)(vecs < p.grid ? vecs : p.grid);
@@ -1521,16 +1552,16 @@ MoePlan plan_moe(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4
   return p;
 }
 
-cudaError_t launch_moe(const MoeArgs& a, cudaStream_t s) {
-  static unsigned done[4] = {0, 0, 0, 0};
+cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
+  static unsigned done[2] = {0, 0};
   const bool one = a.plan.one_token != 0;
-  auto k = a.fp4 ? (one ? moe_kernel<true, true> : moe_kernel<true, false>)
-                 : (one ? moe_kernel<false, true> : moe_kernel<false, false>);
-  cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[(a.fp4 ? 2 : 0) + (one ? 1 : 0)]);
+  auto k = one ? moe_kernel<kFp4, true> : moe_kernel<kFp4, false>;
+  cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[one ? 1 : 0]);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
+}  // namespace
 }  // namespace qs
