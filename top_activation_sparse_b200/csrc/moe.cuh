@@ -27,7 +27,7 @@ struct MoePlan {
   int down_pitch = 0, down_stages = 0;
   int hidden_tokens = 0;    // tokens per pass of the hidden layer
   int x_bytes = 0;          // shared memory of x (4-bit weights)
-  int row_bytes = 0, scale_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
+  int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
 };
 MoePlan plan_moe_bf16(int T, int d_model, int n_experts, int top_k);

@@ -64,7 +64,7 @@ constexpr int kBatch = 64;             // neurons per batch (32 with two groups 
 constexpr int kListD = 8 * kMThreads;  // neurons per round of the down projection
 constexpr int kRowsD = 128;            // flagged neurons whose h is staged at a time
 constexpr int kHPitch = kRowsD + 16;   // bf16 entries per token (pitch = 32 bytes mod 128)
-constexpr int kTail = 176 * 1024;      // x (4-bit weights), then the ring of rows
+constexpr int kTail = (kFp4 ? 172 : 176) * 1024;      // x (4-bit weights), then the ring of rows
 constexpr int kMaxStages = 8;
 
 struct Smem {
@@ -88,6 +88,8 @@ struct Smem {
   // this call's routing
   int16_t expert[kMoeMaxE], firsts[kMoeMaxE], count[kMoeMaxE];
   int16_t token[kMoeMaxSlots], slot[kMoeMaxSlots];
+  int16_t cum[2][kMoeMaxE + 1];                  // passes before each active expert (hidden layer, down)
+  uint8_t slot_expert[kMoeMaxSlots];             // the active expert of a slot
   float share[kMoeMaxSlots];
   float xup[kMoeMaxT];                           // 4-bit weights: the power of two x is multiplied with
   int active;
@@ -358,12 +360,25 @@ __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logit
     for (int i = 0; i < n; ++i)
       if (sm.sel[i] == e) {
         sm.token[at] = (int16_t)(i / K);
+        sm.slot_expert[at] = (uint8_t)ai;
         sm.slot[i] = (int16_t)at;
         ++at;
       }
   }
   if (threadIdx.x == 0) sm.active = total >> 16;
   csync();
+}
+
+// passes over an expert's weights: what its neurons weigh when work is dealt out
+__device__ __forceinline__ int passes_of(const Smem& sm, int kind, int ai) { return sm.cum[kind][ai + 1] - sm.cum[kind][ai]; }
+__device__ __forceinline__ void count_passes(const MoeArgs& a, Smem& sm) {
+  for (int i = threadIdx.x; i < 2 * (sm.active + 1); i += kMThreads) {
+    const int kind = i & 1, ai = i >> 1, tokens = kind ? a.plan.down_tokens : a.plan.hidden_tokens;
+    int n = 0;
+#pragma unroll 4
+    for (int k = 0; k < ai; ++k) n += (sm.count[k] + tokens - 1) / tokens;
+    sm.cum[kind][ai] = (int16_t)n;
+  }
 }
 
 // the routing from sm to the workspace, and back in every other CTA
@@ -391,6 +406,9 @@ __device__ void fetch_routing(const MoeArgs& a, Smem& sm) {
   for (int i = tid; i < n; i += kMThreads) {
     sm.token[i] = (int16_t)__ldcg(a.table + kMtToken + i);
     sm.slot[i] = (int16_t)__ldcg(a.table + kMtSlot + i);
+    int ai = 0;                          // (active experts are few where slots are)
+    while (ai + 1 < A && __ldcg(a.table + kMtFirst + ai + 1) <= i) ++ai;
+    sm.slot_expert[i] = (uint8_t)ai;
     sm.share[i] = __ldcg(a.share + i);
   }
   if (a.fp4)
@@ -452,6 +470,7 @@ __device__ __forceinline__ float relu_nan(float v) { return v <= 0.0f ? 0.0f : v
 // How rows lie in the ring, from the plan; the same in both roles.
 struct Ring {
   int rb, sb;          // bytes of a row, and of its scales where they travel with it (else 0)
+  int stage;           // bytes of a stage: rps rows at `pitch`, then their scales
   int pitch;           // bytes between rows
   int rps;             // rows per stage
   int stages;
@@ -498,12 +517,16 @@ __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, D
     if (__all_sync(0xffffffffu, ok)) {
       if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.sl], (uint32_t)(nr * (R.rb + R.sb)));
       __syncwarp();
-      unsigned char* dst = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+      unsigned char* dst = sm.tail + R.off + (size_t)at.sl * R.stage;
       for (int r = lane; r < nr; r += 32) {
         const size_t j = (size_t)(list ? list[i0 + r] : j0 + i0 + r);
         bulk_g2s(dst + r * R.pitch, w + j * R.rb, (uint32_t)R.rb, &sm.full[at.sl]);
-        if (R.sb) bulk_g2s(dst + r * R.pitch + R.rb, sc + j * R.sb, (uint32_t)R.sb, &sm.full[at.sl]);
+        if (R.sb && list) bulk_g2s(dst + R.rps * R.pitch + r * R.sb, sc + j * R.sb, (uint32_t)R.sb, &sm.full[at.sl]);
       }
+      // (the scales of neighbouring rows in one copy: one of 128 bytes beside each
+      // row's 2 KB takes a third of the copies' bandwidth, 5.9 -> 4.1 TB/s)
+      if (R.sb && !list && lane == 0)
+        bulk_g2s(dst + R.rps * R.pitch, sc + (size_t)(j0 + i0) * R.sb, (uint32_t)(nr * R.sb), &sm.full[at.sl]);
       ++at.issued;
     }
     at.next(R);
@@ -533,14 +556,6 @@ struct Split {
   }
 };
 
-// bits 4c..4c+3 of each half of p (a code each) -> a pair of float16, times 2^-14
-template <int C>
-__device__ __forceinline__ uint32_t half_pair(uint32_t p) {
-  const uint32_t m = C == 3 ? p >> 3 : p << (9 - 4 * C);
-  const uint32_t s = C == 3 ? p : p << (12 - 4 * C);
-  return (m & 0x0e000e00u) | (s & 0x80008000u);
-}
-
 template <int KU, int NG>
 __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const Split& P, XFrag<KU, NG>& x, int lane) {
   const int g = lane >> 2, q = lane & 3;
@@ -557,14 +572,13 @@ __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const S
   }
 }
 
-// 4-bit weights: a code's bits, moved to the lowest exponent bits and the
-// highest mantissa bit of float16, are its value times 2^-14 (subnormals
-// included): no conversion, four operations a pair.  (The conversion instruction
-// takes as long, at a quarter of the rate; matrix instructions of e4m3, into
-// which a code goes as easily, were three times slower than those of float16.)
-// x, times the power of two that brings its token's largest into [2^14, 2^15), is
-// float16, exact down to 2^-39 of that largest.  Each 8 values lie in the order
-// 0, 4, 1, 5, 2, 6, 3, 7, in which the codes come out of their words.
+// 4-bit weights: codes become float16 by the conversion instruction, a byte (two
+// codes) at a time.  (It runs at a quarter of the rate of simple instructions,
+// but moving a code's bits to the exponent and mantissa bits of float16 takes
+// four of those a pair, and the warps are short of issue slots; matrix
+// instructions of e4m3, into which codes go by two shifts, were three times slower
+// than those of float16.)  x, times the power of two that brings its token's
+// largest into [2^14, 2^15), is float16, exact down to 2^-39 of that largest.
 __device__ __forceinline__ int x_pitch(int d) { return (d * 2 + 63) / 128 * 128 + 64; }   // 64 mod 128
 __device__ __forceinline__ void stage_x(const MoeArgs& a, Smem& sm, int nt) {
   const int per = a.d_model / 8, pitch = x_pitch(a.d_model);
@@ -576,9 +590,7 @@ __device__ __forceinline__ void stage_x(const MoeArgs& a, Smem& sm, int nt) {
     uint32_t r[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint32_t lo = u[c >> 1], hi = u[2 + (c >> 1)];
-      const __half2 h = c & 1 ? __floats2half2_rn(bf16hi(lo) * up, bf16hi(hi) * up)
-                              : __floats2half2_rn(bf16lo(lo) * up, bf16lo(hi) * up);
+      const __half2 h = __floats2half2_rn(bf16lo(u[c]) * up, bf16hi(u[c]) * up);
       r[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(sm.tail + n * pitch + k * 2) = make_uint4(r[0], r[1], r[2], r[3]);
@@ -605,7 +617,7 @@ __device__ __forceinline__ void dot_rows_bf16(const MoeArgs& a, const Ring& R, R
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
-    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.stage;
     for (int t0 = P.group * 8; t0 < nr; t0 += P.groups * 8) {
       const unsigned char* row = stage + (t0 + g < nr ? t0 + g : t0) * R.pitch + first * 64 + q * 16;
       // four sums in turn: one matrix instruction after the other into the
@@ -654,44 +666,46 @@ __device__ __forceinline__ void dot_rows_bf16(const MoeArgs& a, const Ring& R, R
 // block's second product waits for its first).
 __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P, int nt,
                                              const uint8_t* sc, const int* list, int j0, int n, int lane) {
-  const int g = lane >> 2, q = lane & 3, first = P.part * P.per;
+  const int g = lane >> 2, q = lane & 3, first = P.part * P.per, sb = a.d_model / 32;
   float* red = sm.red + (size_t)P.part * kBatch * 8;
   const unsigned char* xs = sm.tail + (g < nt ? g : 0) * x_pitch(a.d_model) + first * 64 + q * 16;
-  const bool has = g < nt;
+  const bool has = g < nt, whole = R.sb && P.per == 16;     // 16 scales of a row in one load
   int tile = 0;
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 75);
-    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.stage;
     for (int t0 = 0; t0 < nr; t0 += 16, ++tile) {
       if ((tile & (P.groups - 1)) != P.group) continue;
       const int ra = t0 + g < nr ? t0 + g : t0, rc = t0 + 8 + g < nr ? t0 + 8 + g : t0;
       const unsigned char* wa = stage + ra * R.pitch + first * 16 + q * 4;
       const unsigned char* wb = stage + rc * R.pitch + first * 16 + q * 4;
       const uint8_t *pa, *pb;                         // the blocks' scales
+      uint4 ca = make_uint4(0, 0, 0, 0), cb = ca;
       if (R.sb) {
-        pa = stage + ra * R.pitch + R.rb + first;
-        pb = stage + rc * R.pitch + R.rb + first;
+        pa = stage + R.rps * R.pitch + ra * R.sb + first;
+        pb = stage + R.rps * R.pitch + rc * R.sb + first;
+        if (whole) ca = *reinterpret_cast<const uint4*>(pa), cb = *reinterpret_cast<const uint4*>(pb);
       } else {
-        pa = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * (a.d_model / 32) + first;
-        pb = sc + (size_t)(list ? list[i0 + rc] : j0 + i0 + rc) * (a.d_model / 32) + first;
+        pa = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * sb + first;
+        pb = sc + (size_t)(list ? list[i0 + rc] : j0 + i0 + rc) * sb + first;
       }
-      const bool words = R.sb && P.per % 4 == 0;      // scales in whole words
       float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-      for (int h = 0; h < P.n; h += 4) {
-        uint32_t sa, sb, va[4], vb[4];
+#pragma unroll
+      for (int h = 0; h < 16; h += 4) {
+        if (h >= P.n) break;
+        uint32_t sa, sbw, va[4], vb[4];
         uint4 x[4];
-        if (words) {
-          sa = *reinterpret_cast<const uint32_t*>(pa + h);
-          sb = *reinterpret_cast<const uint32_t*>(pb + h);
+        if (whole) {
+          sa = h == 0 ? ca.x : h == 4 ? ca.y : h == 8 ? ca.z : ca.w;
+          sbw = h == 0 ? cb.x : h == 4 ? cb.y : h == 8 ? cb.z : cb.w;
         } else {
-          sa = sb = 0;
+          sa = sbw = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (h + i < P.n) {
               sa |= (uint32_t)(R.sb ? pa[h + i] : __ldg(pa + h + i)) << (8 * i);
-              sb |= (uint32_t)(R.sb ? pb[h + i] : __ldg(pb + h + i)) << (8 * i);
+              sbw |= (uint32_t)(R.sb ? pb[h + i] : __ldg(pb + h + i)) << (8 * i);
             }
         }
 #pragma unroll
@@ -702,19 +716,21 @@ __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, Ri
           x[i] = has && h + i < P.n ? *reinterpret_cast<const uint4*>(xs + k * 64) : make_uint4(0, 0, 0, 0);
         }
         float d[4][4];
+        uint32_t ha[4][4], hb[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
-          mma_f16(d[i], half_pair<0>(va[i]), half_pair<0>(vb[i]), half_pair<1>(va[i]), half_pair<1>(vb[i]), x[i].x, x[i].y);
+          e2m1x8_to_half2(va[i], ha[i]);
+          e2m1x8_to_half2(vb[i], hb[i]);
+          mma_f16(d[i], ha[i][0], hb[i][0], ha[i][1], hb[i][1], x[i].x, x[i].y);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_f16(d[i], half_pair<2>(va[i]), half_pair<2>(vb[i]), half_pair<3>(va[i]), half_pair<3>(vb[i]), x[i].z, x[i].w);
+        for (int i = 0; i < 4; ++i) mma_f16(d[i], ha[i][2], hb[i][2], ha[i][3], hb[i][3], x[i].z, x[i].w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
           // of its codes, all 0)
-          const float f0 = __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), f1 = __uint_as_float(((sb >> (8 * i)) & 0xffu) << 23);
+          const float f0 = __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), f1 = __uint_as_float(((sbw >> (8 * i)) & 0xffu) << 23);
           acc[0] = fmaf(d[i][0], f0, acc[0]);
           acc[1] = fmaf(d[i][1], f0, acc[1]);
           acc[2] = fmaf(d[i][2], f1, acc[2]);
@@ -742,7 +758,7 @@ __device__ __forceinline__ void down_stage_rows(const MoeArgs& a, const Ring& R,
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
     ring_wait(&sm.full[at.sl], at.ph, sm, a.status, 76);
-    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.rps * R.pitch;
+    const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * R.stage;
 #pragma unroll 4
     for (int r = 0; r < nr; ++r) {
       const unsigned char* row = stage + r * R.pitch;
@@ -760,7 +776,8 @@ __device__ __forceinline__ void down_stage_rows(const MoeArgs& a, const Ring& R,
             y[v][2 * c + 1] = fmaf(h, bf16hi(u[c]), y[v][2 * c + 1]);
           }
         } else {
-          const uint32_t b = R.sb ? row[R.rb + col / 32] : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + col / 32);
+          const uint32_t b = R.sb ? stage[R.rps * R.pitch + r * R.sb + col / 32]
+                                  : __ldg(sc + (size_t)list[i0 + r] * (a.d_model / 32) + col / 32);
           const float hs = h * e8m0_value(b);
           uint32_t f[4];
           e2m1x8_to_half2(*reinterpret_cast<const uint32_t*>(row + col / 2), f);
@@ -859,7 +876,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
   constexpr int kPer = kBatch * 8 / kMThreads, kTok = 8 * NG, kRowsPerWarp = 32 / kTok;
   const int c = tid % kTok, r0 = tid / kTok;
   constexpr int kStep = kMThreads / kTok;                // rows between a thread's places
-  const float back = FP4 && c < u.nt ? 16384.0f / sm.xup[sm.tok[c]] : 1.0f;
+  const float back = FP4 && c < u.nt ? 1.0f / sm.xup[sm.tok[c]] : 1.0f;
   const float share = ONE ? choice_share(a, sm, u.slot0) : 0.0f;
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
     // (one body for both factors: the code of two does not stay in the
@@ -976,17 +993,27 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
 }
 
 // The runs of a hidden-layer item, in the order both roles take them: f(run).
+// The items have equal shares of the neurons times their experts' passes.
 template <typename F>
 __device__ __forceinline__ void each_run(const MoeArgs& a, const Smem& sm, int item, int pass, F&& f) {
-  const long long N = (long long)sm.active * a.d_ff;
-  const long long n1 = N * (item + 1) / a.plan.hidden_items;
-  for (long long n0 = N * item / a.plan.hidden_items; n0 < n1;) {
+  const long long N = (long long)sm.cum[0][sm.active] * a.d_ff;
+  const long long n0 = N * item / a.plan.hidden_items, n1 = N * (item + 1) / a.plan.hidden_items;
+  // the first expert of the range
+  int ai = 0;
+  for (int step = kMoeMaxE / 2; step; step >>= 1)
+    if (ai + step < sm.active && (long long)sm.cum[0][ai + step] * a.d_ff <= n0) ai += step;
+  for (; ai < sm.active; ++ai) {
+    const long long at = (long long)sm.cum[0][ai] * a.d_ff;
+    if (at >= n1) break;
+    const int np = passes_of(sm, 0, ai);
+    const long long lo = max(n0 - at, 0ll), hi = min(n1 - at, (long long)np * a.d_ff);
     Run u;
-    u.ai = (int)(n0 / a.d_ff);
-    u.j0 = (int)(n0 - (long long)u.ai * a.d_ff);
-    u.j1 = (int)min((long long)a.d_ff, (long long)u.j0 + (n1 - n0));
-    u.e = sm.expert[u.ai];
-    const int cnt = sm.count[u.ai], first = sm.firsts[u.ai];
+    u.ai = ai;
+    u.j0 = (int)(lo / np);
+    u.j1 = (int)(hi / np);
+    if (hi <= 0 || u.j0 >= u.j1) continue;
+    u.e = sm.expert[ai];
+    const int cnt = sm.count[ai], first = sm.firsts[ai];
     // (every pass over a batch's worth of neurons before the next, so that the
     // second pass finds the rows in L2)
     const int step = cnt > pass ? 2 * kBatch : u.j1 - u.j0;
@@ -1005,7 +1032,6 @@ __device__ __forceinline__ void each_run(const MoeArgs& a, const Smem& sm, int i
         v.keep_zeros = cnt > pass;
         f(v);
       }
-    n0 += end - u.j0;
   }
 }
 
@@ -1081,28 +1107,41 @@ __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, Rin
 // their h is staged as three bf16 numbers, 128 neurons at a time.  A warp has
 // STR strips of 64 columns (4-bit weights: 128), in turn over the warps.
 struct DownItem {
-  int ai, e, ct, s, j0, j1, c0, cw;      // columns [c0, c0 + cw)
+  int ai, e, s, j0, j1, c0, cw;          // columns [c0, c0 + cw)
 };
 // Its stages are others than the hidden layer's, in the same memory, with
 // barriers of their own (an item begins and ends with every stage free).
 struct DownRing {
-  int pb, sb;                            // bytes of a piece, of its scales (0: not in the ring)
+  int pb;                                // bytes of a piece
   int pitch, stages, off;
 };
 constexpr int kRowsStage = 16;
 
-template <bool FP4>
+// splits of an expert's neurons: S per pass over them, about one item per CTA in
+// all; the buffers hold max_splits
+__device__ __forceinline__ int down_splits(const MoeArgs& a, const Smem& sm) {
+  const int s = a.plan.grid / (sm.cum[1][sm.active] * a.plan.col_tiles);
+  return max(1, s);
+}
+__device__ __forceinline__ int expert_splits(const MoeArgs& a, const Smem& sm, int ai, int S) {
+  return min(S * passes_of(sm, 1, ai), a.plan.max_splits);
+}
+__device__ __forceinline__ int down_items(const MoeArgs& a, const Smem& sm, int S) {
+  int n = 0;
+  for (int ai = 0; ai < sm.active; ++ai) n += expert_splits(a, sm, ai, S);
+  return n * a.plan.col_tiles;
+}
+
 __device__ __forceinline__ DownItem down_place(const MoeArgs& a, const Smem& sm, int item, int S) {
   DownItem d;
-  d.ct = item % a.plan.col_tiles;
-  const int rest = item / a.plan.col_tiles;
-  d.s = rest % S;
-  d.ai = rest / S;
+  int rest = item / a.plan.col_tiles, n = expert_splits(a, sm, 0, S);
+  for (d.ai = 0; rest >= n; n = expert_splits(a, sm, ++d.ai, S)) rest -= n;
+  d.s = rest;
   d.e = sm.expert[d.ai];
   // whole groups of 8 neurons (their flags are read 8 at a time)
-  d.j0 = (int)((long long)(a.d_ff / 8) * d.s / S) * 8;
-  d.j1 = (int)((long long)(a.d_ff / 8) * (d.s + 1) / S) * 8;
-  d.c0 = d.ct * a.plan.tile_cols;
+  d.j0 = (int)((long long)(a.d_ff / 8) * d.s / n) * 8;
+  d.j1 = (int)((long long)(a.d_ff / 8) * (d.s + 1) / n) * 8;
+  d.c0 = item % a.plan.col_tiles * a.plan.tile_cols;
   d.cw = min(a.plan.tile_cols, a.d_model - d.c0);
   return d;
 }
@@ -1110,7 +1149,6 @@ template <bool FP4>
 __device__ __forceinline__ DownRing down_ring(const MoeArgs& a, const DownItem& d) {
   DownRing r;
   r.pb = FP4 ? d.cw / 2 : d.cw * 2;
-  r.sb = FP4 && a.plan.scale_bytes && d.cw % 512 == 0 && d.c0 % 512 == 0 ? d.cw / 32 : 0;
   r.pitch = a.plan.down_pitch;
   r.stages = a.plan.down_stages;
   r.off = 0;
@@ -1122,7 +1160,6 @@ __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem
   const DownRing R = down_ring<FP4>(a, d);
   const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;
   const uint8_t* w = a.wd + (size_t)d.e * a.d_ff * rb + (FP4 ? d.c0 / 2 : d.c0 * 2);
-  const uint8_t* sc = FP4 ? a.sd + (size_t)d.e * a.d_ff * (a.d_model / 32) + d.c0 / 32 : nullptr;
   for (int p = 0; p < passes; ++p)
     for (int jl = d.j0; jl < d.j1; jl += kListD) {
       list_wait(sm, at, 2, a.status);
@@ -1131,13 +1168,12 @@ __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem
         const int nr = min(kRowsStage, total - i0);
         const bool ok = ring_wait(&sm.dempty[at.sl], at.ph ^ 1u, sm, a.status, 80);
         if (__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.dfull[at.sl], (uint32_t)(nr * (R.pb + R.sb)));
+          if (lane == 0) mbar_arrive_expect_tx(&sm.dfull[at.sl], (uint32_t)(nr * R.pb));
           __syncwarp();
           unsigned char* dst = sm.tail + R.off + (size_t)at.sl * kRowsStage * R.pitch;
           if (lane < nr) {
             const size_t j = (size_t)(jl + sm.d.list[i0 + lane]);
             bulk_g2s(dst + lane * R.pitch, w + j * rb, (uint32_t)R.pb, &sm.dfull[at.sl]);
-            if (R.sb) bulk_g2s(dst + lane * R.pitch + R.pb, sc + j * (a.d_model / 32), (uint32_t)R.sb, &sm.dfull[at.sl]);
           }
           ++at.issued;
         }
@@ -1219,7 +1255,28 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
         }
       }
       csync();
+      // 4-bit weights: the scales of this lane's rows and strips, a stage ahead
+      uint32_t ns[STR][4];
+      auto ahead = [&](int st) {
+        if constexpr (FP4) {
+          const int left = n - st * 16;
+          if (left > 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint8_t* p = sc + (size_t)(jl + sm.d.list[l0 + st * 16 + (4 * i + q < left ? 4 * i + q : 0)]) * (a.d_model / 32);
+#pragma unroll
+              for (int x = 0; x < STR; ++x) ns[x][i] = __ldg(p + (col[x] < d.cw ? col[x] : 0) / 32);
+            }
+        }
+      };
+      ahead(0);
       for (int st = 0; st < np / 16; ++st) {
+        uint32_t cs[STR][4];
+#pragma unroll
+        for (int x = 0; x < STR; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) cs[x][i] = FP4 ? ns[x][i] : 0u;
+        ahead(st + 1);
         const int nr = min(kRowsStage, n - st * 16);
         ring_wait(&sm.dfull[at.sl], at.ph, sm, a.status, 81);
         const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * kRowsStage * R.pitch;
@@ -1258,13 +1315,9 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
                    __byte_perm(u2[m], u3[m], 0x5410), __byte_perm(u2[m], u3[m], 0x7632));
           } else {
             uint2 v[4];
-            uint32_t s[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[i] = *reinterpret_cast<const uint2*>(row[i] + cl / 2);
-              s[i] = R.sb ? row[i][R.pb + cl / 32]
-                          : __ldg(sc + (size_t)(jl + sm.d.list[l0 + st * 16 + (4 * i + q < nr ? 4 * i + q : 0)]) * (a.d_model / 32) + cl / 32);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint2*>(row[i] + cl / 2);
+            const uint32_t(&s)[4] = cs[x];
             // pairs of neurons (0, 1) and (2, 3), one code of each per half
             const uint32_t lo01 = scale_lo(s[0]) | (scale_lo(s[1]) << 16), lo23 = scale_lo(s[2]) | (scale_lo(s[3]) << 16);
             const uint32_t hi01 = scale_hi(s[0]) | (scale_hi(s[1]) << 16), hi23 = scale_hi(s[2]) | (scale_hi(s[3]) << 16);
@@ -1313,15 +1366,9 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
 template <bool FP4>
 constexpr int kStrips = FP4 ? 1 : 4;
 
-// splits of an expert's neurons: about one item per CTA in all
-__device__ __forceinline__ int down_splits(const MoeArgs& a, int A) {
-  const int s = a.plan.grid / (A * a.plan.col_tiles);
-  return max(1, min(s, a.plan.max_splits));
-}
-
 template <bool FP4>
 __device__ void down_item(const MoeArgs& a, RingAt& at, Smem& sm, int item, int S, int lane, int warp) {
-  const DownItem d = down_place<FP4>(a, sm, item, S);
+  const DownItem d = down_place(a, sm, item, S);
   const int first = sm.firsts[d.ai], cnt = sm.count[d.ai], pass = a.plan.down_tokens;
   if (warp == kMWarps) {
     send_down<FP4>(a, at, sm, d, (cnt + pass - 1) / pass, lane);
@@ -1357,14 +1404,16 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
         y.x += u.x, y.y += u.y, y.z += u.z, y.w += u.w;
       }
     } else {
-      const int n = a.top_k * S;
-#pragma unroll 4
-      for (int k = part; k < n; k += kMThreads / 16) {
-        const int j = k / S, s = k - j * S;
+      for (int j = 0; j < a.top_k; ++j) {
+        const int slot = sm.slot[t * a.top_k + j];
         const float p = sm.share[t * a.top_k + j];
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(
-            a.parts + ((size_t)s * slots + sm.slot[t * a.top_k + j]) * a.d_model + c));
-        y.x = fmaf(p, u.x, y.x), y.y = fmaf(p, u.y, y.y), y.z = fmaf(p, u.z, y.z), y.w = fmaf(p, u.w, y.w);
+        const float* src = a.parts + (size_t)slot * a.d_model + c;
+        const int n = expert_splits(a, sm, sm.slot_expert[slot], S);
+#pragma unroll 4
+        for (int s = part; s < n; s += kMThreads / 16) {
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * slots * a.d_model));
+          y.x = fmaf(p, u.x, y.x), y.y = fmaf(p, u.y, y.y), y.z = fmaf(p, u.z, y.z), y.w = fmaf(p, u.w, y.w);
+        }
       }
     }
   }
@@ -1396,7 +1445,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool computes = warp < kMWarps;
   const MoePlan& P = a.plan;
-  const Ring R{P.row_bytes, P.scale_bytes, P.pitch, P.stage_rows, P.stages, P.x_bytes};
+  const Ring R{P.row_bytes, P.scale_bytes, P.stage_bytes, P.pitch, P.stage_rows, P.stages, P.x_bytes};
   RingAt at, atd;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R.stages; ++i) {
@@ -1452,13 +1501,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
           } else if (threadIdx.x == 0) {
             sm.active = 0;              // no tables to go by
           }
+          csync();
+          count_passes(a, sm);
         }
         __syncthreads();
         if (sm.active == 0) break;
         routed = true;
         if constexpr (!ONE) {
-          S = down_splits(a, sm.active);
-          nD = sm.active * S * P.col_tiles;
+          S = down_splits(a, sm);
+          nD = down_items(a, sm, S);
         }
       }
       if (i < P.hidden_items) {
@@ -1523,16 +1574,17 @@ MoePlan make_plan(int T, int d_model, int n_experts, int top_k) {
   p.x_bytes = fp4 ? (T < p.hidden_tokens ? T : p.hidden_tokens) * ((d_model * 2 + 63) / 128 * 128 + 64) : 0;
   p.x_bytes = (p.x_bytes + 127) / 128 * 128;
   // the ring: stages of about 36 KB, whole tiles of 8 or 16 rows where rows are
-  // short; a row's scales travel with it where bulk copies can take them
+  // short
   p.row_bytes = fp4 ? d_model / 2 : d_model * 2;
-  p.scale_bytes = fp4 && d_model % 512 == 0 ? d_model / 32 : 0;
   // eight rows' loads of 64 or 16 bytes each do not meet in a bank
   const int apart = fp4 ? 16 : 64, tile = fp4 ? 16 : 8;
-  p.pitch = (p.row_bytes + p.scale_bytes + 127 - apart) / 128 * 128 + apart;
-  p.stage_rows = 36 * 1024 / p.pitch;
+  p.scale_bytes = fp4 && d_model % 512 == 0 ? d_model / 32 : 0;     // what bulk copies can take
+  p.pitch = (p.row_bytes + 127 - apart) / 128 * 128 + apart;
+  p.stage_rows = 36 * 1024 / (p.pitch + p.scale_bytes);
   if (p.stage_rows < 1) p.stage_rows = 1;
   if (p.stage_rows > tile) p.stage_rows = p.stage_rows > 64 ? 64 : p.stage_rows / tile * tile;
-  p.stages = (kTail - p.x_bytes) / (p.stage_rows * p.pitch);
+  p.stage_bytes = (p.stage_rows * (p.pitch + p.scale_bytes) + 127) / 128 * 128;
+  p.stages = (kTail - p.x_bytes) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   // the down projection: tiles of the warps' strips
   p.down_tokens = fp4 || T <= 8 ? 8 : 16;
@@ -1541,7 +1593,7 @@ MoePlan make_plan(int T, int d_model, int n_experts, int top_k) {
   if (p.tile_cols > d_model) p.tile_cols = d_model;
   p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
   // 32 mod 128: four rows' loads do not meet in a bank
-  p.down_pitch = ((fp4 ? p.tile_cols / 2 + p.tile_cols / 32 : p.tile_cols * 2) + 95) / 128 * 128 + 32;
+  p.down_pitch = ((fp4 ? p.tile_cols / 2 : p.tile_cols * 2) + 95) / 128 * 128 + 32;
   p.down_stages = kTail / (kRowsStage * p.down_pitch);
   if (p.down_stages > kMaxStages) p.down_stages = kMaxStages;
   const long vecs = ((long)T * (d_model / 4) + 15) / 16;
