@@ -890,7 +890,7 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   if (st != QS_OK) return st;
   const Fp4GemmPlan plan = plan_fp4_gemm(T, d_in, d_out);
   if (!fp4_gemm_supported() ||
-      (long long)plan.mtiles * plan.ntiles * plan.nk >= (1ll << 31))
+      ((T + 127ll) / 128) * ((d_out + 127) / 128) * ((d_in + 255) / 256) >= (1ll << 31))
     return QS_ERR_UNSUPPORTED;
   WsView w{(unsigned char*)ws};
   cudaStream_t s = (cudaStream_t)stream;

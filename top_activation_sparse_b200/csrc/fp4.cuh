@@ -77,7 +77,7 @@ struct Fp4QuantArgs {
 cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, cudaStream_t s);
 
 struct Fp4GemmPlan {
-  int nt = 0;          // tokens per tile: 8, 16, 32, 64, 128 or 256
+  int nt = 0;          // tokens per tile: 8, 16, 32, 64 or 128; 256: fp4_gemm_wide.cu
   int mtiles = 0;      // tiles of 128 outputs
   int ntiles = 0;      // tiles of nt tokens
   int nk = 0;          // steps of 256 inputs
@@ -102,5 +102,7 @@ struct Fp4GemmArgs {
 };
 bool fp4_gemm_supported();
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t s);
+int fp4_wide_pairs();
+cudaError_t launch_fp4_gemm_wide(const Fp4GemmArgs& a, cudaStream_t s);
 
 }  // namespace qs

@@ -6,9 +6,9 @@
 // A product of two e2m1 numbers is a multiple of 1/4 of at most 36, so a
 // block's sum is exact; the scaled sums are added in float32.
 //
-// The weight is the MMA's M side (tiles of 128 outputs) whatever the number of
-// tokens, which are its N side (8 to 256): a few tokens then cost what the
-// weight's bytes cost, and many tokens fill 128 x 256 tiles.
+// The weight is the MMA's M side (tiles of 128 outputs), the tokens are its N side
+// (8 to 128): a few tokens then cost what the weight's bytes cost.  (Many tokens:
+// fp4_gemm_wide.cu.)
 //   * warp 0 copies steps of 256 inputs into a ring: 128 weight rows and the
 //     tile's tokens (128-byte rows, 128-byte swizzle, 2-D TMA) and the scales'
 //     512-byte tiles (plain bulk copies; their layout in global memory is the
@@ -49,14 +49,13 @@ constexpr int gmin(int a, int b) { return a < b ? a : b; }
 template <bool NV, int NT>
 struct GShape {
   static constexpr int kAtoms = kGK / (NV ? 16 : 32) / 4;    // 512-byte scale tiles per step (4 / 2)
-  static constexpr int kRT = NT > 128 ? 2 : 1;               // 128-row scale tiles of the tokens
   static constexpr int kB = NT * kGK / 2;
   static constexpr int kSfA = kAtoms * kSfTile;
-  static constexpr int kSfB = kAtoms * kRT * kSfTile;
+  static constexpr int kSfB = kAtoms * kSfTile;
   static constexpr int kStage = kGABytes + kB + kSfA + kSfB;
   static constexpr int kAcc = NT < 32 ? 32 : NT;             // accumulator columns (allocated)
-  static constexpr int kNacc = 2 * kAcc <= 256 ? 2 : 1;      // two accumulators up to 128 tokens
-  static constexpr int kSfCols = kAtoms * 4 * (1 + kRT);     // tensor-memory columns per stage
+  static constexpr int kNacc = 2;                            // accumulators
+  static constexpr int kSfCols = kAtoms * 8;                 // tensor-memory columns per stage
   static constexpr int kStages = gmin((kGSmemCap - 1024) / kStage, (512 - kNacc * kAcc) / kSfCols);
   static constexpr int kSmem = kStages * kStage + 1024;
   static_assert(kStage % 1024 == 0, "the swizzled tiles start on 1 KB");
@@ -221,13 +220,12 @@ __global__ void __launch_bounds__(kGThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---- copies ----
-      // a row's last step may have fewer scale tiles, the last tokens' tile only one of two
+      // a row's last step may have fewer scale tiles
       auto atoms_at = [&](int ks) { return gmin(S::kAtoms, (int)tpr - ks * S::kAtoms); };
-      auto token_tiles = [&](int nt) { return gmin(S::kRT, (a.T - nt * NT + 127) / 128); };
       auto copy_w = [&](const GWalk& w, int sl) {
         const int at = atoms_at(w.ks);
         const uint32_t st = base + (uint32_t)(sl * S::kStage);
-        mbar_arrive_expect_tx(&s_full[sl], (uint32_t)(kGABytes + S::kB + at * kSfTile * (1 + token_tiles(w.nt))));
+        mbar_arrive_expect_tx(&s_full[sl], (uint32_t)(kGABytes + S::kB + 2 * at * kSfTile));
         g_tma(st, &map_w, w.ks * (kGK / 2), w.mt * kGM, &s_full[sl]);
         g_bulk(st + kGABytes + S::kB, a.ws + ((size_t)w.mt * tpr + (size_t)w.ks * S::kAtoms) * kSfTile,
                (uint32_t)(at * kSfTile), &s_full[sl]);
@@ -236,11 +234,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
         const int at = atoms_at(w.ks);
         const uint32_t st = base + (uint32_t)(sl * S::kStage);
         g_tma(st + kGABytes, &map_x, w.ks * (kGK / 2), w.nt * NT, &s_full[sl]);
-        const int rts = token_tiles(w.nt);
-        for (int r = 0; r < rts; ++r)
-          g_bulk(st + kGABytes + S::kB + S::kSfA + (uint32_t)(r * S::kAtoms * kSfTile),
-                 a.xs + ((size_t)(w.nt * S::kRT + r) * tpr + (size_t)w.ks * S::kAtoms) * kSfTile,
-                 (uint32_t)(at * kSfTile), &s_full[sl]);
+        g_bulk(st + kGABytes + S::kB + S::kSfA, a.xs + ((size_t)w.nt * tpr + (size_t)w.ks * S::kAtoms) * kSfTile,
+               (uint32_t)(at * kSfTile), &s_full[sl]);
       };
       const int head = n < S::kStages ? n : S::kStages;
       GWalk w(P), wx(P);
@@ -286,10 +281,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
         for (int t = 0; t < S::kAtoms; ++t) {
           g_cp_sf(sfa + t * 4, g_desc(st + kGABytes + S::kB + t * kSfTile, 128, 0));
-#pragma unroll
-          for (int r = 0; r < S::kRT; ++r)
-            g_cp_sf(sfb + (t * S::kRT + r) * 4,
-                    g_desc(st + kGABytes + S::kB + S::kSfA + (r * S::kAtoms + t) * kSfTile, 128, 0));
+          g_cp_sf(sfb + t * 4, g_desc(st + kGABytes + S::kB + S::kSfA + t * kSfTile, 128, 0));
         }
         const int rest = a.d_in - ks * kGK;                    // inputs from this step on
 #pragma unroll
@@ -299,7 +291,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             const uint64_t bd = g_desc(st + kGABytes + kk * 32, 1024, 2);
             const int t = NV ? kk : kk >> 1;
             const uint32_t id = NV ? 0u : (uint32_t)(kk & 1) * 2u;
-            g_mma<NV>(acc, ad, bd, g_idesc<NV, NT>(id), sfa + t * 4, sfb + t * S::kRT * 4, fresh ? 0u : 1u);
+            g_mma<NV>(acc, ad, bd, g_idesc<NV, NT>(id), sfa + t * 4, sfb + t * 4, fresh ? 0u : 1u);
             fresh = false;
           }
         }
@@ -484,7 +476,6 @@ cudaError_t g_dispatch(const CUtensorMap& mw, const CUtensorMap& mx, const Fp4Ge
     case 32: return g_launch<NV, 32>(mw, mx, a, s);
     case 64: return g_launch<NV, 64>(mw, mx, a, s);
     case 128: return g_launch<NV, 128>(mw, mx, a, s);
-    case 256: return g_launch<NV, 256>(mw, mx, a, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -497,14 +488,14 @@ Fp4GemmPlan plan_fp4_gemm(int T, int d_in, int d_out) {
   Fp4GemmPlan p;
   p.mtiles = (d_out + kGM - 1) / kGM;
   p.nk = (d_in + kGK - 1) / kGK;
-  // tiles of 256 tokens where they give every SM one, else the smallest tile
-  // that holds the tokens (at most 128)
-  if (T > 128 && (long)p.mtiles * ((T + 255) / 256) >= kNumSMs) {
+  // tiles of 256 x 256 on two SMs where they give every pair one, else the
+  // smallest tile of 128 outputs that holds the tokens (at most 128)
+  if (T > 128 && fp4_wide_pairs() > 0 && (long)((T + 255) / 256) * ((d_out + 255) / 256) >= fp4_wide_pairs()) {
     p.nt = 256;
-  } else {
-    p.nt = 8;
-    while (p.nt < T && p.nt < 128) p.nt *= 2;
+    return p;
   }
+  p.nt = 8;
+  while (p.nt < T && p.nt < 128) p.nt *= 2;
   p.ntiles = (T + p.nt - 1) / p.nt;
   const long tiles = (long)p.mtiles * p.ntiles;
   // the largest cluster of which every tile has one at once, with at least 2
@@ -517,6 +508,7 @@ Fp4GemmPlan plan_fp4_gemm(int T, int d_in, int d_out) {
 }
 
 cudaError_t launch_fp4_gemm(const Fp4GemmArgs& a, cudaStream_t s) {
+  if (a.plan.nt == 256) return launch_fp4_gemm_wide(a, s);
   CUtensorMap mw, mx;
   if (!g_map(&mw, a.wc, (uint64_t)(a.d_in / 2), (uint64_t)a.d_out, kGM) ||
       !g_map(&mx, a.xc, (uint64_t)(a.d_in / 2), (uint64_t)a.T, (uint32_t)a.plan.nt))
