@@ -240,6 +240,9 @@ def _current_stream_ptr(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+_HERE_CONTEXT = contextlib.nullcontext()
+
+
 def _call_context(dev, stream):
     """Run a call's allocations and launch on the tensors' device, and on
     `stream` where one is given."""
@@ -247,9 +250,9 @@ def _call_context(dev, stream):
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != torch._C._cuda_getDevice():
         return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return _HERE_CONTEXT
 
 
 _ws_need: dict = {}
@@ -593,6 +596,15 @@ def _fp4_code(table, name):
     return table[name] if isinstance(name, str) else int(name)
 
 
+def _out8(spec, shape, like):
+    """A uint8 output on `like`'s device: spec as for _out, checked for placement."""
+    if spec is True:
+        return like.new_empty(shape, dtype=torch.uint8)
+    out = _out(spec, shape, torch.uint8, like.device)
+    _need_cuda(like, out)
+    return out
+
+
 def _scalar_f32(t, name):
     if t is not None and (t.numel() != 1 or t.dtype != torch.float32):
         raise ValueError(f"{name} must be one float32 on the device")
@@ -613,20 +625,20 @@ def qs_fp4_quantize(x: torch.Tensor, format="mx", scale_layout="tiled", tensor_s
     for scale_layout "rows", one flat array for "tiled" (all rows of x as one
     matrix); values [..., d]: the rounded x in its own type."""
     dev = _need_cuda(x, tensor_scale)
-    _scalar_f32(tensor_scale, "tensor_scale")
+    if tensor_scale is not None:
+        _scalar_f32(tensor_scale, "tensor_scale")
     fmt, lay = _fp4_code(_FP4_FORMATS, format), _fp4_code(_FP4_LAYOUTS, scale_layout)
     d = x.shape[-1]
     if d < 32 or d % 32:
         raise QSError("qs_fp4_quantize", QS_ERR_ALIGNMENT)
-    R = x.numel() // d
-    lead = tuple(x.shape[:-1])
+    R, lead = x.numel() // d, x.shape[:-1]
     with _call_context(dev, stream):
-        codes = _out(codes, lead + (d // 2,), torch.uint8, dev)
-        shape = lead + (d // (32 if fmt == QS_FP4_MX else 16),) if lay == QS_FP4_SCALES_ROWS else \
-            (qs_fp4_scale_bytes(R, d, fmt, lay),)
-        scales = _out(scales, shape, torch.uint8, dev)
-        values = _out(values, tuple(x.shape), x.dtype, dev)
-        _need_cuda(x, codes, scales, values)
+        codes = _out8(codes, (*lead, d // 2), x)
+        scales = _out8(scales, (*lead, d // (32 if fmt == QS_FP4_MX else 16)) if lay == QS_FP4_SCALES_ROWS else
+                       (qs_fp4_scale_bytes(R, d, fmt, lay),), x)
+        values = torch.empty_like(x) if values is True else _out(values, x.shape, x.dtype, dev)
+        if values is not None:
+            _need_cuda(x, values)
         _check("qs_fp4_quantize", lib().qs_fp4_quantize(
             x.data_ptr(), _dtype_code(x), R, d, fmt, _ptr(tensor_scale), lay, _ptr(codes),
             _ptr(scales), _ptr(values), _current_stream_ptr(dev)))

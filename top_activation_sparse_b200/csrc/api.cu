@@ -191,7 +191,6 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       if (T < 1 || d_in < 32 || d_out < 8 || d_in > QS_MAX_ROW || d_out > QS_MAX_ROW || k < 0 ||
           k > d_in || (d_in % 32) != 0 || (d_out % 8) != 0)
         return false;
-      L->xs_masked = take((size_t)T * d_in * sizeof(float));
       L->fp4_codes = take((size_t)T * (d_in / 2));
       // the NV form has more scales than the MX form
       L->fp4_scales = take(qs_fp4_scale_bytes(T, d_in, QS_FP4_NV, QS_FP4_SCALES_TILED));
@@ -901,15 +900,6 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   QS_TRY_CUDA(mark(0));
   Fp4QuantArgs q;
   q.x = x;
-  if (k < d_in) {
-    TopkArgs a;
-    a.x = x; a.T = T; a.d = d_in; a.k = k;
-    a.kind = dtype == QS_F32 ? TK_F32 : TK_BF16;
-    a.xs = w.at<void>(L.xs_masked);
-    a.status = w.status();
-    QS_TRY_CUDA(launch_topk(a, s));
-    q.x = a.xs;
-  }
   q.R = (size_t)T; q.d = d_in;
   q.bf16 = dtype == QS_BF16;
   q.format = format;
@@ -917,7 +907,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
   q.tensor_scale = x_scale;
   q.codes = w.at<uint8_t>(L.fp4_codes);
   q.scales = w.at<uint8_t>(L.fp4_scales);
-  QS_TRY_CUDA(launch_fp4_quantize(q, s));
+  q.k = k;
+  QS_TRY_CUDA(k < d_in ? launch_fp4_topk_quantize(q, s) : launch_fp4_quantize(q, s));
   QS_TRY_CUDA(mark(1));
   Fp4GemmArgs g;
   g.xc = q.codes; g.xs = q.scales;

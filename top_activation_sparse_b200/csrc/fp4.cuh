@@ -66,6 +66,7 @@ struct Fp4QuantArgs {
   size_t R = 0;
   int d = 0;
   int bf16 = 1;
+  int k = 0;                        // launch_fp4_topk_quantize: values kept per row
   int format = QS_FP4_MX;
   int tiled = 1;                    // scale layout
   int pad_rows = 1;                 // tiled: zero the scales of the rows behind the last
@@ -75,6 +76,9 @@ struct Fp4QuantArgs {
   void* values = nullptr;           // [R, d] in x's type, or NULL
 };
 cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, cudaStream_t s);
+// the k largest |x| of each row (ties: lower index), the rest 0; d <= QS_MAX_ROW,
+// tiled scales, no rows behind the last
+cudaError_t launch_fp4_topk_quantize(const Fp4QuantArgs& a, cudaStream_t s);
 
 struct Fp4GemmPlan {
   int nt = 0;          // tokens per tile: 8, 16, 32, 64 or 128; 256: fp4_gemm_wide.cu

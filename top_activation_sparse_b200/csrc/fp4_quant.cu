@@ -176,6 +176,168 @@ __global__ void __launch_bounds__(kQThreads) fp4_quant_kernel(Fp4QuantArgs a) {
   }
 }
 
+// ---- top-K and quantisation of a row in one kernel ------------------------------
+// One CTA per row; a thread keeps NV vectors of 8 neighbouring values in registers
+// (vector v of thread t: values (v * threads + t) * 8 ...), so that the row is
+// read once and only its codes and scales are written.  The K-th largest |x| (as
+// bits) is found by radix passes of 11, 10 and 10 bits (bf16: 11 and 4) on
+// histograms in shared memory: 2048 bins spread the few exponents that a row's
+// values share over enough addresses for the atomics.  Equal magnitudes at the
+// threshold are kept in index order, by one scan, where not all of them are.
+// Bound by latency for a few rows (the passes' barriers); with the masked row
+// written and read again between two kernels, 2048 rows of 4096 bf16 took 38 us,
+// this kernel MEASURE_T.
+template <int THREADS>
+__device__ __forceinline__ int block_exclusive(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int c = s_warp[w];
+    if (w < warp) before += c;
+    total += c;
+  }
+  return before + inc - v;
+}
+
+template <bool BF16, bool NV, int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS) fp4_topk_quant_kernel(Fp4QuantArgs a) {
+  constexpr int kBits = BF16 ? 15 : 31, kBins = 2048;
+  __shared__ int s_hist[kBins];
+  __shared__ int s_warp[THREADS / 32];
+  __shared__ int s_digit, s_above, s_equal;
+  const int tid = threadIdx.x, per = a.d / 8;
+  pdl_begin();
+  const float g = (NV && a.tensor_scale) ? *a.tensor_scale : 1.0f;
+  const size_t row0 = (size_t)blockIdx.x * per;        // first vector of the row
+  float f[VECS][8];
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    const int at = v * THREADS + tid;
+    if (at < per) {
+      load8<BF16>(a.x, row0 + at, f[v]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[v][i] = 0.0f;
+    }
+  }
+  auto key_of = [&](float x) { return (__float_as_uint(x) & 0x7fffffffu) >> (BF16 ? 16 : 0); };
+
+  // the threshold: digits from the top; `need` of the values that share the
+  // digits so far are kept
+  uint32_t prefix = 0;
+  int shift = kBits, need = a.k, equal = 0;
+  if (need > 0) {
+#pragma unroll 1
+    for (int pass = 0; shift > 0; ++pass) {
+      const int bits = min(pass == 0 ? 11 : 10, shift);
+      const uint32_t before = shift >= 31 ? 0u : prefix >> shift;     // digits so far
+      shift -= bits;
+      for (int i = tid; i < (1 << bits); i += THREADS) s_hist[i] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        if (v * THREADS + tid < per) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t k = key_of(f[v][i]);
+            if (pass == 0 || (k >> (shift + bits)) == before) atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+          }
+        }
+      }
+      __syncthreads();
+      // counts from the top: thread t has the bins of the t-th share from the top
+      const int n = 1 << bits, share = (n + THREADS - 1) / THREADS;
+      int mine = 0;
+      for (int i = 0; i < share; ++i) {
+        const int b = n - 1 - (tid * share + i);
+        if (b >= 0) mine += s_hist[b];
+      }
+      int total;
+      int above = block_exclusive<THREADS>(mine, s_warp, total);
+      if (above < need && above + mine >= need) {
+        for (int i = 0; i < share; ++i) {
+          const int b = n - 1 - (tid * share + i), c = s_hist[b];
+          if (above + c >= need) {
+            s_digit = b;
+            s_above = above;
+            s_equal = c;
+            break;
+          }
+          above += c;
+        }
+      }
+      __syncthreads();
+      prefix |= (uint32_t)s_digit << shift;
+      need -= s_above;
+      equal = s_equal;
+      if (equal == need && shift > 0) break;           // every value that shares these digits is kept
+      __syncthreads();
+    }
+  }
+  const uint32_t low = prefix;                         // keys >= low are kept, or (ties) == low by index
+  const bool ties = need > 0 && equal != need;
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    const int at = v * THREADS + tid;
+    int rank = 0;
+    if (ties) {
+      int c = 0, total;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c += at < per && key_of(f[v][i]) == low;
+      rank = block_exclusive<THREADS>(c, s_warp, total);
+      // (need: what is left for this vector's round and those after it)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t k = key_of(f[v][i]);
+        const bool keep = k > low || (k == low && rank < need);
+        rank += k == low;
+        if (!keep) f[v][i] = 0.0f;
+      }
+      need -= total;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (a.k == 0 || key_of(f[v][i]) < low) f[v][i] = 0.0f;
+    }
+    // (whole warps: a row is a multiple of 4 vectors, not of 32)
+    if (at - (tid & 31) < per) {
+      Fp4QuantArgs b = a;
+      if (at >= per) b.codes = nullptr, b.scales = nullptr, b.values = nullptr;
+      quant8<BF16, NV>(b, row0 + at, f[v], g, true);
+    }
+  }
+  // the blocks that fill the row's last scale tile are 0
+  const int nb = a.d / (NV ? 16 : 32);
+  const size_t tpr = fp4_tiles_per_row(nb);
+  for (int i = tid; i < (int)(tpr * 4) - nb; i += THREADS) a.scales[fp4_tiled_offset(blockIdx.x, nb + i, tpr)] = 0;
+}
+
+template <bool BF16, bool NV>
+cudaError_t launch_topk_quant(const Fp4QuantArgs& a, cudaStream_t s) {
+  const int per = a.d / 8;
+  const dim3 grid((unsigned)a.R);
+  // one vector per thread for a few rows (latency), two where rows queue for the
+  // SMs, more for long rows
+  if (per <= 128) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 128, 1>, grid, dim3(128), 0, s, a);
+  if (per <= 256) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 256, 1>, grid, dim3(256), 0, s, a);
+  if (per <= 512 && a.R > (size_t)kNumSMs * 2) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 256, 2>, grid, dim3(256), 0, s, a);
+  if (per <= 512) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 512, 1>, grid, dim3(512), 0, s, a);
+  if (per <= 1024) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 512, 2>, grid, dim3(512), 0, s, a);
+  if (per <= 2048) return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 1024, 2>, grid, dim3(1024), 0, s, a);
+  return launch_pdl(fp4_topk_quant_kernel<BF16, NV, 1024, 6>, grid, dim3(1024), 0, s, a);
+}
+
 }  // namespace
 
 cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, cudaStream_t s) {
@@ -196,6 +358,14 @@ cudaError_t launch_fp4_quantize(const Fp4QuantArgs& a, cudaStream_t s) {
     k = a.bf16 ? (nv ? fp4_quant_kernel<true, true, 1> : fp4_quant_kernel<true, false, 1>)
                : (nv ? fp4_quant_kernel<false, true, 1> : fp4_quant_kernel<false, false, 1>);
   cudaError_t e = launch_pdl(k, dim3((unsigned)grid), dim3(kQThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_topk_quantize(const Fp4QuantArgs& a, cudaStream_t s) {
+  const bool nv = a.format == QS_FP4_NV;
+  const cudaError_t e = a.bf16 ? (nv ? launch_topk_quant<true, true>(a, s) : launch_topk_quant<true, false>(a, s))
+                               : (nv ? launch_topk_quant<false, true>(a, s) : launch_topk_quant<false, false>(a, s));
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -220,7 +220,6 @@ struct WsLayout {
   size_t xq_h = 0;            // [T, d_ff] int8 dense masked codes of h (quantized ffn)
   size_t gamma_h = 0;         // [T] f32 (quantized ffn)
   size_t xs_bf16 = 0;         // [T, d_in] bf16 (prefill)
-  size_t xs_masked = 0;       // [T, d_in] X_sparse in x's type (4-bit projection)
   size_t fp4_codes = 0;       // [T, d_in/2] 4-bit codes of X_sparse
   size_t fp4_scales = 0;      // their scales, tiled
   size_t moe_logits = 0;      // [Tc, experts] f32 (mixture of experts)
