@@ -219,3 +219,150 @@ def test_linear_nan_block_stays_in_its_rows():
     assert torch.isnan(y[:, 5]).all()
     keep = [j for j in range(136) if j != 5]
     assert torch.equal(y[:, keep], y0[:, keep])
+
+
+# ---- the selection that feeds the projection ---------------------------------------------
+
+def _kept_through_identity(x, k, fmt, dtype):
+    """What the projection multiplies, read back through a weight that is the
+    identity on blocks of columns (exact in 4 bits: 1 = code 2, scale 1)."""
+    T, d = x.shape
+    eye = np.zeros((d, d), dtype=np.float32)
+    np.fill_diagonal(eye, 1.0)
+    w = qs.qs_fp4_quantize(to_dev(eye, "f32"), fmt, "tiled")
+    values = oracle.fp4_quantize(eye, fmt)["values"]
+    assert np.abs(values - eye).max() <= 2.0 ** -5
+    return _check_linear(x, k, fmt, dtype, "f32", w, values, 1.0)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_linear_ties_are_kept_in_index_order(dtype, fmt):
+    """Rows of few distinct magnitudes (more equal values than are kept), of one,
+    of zeros, and with both signs of zero."""
+    need_gpu()
+    g = workloads.rng(12)
+    d = 512
+    x = g.integers(-2, 3, size=(6, d)).astype(np.float32)
+    x[1] = 1.5
+    x[2] = 0.0
+    x[3, ::2] = -0.0
+    x[4] = 0.0
+    x[4, 100:140] = -3.0
+    x[5, :] = np.where(np.arange(d) % 3 == 0, 2.0, -2.0)
+    for k in (1, 7, 33, 100, 255, 511):
+        y = _kept_through_identity(x, k, fmt, dtype)
+        kept = to_np(y)[1] != 0
+        assert kept[:k].all() and not kept[k:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d", [(2, 1024), (2, 1056), (3, 2048), (2, 2080), (300, 2080), (297, 4096), (5, 4096),
+                                 (2, 4128), (2, 8192), (2, 8224), (1, 16384), (2, 16416), (1, 49152)])
+def test_linear_rows_of_every_length(T, d, dtype):
+    need_gpu()
+    g = workloads.rng(T + d)
+    x = workloads.normal_f32(g, (T, d))
+    if T > 1:
+        x[-1] = np.round(x[-1] * 2) / 2            # many ties
+    x = workloads.round_to_dtype(x, dtype)
+    fmt = "nv" if (d // 32) % 2 else "mx"
+    w, values, s = _weight(d, 72, d, fmt)
+    for k in (1, d // 3, d - 1):
+        _check_linear(x, k, fmt, dtype, "f32", w, values, s)
+
+
+def test_linear_equal_values_spread_over_the_row():
+    """Ties in more places than a short list of them holds, at every length class."""
+    need_gpu()
+    for d in (1024, 2048, 4096, 8192, 16384):
+        x = np.tile(np.array([1.0, -2.0, 0.5, 2.0], dtype=np.float32), (2, d // 4))
+        w, values, s = _weight(d, 40, d, "mx")
+        for k in (d // 4 + 3, d // 2, d // 2 + 1, d - 5):
+            _check_linear(x, k, "mx", "bf16", "f32", w, values, s)
+
+
+def test_linear_captured_and_replayed():
+    need_gpu()
+    g = workloads.rng(40)
+    x = to_dev(workloads.normal_f32(g, (9, 512)), "bf16")
+    w, values, s = _weight(41, 264, 512, "nv")
+    sc = torch.tensor([s], device="cuda")
+    call = lambda x: qs.qs_fp4_sparse_linear(x, w.codes, w.scales, 300, "nv", None, sc)  # noqa: E731
+    eager = call(x)
+    static = torch.zeros_like(x)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            q = qs.qs_fp4_quantize(static, "nv", "rows", values=True)
+            y = call(static)
+        graphs.append((graph, y, q))
+    static.copy_(x)
+    want = qs.qs_fp4_quantize(x, "nv", "rows", values=True)
+    for _ in range(3):
+        for graph, y, q in graphs:
+            graph.replay()
+            assert torch.equal(y, eager) and torch.equal(q.codes, want.codes) and torch.equal(q.values, want.values)
+    assert torch.equal(call(x), eager)
+
+
+def test_linear_on_two_streams_at_once():
+    need_gpu()
+    g = workloads.rng(42)
+    xs = [to_dev(workloads.normal_f32(g, (T, 1024)), "bf16") for T in (3, 40, 700)]
+    w, values, s = _weight(43, 6400, 1024, "mx")
+    want = [qs.qs_fp4_sparse_linear(x, w.codes, w.scales, 700) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for i, x in enumerate(xs):
+            got += [(i, qs.qs_fp4_sparse_linear(x, w.codes, w.scales, 700, stream=st)) for st in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
+
+
+def test_linear_rows_behind_the_last_are_left_as_they_were():
+    need_gpu()
+    g = workloads.rng(44)
+    for T, d_out in ((5, 136), (130, 264), (600, 6408)):
+        x = to_dev(workloads.normal_f32(g, (T, 96)), "bf16")
+        w, _, _ = _weight(d_out, d_out, 96, "mx")
+        buf = torch.full((T + 60, d_out), 7.0, device="cuda")
+        y = qs.qs_fp4_sparse_linear(x, w.codes, w.scales, 96, y=buf[:T])
+        assert bool((buf[T:] == 7.0).all())
+        assert torch.equal(y, qs.qs_fp4_sparse_linear(x, w.codes, w.scales, 96, y_dtype=torch.float32))
+
+
+def test_quantize_leaves_what_lies_behind_its_outputs():
+    need_gpu()
+    x = torch.randn(5, 96, device="cuda")
+    codes = torch.full((7, 48), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((512 + 64,), 9, dtype=torch.uint8, device="cuda")
+    values = torch.full((7, 96), 9.0, device="cuda")
+    qs.qs_fp4_quantize(x, "mx", "tiled", codes=codes[:5], scales=scales[:512], values=values[:5])
+    assert bool((codes[5:] == 9).all()) and bool((scales[512:] == 9).all()) and bool((values[5:] == 9).all())
+
+
+def test_refusals_on_the_device():
+    need_gpu()
+    x = torch.randn(3, 64, device="cuda")
+    w = qs.qs_fp4_quantize(torch.randn(16, 64, device="cuda"))
+    lin = qs.qs_fp4_sparse_linear
+    with pytest.raises(qs.QSError):
+        lin(x, w.codes, w.scales, 65)
+    with pytest.raises(qs.QSError):
+        lin(x, w.codes, w.scales, 8, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(qs.QSError):
+        lin(x[:0], w.codes, w.scales, 8)
+    for bad in (lambda: lin(x, w.codes[:, :16].contiguous(), w.scales, 8), lambda: lin(x, w.codes, w.scales[:-16], 8),
+                lambda: lin(x.t(), w.codes, w.scales, 8), lambda: lin(x, w.codes, w.scales, 8, w_scale=torch.ones(2, device="cuda")),
+                lambda: lin(x, w.codes.cpu(), w.scales, 8), lambda: qs.qs_fp4_quantize(x.t()),
+                lambda: qs.qs_fp4_quantize(x, tensor_scale=torch.ones(1, device="cuda", dtype=torch.float64))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: qs.qs_fp4_quantize(x[:, :40].contiguous()), lambda: qs.qs_fp4_quantize(x[:0]),
+                lambda: qs.qs_fp4_quantize(x, codes=None, scales=None)):
+        with pytest.raises(qs.QSError):
+            bad()

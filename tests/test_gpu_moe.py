@@ -14,8 +14,7 @@ import torch
 
 import oracle
 import top_activation_sparse_b200 as qs
-import workloads
-from gpu_common import bits, check_status, need_gpu, to_np
+from gpu_common import check_status, need_gpu, to_np
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -193,3 +192,128 @@ def test_rows_behind_the_last_are_left_as_they_were():
     buf = torch.full((9, 64), 7.0, device=DEV)
     qs.qs_moe_ffn(top_k=2, act="drelu", y=buf[:5], **a)
     assert bool((buf[5:] == 7.0).all()) and not bool((buf[:5] == 7.0).any())
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("T,dm", [(1, 4128), (1, 8192), (3, 8192), (20, 5120), (64, 8160)])
+def test_rows_longer_than_4096(T, dm, fp4):
+    run_check(T + dm, T, dm, 200, 4, 2, "drelu", fp4)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("dm,dff,E,top_k", [(544, 1000, 4, 2), (4096, 2056, 2, 2), (96, 49152, 1, 1), (2080, 4104, 8, 8)])
+def test_one_token(dm, dff, E, top_k, fp4):
+    """Rows whose scales the copies cannot bring (d_model not a multiple of 512),
+    several batches per CTA, a last batch that is not whole."""
+    run_check(dm + dff, 1, dm, dff, E, top_k, "drelu", fp4)
+    run_check(dm + dff, 1, dm, dff, E, top_k, "relu2_glu", fp4, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("T", [1, 3])
+def test_closed_batches(T, fp4):
+    """No neuron is open over many batches in a row (empty lists), then one is,
+    then its second factor is 0 as well."""
+    need_gpu()
+    dm, dff, E = 256, 40000, 1
+    a, vals = make(31, T, dm, dff, E, "drelu", fp4, bias=-100.0)
+    r = qs.qs_moe_ffn(top_k=1, act="drelu", y_dtype=torch.float32, **a)
+    assert torch.count_nonzero(r.y).item() == 0
+    a["b_gate"][:, 39990] = 50.0                       # open, but the second factor is closed
+    r = qs.qs_moe_ffn(top_k=1, act="drelu", y_dtype=torch.float32, **a)
+    assert torch.count_nonzero(r.y).item() == 0
+    a["b_gate"][:, 17] = a["b_up"][:, 17] = 50.0
+    a["b_gate"][:, 20011] = a["b_up"][:, 20011] = 50.0
+    r = qs.qs_moe_ffn(top_k=1, act="drelu", y_dtype=torch.float32, experts=True, weights=True, **a)
+    check(r, reference(a, vals, 1, "drelu"), dm, torch.float32)
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("T", [4, 20])
+def test_a_token_that_is_not_finite_stays_alone(T, fp4):
+    need_gpu()
+    a, vals = make(33, T, 128, 256, 4, "drelu", fp4)
+    want = reference(a, vals, 2, "drelu")
+    a["x"][2, 5] = float("nan")
+    r = qs.qs_moe_ffn(top_k=2, act="drelu", y_dtype=torch.float32, experts=True, weights=True, **a)
+    assert torch.isnan(r.y[2]).all()
+    keep = [t for t in range(T) if t != 2]
+    part = qs.MoeResult(r.y[keep], r.experts[keep], r.weights[keep])
+    check(part, {k: v[keep] for k, v in want.items()}, 128, torch.float32)
+
+
+def test_inputs_far_from_one():
+    """x of 2^-10 and 2^20 (beyond float16, into which 4-bit weights bring x), and zeros."""
+    need_gpu()
+    for fp4 in (False, True):
+        a, vals = make(34, 3, 128, 256, 4, "relu2_glu", fp4)
+        a["x"][0] *= 2.0 ** -10
+        a["x"][1] *= 2.0 ** 20
+        a["x"][2] = 0.0
+        r = qs.qs_moe_ffn(top_k=2, act="relu2_glu", y_dtype=torch.float32, experts=True, weights=True, **a)
+        want = reference(a, vals, 2, "relu2_glu")
+        check(qs.MoeResult(r.y[:2], r.experts[:2], r.weights[:2]), {k: v[:2] for k, v in want.items()}, 128, torch.float32)
+        assert torch.count_nonzero(r.y[2]).item() == 0 and r.experts[2].tolist() == [0, 1]
+
+
+def test_workspace_too_small_and_wrong_shapes_are_refused():
+    need_gpu()
+    a, _ = make(35, 2, 64, 64, 4, "drelu", False)
+    need = qs.qs_workspace_size(qs.QS_OP_MOE_FFN, 2, 64, 64, 2)
+    with pytest.raises(qs.QSError):
+        qs.qs_moe_ffn(top_k=2, act="drelu", ws=torch.zeros(need - 16, dtype=torch.uint8, device=DEV), **a)
+    for bad in (dict(x=a["x"].float()), dict(x=a["x"][:, :32]), dict(w_down=a["w_down"].transpose(1, 2)),
+                dict(w_router=a["w_router"][:3]), dict(b_gate=a["b_gate"].half()), dict(s_up=a["w_up"].to(torch.uint8))):
+        with pytest.raises(ValueError):
+            qs.qs_moe_ffn(top_k=2, act="drelu", **{**a, **bad})
+    for top_k in (0, 5):
+        with pytest.raises(qs.QSError):
+            qs.qs_moe_ffn(top_k=top_k, act="drelu", **a)
+    with pytest.raises(qs.QSError):
+        qs.qs_moe_ffn(top_k=2, act="drelu", **{**a, "x": a["x"][:0]})
+
+
+def test_operators_together_eager_and_captured():
+    """The layers of one block: weights quantised once, a 4-bit projection of
+    sparsified activations, then 4-bit experts on its output; each step against
+    the oracle on the step's own input, then the whole replayed."""
+    need_gpu()
+    T, d, dm, dff, E, K = 6, 512, 256, 320, 6, 2
+    a, vals = make(36, T, dm, dff, E, "drelu", True)
+    x = a.pop("x")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(2)
+    x = torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn(dm, d, generator=g, device=DEV) * d ** -0.5
+    wq = qs.qs_fp4_quantize(w, "mx", "tiled")
+
+    def block(x):
+        u = qs.qs_fp4_sparse_linear(x, wq.codes, wq.scales, 358)
+        return u, qs.qs_moe_ffn(u, top_k=K, act="drelu", y_dtype=torch.float32, experts=True, weights=True, **a)
+
+    u, r = block(x)
+    wv = oracle.fp4_quantize(w.cpu().numpy(), "mx")["values"]
+    ref = oracle.fp4_sparse_linear(x.float().cpu().numpy(), wv, 358, "mx")
+    # block sums in float32, then half a step of bf16
+    assert np.all(np.abs(to_np(u) - ref["y"]) <= (d / 32 + 8) * 2.0 ** -23 * ref["mag"] + 2.0 ** -8 * np.abs(ref["y"]))
+    check(r, reference({**a, "x": u}, vals, K, "drelu"), dm, torch.float32)
+
+    static = torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gu, gr = block(static)
+    static.copy_(x)
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(gu, u) and torch.equal(gr.y, r.y) and torch.equal(gr.experts, r.experts)
+    # the same on a stream of its own, while the default one is busy with the graph
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        graph.replay()
+        with torch.cuda.stream(s):
+            u2, r2 = block(x)
+        s.synchronize()
+        assert torch.equal(u2, u) and torch.equal(r2.y, r.y)
+    torch.cuda.synchronize()
+    assert torch.equal(gr.y, r.y)

@@ -243,12 +243,16 @@ def _current_stream_ptr(dev) -> int:
 _HERE_CONTEXT = contextlib.nullcontext()
 
 
-def _call_context(dev, stream):
+def _call_context(dev, stream, *tensors):
     """Run a call's allocations and launch on the tensors' device, and on
-    `stream` where one is given."""
+    `stream` where one is given: the caller's tensors, which may belong to
+    another stream, are then not reused before that stream is done with them."""
     if stream is not None:
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        for t in tensors:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
         return torch.cuda.stream(stream)
     if dev.index != torch._C._cuda_getDevice():
         return torch.cuda.device(dev)
@@ -632,7 +636,7 @@ def qs_fp4_quantize(x: torch.Tensor, format="mx", scale_layout="tiled", tensor_s
     if d < 32 or d % 32:
         raise QSError("qs_fp4_quantize", QS_ERR_ALIGNMENT)
     R, lead = x.numel() // d, x.shape[:-1]
-    with _call_context(dev, stream):
+    with _call_context(dev, stream, x, tensor_scale, codes, scales, values):
         codes = _out8(codes, (*lead, d // 2), x)
         scales = _out8(scales, (*lead, d // (32 if fmt == QS_FP4_MX else 16)) if lay == QS_FP4_SCALES_ROWS else
                        (qs_fp4_scale_bytes(R, d, fmt, lay),), x)
@@ -661,7 +665,7 @@ def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch
         raise ValueError("w_codes must be [d_out, d_in/2] uint8")
     if w_scales.dtype != torch.uint8 or w_scales.numel() != qs_fp4_scale_bytes(d_out, d_in, fmt, QS_FP4_SCALES_TILED):
         raise ValueError("w_scales must be the tiled uint8 scales of W [d_out, d_in]")
-    with _call_context(dev, stream):
+    with _call_context(dev, stream, x, w_codes, w_scales, x_scale, w_scale, y):
         y = _out(y if y is not None else True, (T, d_out), y.dtype if y is not None else (y_dtype or x.dtype), dev)
         _need_cuda(x, y)
         ws = _stream_workspace(ws, QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, dev)
@@ -703,7 +707,8 @@ def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, 
         if b is not None and (tuple(b.shape) != (E, d_ff) or b.dtype != torch.float32):
             raise ValueError("biases must be [E, d_ff] float32")
     act_code = _ACTS[act] if isinstance(act, str) else int(act)
-    with _call_context(dev, stream):
+    with _call_context(dev, stream, x, w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, b_gate, b_up, y,
+                       experts, weights):
         y = _out(y if y is not None else True, (T, d_model), y.dtype if y is not None else (y_dtype or x.dtype), dev)
         experts = _out(experts, (T, top_k), torch.int32, dev)
         weights = _out(weights, (T, top_k), torch.float32, dev)

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(THREADS) fp4_topk_quant_kernel(Fp4QuantArgs a)
   pdl_begin();
   const float g = (NV && a.tensor_scale) ? *a.tensor_scale : 1.0f;
   const size_t row0 = (size_t)blockIdx.x * per;        // first vector of the row
+  const bool small = row0 + per < (1ull << 32);
   float f[VECS][8];
 #pragma unroll
   for (int v = 0; v < VECS; ++v) {
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(THREADS) fp4_topk_quant_kernel(Fp4QuantArgs a)
     if (at - (tid & 31) < per) {
       Fp4QuantArgs b = a;
       if (at >= per) b.codes = nullptr, b.scales = nullptr, b.values = nullptr;
-      quant8<BF16, NV>(b, row0 + at, f[v], g, true);
+      quant8<BF16, NV>(b, row0 + at, f[v], g, small);
     }
   }
   // the blocks that fill the row's last scale tile are 0
