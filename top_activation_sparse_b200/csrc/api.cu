@@ -207,6 +207,8 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       L->moe_share = take(slots * sizeof(float));
       L->h = take(slots * d_out * sizeof(float));
       L->moe_xup = take((size_t)Tc * sizeof(float));
+      L->moe_xt = take((size_t)Tc * kMoeXTerms * (d_in / 2));
+      L->moe_xs = take((size_t)Tc * moe_xs_pitch(d_in));
       L->moe_nz = take((slots < kMoeMaxE ? slots : kMoeMaxE) * d_out);
       // (a shorter last chunk may split more; its rows are at most as many)
       L->parts1_elems = (size_t)kMoePartRows * d_in;
@@ -966,6 +968,8 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
   a.table = w.at<int32_t>(L.moe_table);
   a.share = w.at<float>(L.moe_share);
   a.xup = w.at<float>(L.moe_xup);
+  a.xt = w.at<uint8_t>(L.moe_xt);
+  a.xs = w.at<uint8_t>(L.moe_xs);
   a.h = w.at<float>(L.h);
   a.nz = w.at<uint8_t>(L.moe_nz);
   a.parts = w.at<float>(L.parts1);
@@ -976,7 +980,7 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
     a.y = (unsigned char*)y + (size_t)t0 * d_model * elem_bytes(y_dtype);
     a.experts = experts ? experts + (size_t)t0 * top_k : nullptr;
     a.weights = weights ? weights + (size_t)t0 * top_k : nullptr;
-    a.plan = (fp4 ? plan_moe_fp4 : plan_moe_bf16)(a.T, d_model, n_experts, top_k);
+    a.plan = (fp4 ? plan_moe_fp4 : plan_moe_bf16)(a.T, d_model, d_ff, n_experts, top_k);
     QS_TRY_CUDA((fp4 ? launch_moe_fp4 : launch_moe_bf16)(a, (cudaStream_t)stream));
   }
   return QS_OK;

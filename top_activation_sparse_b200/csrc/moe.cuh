@@ -29,9 +29,12 @@ struct MoePlan {
   int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
+  // 4-bit weights, kernels of their own before this one route, and compute (1) the
+  // first factors of all neurons, or (2) h (moe_fp4_dense.cu); 0: one kernel does all
+  int tensor = 0;
 };
-MoePlan plan_moe_bf16(int T, int d_model, int n_experts, int top_k);
-MoePlan plan_moe_fp4(int T, int d_model, int n_experts, int top_k);
+MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k);
+MoePlan plan_moe_fp4(int T, int d_model, int d_ff, int n_experts, int top_k);
 
 struct MoeArgs {
   const __nv_bfloat16* x = nullptr;       // [T, d_model]
@@ -59,7 +62,9 @@ struct MoeArgs {
   int32_t* table = nullptr;               // routing tables (see below)
   float* share = nullptr;                 // [T, top_k]
   float* xup = nullptr;                   // [T] power of two that takes x to float16 (4-bit weights)
-  float* h = nullptr;                     // [T * top_k, d_ff]
+  uint8_t* xt = nullptr;                  // [T, 8, d_model/2] x as eight 4-bit numbers (4-bit weights)
+  uint8_t* xs = nullptr;                  // [T, moe_xs_pitch] scale bytes of the first of them
+  float* h = nullptr;                     // [T * top_k, d_ff]; plan.tensor 1: first factors, then h
   uint8_t* nz = nullptr;                  // [min(E, T * top_k), d_ff]
   float* parts = nullptr;                 // [splits][T * top_k][d_model]
   DevStatus* status = nullptr;
@@ -67,6 +72,9 @@ struct MoeArgs {
 };
 cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_fp4_dense(const MoeArgs& a, cudaStream_t s);
+constexpr int kMoeXTerms = 8;
+__host__ __device__ constexpr int moe_xs_pitch(int d_model) { return (d_model / 32 + 31) / 32 * 32; }
 
 // routing tables, int32: [0] active experts A, then per active expert its
 // number, first slot and number of tokens, then per slot its token, then per

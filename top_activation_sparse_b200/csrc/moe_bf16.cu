@@ -8,6 +8,8 @@ constexpr bool kFp4 = false;
 #include "moe_kernel.cuh"
 
 namespace qs {
-MoePlan plan_moe_bf16(int T, int d_model, int n_experts, int top_k) { return make_plan(T, d_model, n_experts, top_k); }
+MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k) {
+  return make_plan(T, d_model, d_ff, n_experts, top_k);
+}
 cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s) { return launch(a, s); }
 }  // namespace qs

@@ -828,7 +828,7 @@ __device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, 
   const ExpertMats M = expert_mats<FP4>(a, u.e);
   const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
-    if (b < nb) {
+    if (b < nb && !(FP4 && a.plan.tensor)) {
       const int jb = u.j0 + b * u.batch;
       send_rows(R, at, sm, a.status, M.w1, M.s1, nullptr, jb, min(u.batch, u.j1 - jb), lane);
     }
@@ -878,6 +878,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
   constexpr int kStep = kMThreads / kTok;                // rows between a thread's places
   const float back = FP4 && c < u.nt ? 1.0f / sm.xup[sm.tok[c]] : 1.0f;
   const float share = ONE ? choice_share(a, sm, u.slot0) : 0.0f;
+  const bool given = FP4 && a.plan.tensor;               // the first factors are in a.h
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
     // (one body for both factors: the code of two does not stay in the
     // instruction cache)
@@ -897,7 +898,8 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         j[k] = r < n ? (list ? list[r] : jb + r) : -1;
         bias[k] = bs && j[k] >= 0 ? __ldg(bs + j[k]) : 0.0f;
       }
-      if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
+      if (given && !second) {}
+      else if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
       else dot_rows_bf16<KU, NG>(a, R, at, sm, P, x, n, lane);
       csync();
       if (!second) {
@@ -906,8 +908,12 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         for (int k = 0; k < kPer; ++k) {
           float v = 0.0f;
           if (j[k] >= 0 && c < u.nt) {
-            v = relu_nan(dot_sum(sm, P, tid + k * kMThreads) * back + bias[k]);
-            if (!a.drelu) v *= v;
+            if (given) {
+              v = __ldcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j[k]);
+            } else {
+              v = relu_nan(dot_sum(sm, P, tid + k * kMThreads) * back + bias[k]);
+              if (!a.drelu) v *= v;
+            }
           }
           sm.first[s][tid + k * kMThreads] = v;
           const unsigned any = __ballot_sync(0xffffffffu, v != 0.0f);
@@ -1439,6 +1445,83 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
   }
 }
 
+// ---- ahead of the tensor-core products (4-bit weights) ---------------------------
+// x as eight 4-bit numbers (moe_fp4_dense.cu): 8 values per thread, the four
+// threads of a block share its largest magnitude.
+__device__ void split_x(const MoeArgs& a, size_t v) {
+  const size_t n8 = (size_t)a.T * a.d_model / 8;
+  const uint32_t per = (uint32_t)a.d_model / 8, t = (uint32_t)v / per, at = (uint32_t)v - t * per;
+  float r[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (v < n8) {
+    const uint4 u = ld_x(a.x + v * 8);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[2 * i] = bf16lo(w[i]), r[2 * i + 1] = bf16hi(w[i]);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(r[i]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  if (v >= n8) return;
+  const bool finite = m < 0x7f800000u;
+  const int first = finite ? max((int)(m >> 23) - 1, 0) : 255;
+  if ((threadIdx.x & 3) == 0) a.xs[(size_t)t * moe_xs_pitch(a.d_model) + at / 4] = (uint8_t)first;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.xt) + (size_t)t * kMoeXTerms * per + at;
+#pragma unroll
+  for (int i = 0; i < kMoeXTerms; ++i) {
+    const uint32_t s = (uint32_t)max(first - 3 * i, 0);
+    const float inv = finite ? __uint_as_float((254u - s) << 23) : 0.0f, back = e8m0_value(s);
+    float q[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q[k] = finite ? r[k] * inv : 0.0f;
+    const uint32_t c = e2m1x8(q);
+    out[(size_t)i * per] = c;
+    uint32_t h[4];
+    e2m1x8_to_half2(c, h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+      r[2 * k] = fmaf(-e.x, back, r[2 * k]);
+      r[2 * k + 1] = fmaf(-e.y, back, r[2 * k + 1]);
+    }
+  }
+}
+
+// Blocks: the router's, of which the last to finish selects; x's powers; x's
+// terms, and what has to be cleared.
+__global__ void __launch_bounds__(kMThreads, 1) moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  Smem& sm = smem();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
+  const int routers = a.plan.router_items - a.plan.x_items;
+  pdl_begin();
+  if (b < routers) {
+    router_item(a, b, lane, warp);
+    if (finish(a.ctl + MC_ROUTED, sm) == routers - 1) {
+      __threadfence();
+      select_experts<false>(a, a.logits, true, lane, warp);
+      publish_routing(a, sm);
+      if (threadIdx.x == 0) a.ctl[MC_ROUTED] = 0;
+    }
+  } else if (b < a.plan.router_items) {
+    const int t = (b - routers) * kMWarps + warp;
+    if (t < a.T) {
+      const float u = x_power(a.x + (size_t)t * a.d_model, a.d_model, lane);
+      if (lane == 0) __stcg(a.xup + t, u);
+    }
+  } else {
+    const size_t i0 = (size_t)(b - a.plan.router_items) * kMThreads + threadIdx.x;
+    split_x(a, i0);
+    const size_t step = (size_t)(gridDim.x - a.plan.router_items) * kMThreads;
+    const int sb = a.d_model / 32, pitch = moe_xs_pitch(a.d_model), rest = pitch - sb;
+    for (size_t i = i0; i < (size_t)a.T * rest; i += step) a.xs[i / rest * pitch + sb + i % rest] = 0;
+    // flags that several passes set
+    if (a.plan.tensor == 2 && a.T > 16)
+      for (size_t i = i0; i < (size_t)min(a.E, a.T * a.top_k) * (a.d_ff / 8); i += step)
+        reinterpret_cast<uint2*>(a.nz)[i] = make_uint2(0u, 0u);
+  }
+}
+
 template <bool FP4, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant__ MoeArgs a) {
   Smem& sm = smem();
@@ -1496,7 +1579,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (computes) {
           if (P.local) {
             route_here(a, item == 0, lane, warp);
-          } else if (wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) {
+          } else if (P.tensor || wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) {
             fetch_routing(a, sm);
           } else if (threadIdx.x == 0) {
             sm.active = 0;              // no tables to go by
@@ -1558,16 +1641,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
 }
 
-MoePlan make_plan(int T, int d_model, int n_experts, int top_k) {
+#ifndef V_MIN
+#define V_MIN 4
+#endif
+#ifndef V_BOTH
+#define V_BOTH 2
+#endif
+MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
   p.grid = kNumSMs;
-  p.local = T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
-  p.x_items = (!p.local && fp4) ? (T + kMWarps - 1) / kMWarps : 0;
+  const long used = n_experts < T * top_k ? n_experts : T * top_k;
+  if (fp4 && used * d_ff * d_model / 2 >= ((long)V_MIN << 20)) p.tensor = T * top_k >= V_BOTH * n_experts ? 2 : 1;
+  p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
+  p.x_items = (!p.local && fp4 && p.tensor != 2) ? (T + kMWarps - 1) / kMWarps : 0;
   p.router_tokens = (long)T * n_experts <= kNumSMs * kMWarps ? 1 : 4;
   p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
-  p.one_token = T == 1 && d_model <= 4096;
-  p.hidden_items = p.grid;
+  p.one_token = T == 1 && d_model <= 4096 && p.tensor != 2;
+  p.hidden_items = p.tensor == 2 ? 0 : p.grid;
   // tokens per pass: two groups of 8 where x of both fits the registers; with
   // 4-bit weights as many as fit 64 KB of shared memory
   p.hidden_tokens = fp4 ? (d_model <= 4096 ? 8 : 4) : (d_model <= 4096 ? 16 : 8);
@@ -1610,7 +1701,21 @@ cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
   auto k = one ? moe_kernel<kFp4, true> : moe_kernel<kFp4, false>;
   cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[one ? 1 : 0]);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, a);
+  MoeArgs b = a;
+  if constexpr (kFp4) {
+    if (a.plan.tensor) {
+      static unsigned done_route = 0;
+      e = ensure_smem_attr(moe_route_kernel, (int)sizeof(Smem), &done_route);
+      if (e != cudaSuccess) return e;
+      const size_t splits = ((size_t)a.T * a.d_model / 8 + kMThreads - 1) / kMThreads;
+      e = launch_pdl(moe_route_kernel, dim3((unsigned)(a.plan.router_items + splits)), dim3(kMThreads), sizeof(Smem), s, a);
+      if (e != cudaSuccess) return e;
+      e = launch_moe_fp4_dense(a, s);
+      if (e != cudaSuccess) return e;
+      b.plan.router_items = b.plan.x_items = 0;
+    }
+  }
+  e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, b);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -226,6 +226,8 @@ struct WsLayout {
   size_t moe_table = 0;       // routing tables, int32
   size_t moe_share = 0;       // [Tc, top_k] f32
   size_t moe_xup = 0;         // [Tc] f32, 4-bit weights
+  size_t moe_xt = 0;          // [Tc, 8, d_model/2] codes of x, 4-bit weights
+  size_t moe_xs = 0;          // [Tc, moe_xs_pitch] their scale bytes
   size_t moe_nz = 0;          // [active experts, d_ff] flags
   size_t alpha_parts = 0;     // f64 partial sums (ternary pack)
   size_t alpha = 0;           // f32 (ternary pack)
