@@ -205,7 +205,7 @@ bool ws_layout(int op, int T, int d_in, int d_out, int k, WsLayout* L) {
       L->moe_logits = take((size_t)Tc * kMoeMaxE * sizeof(float));
       L->moe_table = take(kMtSize * sizeof(int32_t));
       L->moe_share = take(slots * sizeof(float));
-      L->h = take(slots * d_out * sizeof(float));
+      L->h = take(slots * d_out * 3 * sizeof(__nv_bfloat16));   // f32, or three bf16 numbers
       L->moe_xup = take((size_t)Tc * sizeof(float));
       L->moe_xt = take((size_t)Tc * kMoeXTerms * (d_in / 2));
       L->moe_xs = take((size_t)Tc * moe_xs_pitch(d_in));

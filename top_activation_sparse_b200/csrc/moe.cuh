@@ -30,7 +30,8 @@ struct MoePlan {
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
   // 4-bit weights, kernels of their own before this one route, and compute (1) the
-  // first factors of all neurons, or (2) h (moe_fp4_dense.cu); 0: one kernel does all
+  // first factors of all neurons (moe_fp4_dense.cu), or (2) h and the down projection's
+  // partial sums (moe_fp4_down.cu); 0: one kernel does all
   int tensor = 0;
 };
 MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k);
@@ -64,7 +65,8 @@ struct MoeArgs {
   float* xup = nullptr;                   // [T] power of two that takes x to float16 (4-bit weights)
   uint8_t* xt = nullptr;                  // [T, 8, d_model/2] x as eight 4-bit numbers (4-bit weights)
   uint8_t* xs = nullptr;                  // [T, moe_xs_pitch] scale bytes of the first of them
-  float* h = nullptr;                     // [T * top_k, d_ff]; plan.tensor 1: first factors, then h
+  float* h = nullptr;                     // [T * top_k, d_ff] (plan.tensor 1: first factors, then h);
+                                          // plan.tensor 2: [T * top_k, 3, d_ff] bf16
   uint8_t* nz = nullptr;                  // [min(E, T * top_k), d_ff]
   float* parts = nullptr;                 // [splits][T * top_k][d_model]
   DevStatus* status = nullptr;
@@ -73,6 +75,8 @@ struct MoeArgs {
 cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_dense(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s);
+constexpr int kMoeDownTokens = 40, kMoeDownCols = 512;    // moe_fp4_down.cu: per pass, per item
 constexpr int kMoeXTerms = 8;
 __host__ __device__ constexpr int moe_xs_pitch(int d_model) { return (d_model / 32 + 31) / 32 * 32; }
 

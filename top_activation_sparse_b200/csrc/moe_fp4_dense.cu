@@ -26,12 +26,12 @@
 //     its MMAs (N = 8 columns per token: tokens that a pass does not have cost
 //     nothing);
 //   * warps 2 to 5 add the terms and store: with one matrix the first factor,
-//     activated; with both h and the neuron's flag.
+//     activated; with both h, as three bf16 numbers.
 // Units of work (an expert, 128 of its neurons, up to 16 of its tokens) are dealt
 // out in turn; the passes of one tile are neighbours, so that the later ones
 // find the rows in L2.  Every wait is bounded.
 #include "fp4_mma.cuh"
-#include "moe.cuh"
+#include "moe_tables.cuh"
 
 namespace qs {
 namespace {
@@ -60,15 +60,7 @@ struct FUnit {
   int ai, e, m, slot0, nt, np;
 };
 
-// bounded tables of this call's routing
-struct FTables {
-  int16_t expert[kMoeMaxE], first[kMoeMaxE], count[kMoeMaxE];
-  int32_t cum[kMoeMaxE + 1];                    // passes before each active expert
-  int16_t token[kMoeMaxSlots];
-  int active;
-};
-
-__device__ __forceinline__ FUnit f_unit(const FTables& t, int u, int mtiles) {
+__device__ __forceinline__ FUnit f_unit(const MoeTables& t, int u, int mtiles) {
   int ai = 0;
   for (int step = kMoeMaxE / 2; step; step >>= 1)
     if (ai + step < t.active && t.cum[ai + step] * mtiles <= u) ai += step;
@@ -101,7 +93,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   __shared__ __align__(8) uint64_t s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ FTables tb;
+  __shared__ MoeTables tb;
 
   const MoeArgs& a = f.m;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -125,27 +117,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   pdl_begin();
-  // the routing
-  const int A = min(__ldcg(a.table), kMoeMaxE);
-  for (int i = tid; i < A; i += kFThreads) {
-    tb.expert[i] = (int16_t)__ldcg(a.table + kMtExpert + i);
-    tb.first[i] = (int16_t)__ldcg(a.table + kMtFirst + i);
-    tb.count[i] = (int16_t)__ldcg(a.table + kMtCount + i);
-  }
-  for (int i = tid; i < a.T * a.top_k; i += kFThreads) tb.token[i] = (int16_t)__ldcg(a.table + kMtToken + i);
-  if (tid == 0) tb.active = A;
-  __syncthreads();
-  for (int i = tid; i <= A; i += kFThreads) {
-    int n = 0;
-#pragma unroll 4
-    for (int k = 0; k < i; ++k) n += (tb.count[k] + kFTokens - 1) / kFTokens;
-    tb.cum[i] = n;
-  }
+  load_tables(a, tb, kFTokens, kFThreads);
   g_before();
   __syncthreads();
   g_after();
   const uint32_t tmem = s_tmem;
-  const int units = tb.cum[A] * mtiles;
+  const int units = tb.cum[tb.active] * mtiles;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -236,7 +213,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (!g_wait(&s_tfull[ab], (uint32_t)(piece / f.nacc) & 1u, &s_abort, a.status, 68)) break;
       g_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * MATS * f.acc);
-      bool any = false;
       for (int c = 0; c < x.nt; ++c) {
         uint32_t v[MATS][8];
 #pragma unroll
@@ -257,12 +233,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
           if (a.drelu) g = f_relu(g);
           h = h == 0.0f ? 0.0f : h * g;
         }
-        any |= h != 0.0f;
-        if (mine) __stcg(a.h + (size_t)(x.slot0 + c) * a.d_ff + j, h);
-      }
-      if constexpr (MATS == 2) {
-        // (several passes set one flag: cleared before, by the kernel that routes)
-        if (mine && (any || x.np == 1)) a.nz[(size_t)x.ai * a.d_ff + j] = any;
+        if constexpr (MATS == 1) {
+          if (mine) __stcg(a.h + (size_t)(x.slot0 + c) * a.d_ff + j, h);
+        } else {
+          // h as the sum of three bf16 numbers, for the down projection (an
+          // infinity or a NaN has no rest)
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.h) + (size_t)(x.slot0 + c) * 3 * a.d_ff + j;
+          const bool finite = fabsf(h) <= 3.0e38f;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(h);
+            if (mine) o[(size_t)i * a.d_ff] = b;
+            h = finite ? h - __bfloat162float(b) : 0.0f;
+          }
+        }
       }
       g_before();
       __syncwarp();

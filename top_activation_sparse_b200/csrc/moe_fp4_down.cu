@@ -1,0 +1,332 @@
+// Down projection of 4-bit experts for many tokens, on the tensor cores.
+//
+//   part[t, c] = sum_{j in a range} h[t, j] s[j, c / 32] q[j, c]
+//
+// The weights lie neuron by neuron with blocks along the columns: the sum runs
+// across their scales, so the block-scaled MMA does not fit.  They are expanded to
+// bf16 (exactly) on their way through shared memory and multiplied with h, which
+// is the sum of three bf16 numbers, i.e. has its 24 bits (kind::f16, M = 128:
+// three rows per token; N = 512 columns, whose sums fill tensor memory).
+//   * warp 0 copies the codes of 64 neurons x 512 columns per step, warp 2 the
+//     rows of h (2-D TMA, 128-byte swizzle);
+//   * warps 3 to 18 expand: a thread takes a block of 32 codes (16 bytes), 20
+//     instructions per 8 weights, and stores bf16 rows as the MMA reads them (N
+//     contiguous, swizzled).  The columns of a group of 8 are stored in the order
+//     0 4 1 5 2 6 3 7: a word's nibbles i and i + 4 make a pair without moves;
+//   * one thread of warp 1 issues the MMAs;
+//   * warps 3 to 6 add a token's three rows and store.
+// Bound by the expansion and by the tensor cores, both at about 1100 cycles a
+// step of 16 KB.  (In registers for mma.sync, 8 tokens at a time, moe_kernel.cuh:
+// 297 us for 32 tokens, 8 experts of 11008 x 4096; MEASURE_D here.)  Every wait is
+// bounded.
+#include "fp4_mma.cuh"
+#include "moe_tables.cuh"
+
+namespace qs {
+namespace {
+
+constexpr int kDExpand = 16;                    // warps that expand
+constexpr int kDThreads = (3 + kDExpand) * 32;
+constexpr int kDK = 64;                         // neurons per step
+constexpr int kDCols = kMoeDownCols;            // columns per item
+constexpr int kDCodes = kDK * kDCols / 2;       // 16 KB: two boxes of 128 bytes x 64 rows
+constexpr int kDB = kDK * kDCols * 2;           // 64 KB: eight boxes of 64 columns x 64 rows
+constexpr int kDBox = kDK * 128;                // 8 KB
+constexpr int kDA = 128 * kDK * 2;              // 16 KB
+constexpr int kDCodeStages = 3;
+constexpr int kDTenth = 10;                     // tokens per 32 rows (30 of them used)
+static_assert(kMoeDownTokens == 4 * kDTenth, "four quarters of 10 tokens");
+constexpr int kDSmem = 2 * (kDB + kDA) + kDCodeStages * kDCodes + 1024;
+
+struct DItem {
+  int e, ai, s, j0, j1, c0, cw, slot0, cnt, steps;
+};
+
+// The items: (expert, range of neurons, tile of columns), the split as in sum_item
+__device__ __forceinline__ int d_splits(const MoeArgs& a, const MoeTables& t) {
+  return max(1, a.plan.grid / (t.cum[t.active] * a.plan.col_tiles));
+}
+__device__ __forceinline__ int d_expert_splits(const MoeArgs& a, const MoeTables& t, int ai, int S) {
+  return min(S * (t.cum[ai + 1] - t.cum[ai]), a.plan.max_splits);
+}
+__device__ __forceinline__ DItem d_item(const MoeArgs& a, const MoeTables& t, int item, int S) {
+  DItem d;
+  int rest = item / a.plan.col_tiles, n = d_expert_splits(a, t, 0, S);
+  for (d.ai = 0; rest >= n; n = d_expert_splits(a, t, ++d.ai, S)) rest -= n;
+  d.s = rest;
+  d.e = t.expert[d.ai];
+  d.j0 = (int)((long long)(a.d_ff / 8) * d.s / n) * 8;
+  d.j1 = (int)((long long)(a.d_ff / 8) * (d.s + 1) / n) * 8;
+  d.c0 = item % a.plan.col_tiles * kDCols;
+  d.cw = min(kDCols, a.d_model - d.c0);
+  d.slot0 = t.first[d.ai];
+  d.cnt = t.count[d.ai];
+  d.steps = (d.j1 - d.j0 + kDK - 1) / kDK;
+  return d;
+}
+
+__device__ __forceinline__ uint32_t d_idesc(uint32_t n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ uint64_t d_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void d_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// nibbles c and c + 4 of a word as a pair of bf16 (see moe_kernel.cuh: the
+// magnitude read as value * 2^-126, one product for 2^126 and the scale)
+template <int C>
+__device__ __forceinline__ uint32_t d_pair(uint32_t p, uint32_t lo, uint32_t hi, bool big) {
+  const uint32_t m = C == 0 ? p << 6 : C == 1 ? p << 2 : C == 2 ? p >> 2 : p >> 6;
+  const uint32_t s = C == 3 ? p : p << (12 - 4 * C);
+  uint32_t v = (m & 0x01c001c0u) | (s & 0x80008000u);
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(lo));
+  if (big) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(hi));
+  return v;
+}
+
+__global__ void __launch_bounds__(kDThreads, 1)
+    moe_fp4_down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
+                        const __grid_constant__ MoeArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t s_cfull[kDCodeStages], s_cempty[kDCodeStages];
+  __shared__ __align__(8) uint64_t s_afull[2], s_bfull[2], s_empty[2];
+  __shared__ __align__(8) uint64_t s_tfull, s_tempty, s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ MoeTables tb;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sa = base + 2 * kDB, scodes = sa + 2 * kDA;
+  if (tid == 0) {
+    for (int i = 0; i < kDCodeStages; ++i) mbar_init(&s_cfull[i], 1), mbar_init(&s_cempty[i], kDExpand);
+    for (int i = 0; i < 2; ++i) mbar_init(&s_afull[i], 1), mbar_init(&s_bfull[i], kDExpand), mbar_init(&s_empty[i], 1);
+    mbar_init(&s_tfull, 1);
+    mbar_init(&s_tempty, 4);
+    mbar_init(&s_done, 1);
+    mbar_fence_init();
+    s_abort = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_begin();
+  load_tables(a, tb, kMoeDownTokens, kDThreads);
+  g_before();
+  __syncthreads();
+  g_after();
+  const uint32_t tmem = s_tmem;
+  const int S = d_splits(a, tb);
+  int items = 0;
+  for (int i = 0; i < tb.active; ++i) items += d_expert_splits(a, tb, i, S);
+  items *= a.plan.col_tiles;
+
+  if (warp == 0 || warp == 2) {
+    if (lane == 0) {
+      // ---- copies: codes (warp 0), h (warp 2) ----
+      const bool codes = warp == 0;
+      const int stages = codes ? kDCodeStages : 2;
+      uint64_t* full = codes ? s_cfull : s_afull;
+      uint64_t* empty = codes ? s_cempty : s_empty;
+      int n = 0, sl = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const DItem d = d_item(a, tb, it, S);
+        for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
+          const int nt = min(kMoeDownTokens, d.cnt - t0), quarters = (nt + kDTenth - 1) / kDTenth;
+          for (int ks = 0; ks < d.steps; ++ks, ++n) {
+            if (!(ok = g_wait(&empty[sl], ph ^ 1u, &s_abort, a.status, 90))) break;
+            const int j = d.j0 + ks * kDK;
+            if (codes) {
+              const int boxes = (d.cw + 255) / 256;
+              mbar_arrive_expect_tx(&full[sl], (uint32_t)(boxes * kDK * 128));
+              for (int b = 0; b < boxes; ++b)
+                g_tma(scodes + (uint32_t)(sl * kDCodes + b * kDK * 128), &map_w, d.c0 / 2 + b * 128, d.e * a.d_ff + j, &full[sl]);
+            } else {
+              mbar_arrive_expect_tx(&full[sl], (uint32_t)(quarters * 32 * 128));
+              for (int q = 0; q < quarters; ++q)
+                g_tma(sa + (uint32_t)(sl * kDA + q * 32 * 128), &map_h, j, (d.slot0 + t0 + q * kDTenth) * 3, &full[sl]);
+            }
+            if (++sl == stages) sl = 0, ph ^= 1u;
+          }
+        }
+      }
+      // after a give-up: let the copies in flight land
+      if (*(volatile int*)&s_abort)
+        for (int j = 0; j < stages && j < n; ++j) {
+          const int g = n - 1 - j;
+          mbar_wait(&full[g % stages], (uint32_t)(g / stages) & 1u);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMAs ----
+      int b = 0, piece = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const DItem d = d_item(a, tb, it, S);
+        for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
+          if (piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
+          g_after();
+          for (int ks = 0; ks < d.steps; ++ks) {
+            if (!(ok = g_wait(&s_afull[b], ph, &s_abort, a.status, 92))) break;
+            if (!(ok = g_wait(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
+            g_after();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int n = min(256, d.cw - half * 256);
+              if (n <= 0) break;
+#pragma unroll
+              for (int kk = 0; kk < kDK / 16; ++kk)
+                d_mma(tmem + half * 256, d_desc(sa + (uint32_t)(b * kDA + kk * 32), 16, 1024),
+                      d_desc(base + (uint32_t)(b * kDB + half * 4 * kDBox + kk * 2048), kDBox, 1024), d_idesc((uint32_t)n),
+                      ks > 0 || kk > 0);
+            }
+            g_commit(&s_empty[b]);
+            if ((b ^= 1) == 0) ph ^= 1u;
+          }
+          if (ok) g_commit(&s_tfull);
+        }
+      }
+      g_commit(&s_done);                    // every MMA issued has completed when this arrives
+      mbar_wait(&s_done, 0u);
+    }
+  } else {
+    // ---- expansion: rows (w & 7) * 8 + lane % 8 of a step, blocks of 32 columns
+    // (w >> 3) * 8 + lane / 8 and 4 further ----
+    const int w = warp - 3, r = (w & 7) * 8 + (lane & 7), cb = (w >> 3) * 8 + (lane >> 3);
+    const int sb = a.d_model / 32;
+    const uint32_t x7 = (uint32_t)(r & 7) << 4;
+    // codes: 16-byte chunk of the row in its box; bf16: 64 bytes of the row in theirs
+    uint32_t src[2], dst[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = cb + 4 * i;
+      src[i] = (uint32_t)((c >> 3) * kDK * 128 + r * 128) + ((uint32_t)((c & 7) << 4) ^ x7);
+      dst[i] = (uint32_t)((c >> 1) * kDBox + r * 128);
+    }
+    const uint32_t part = (uint32_t)(cb & 1) << 6;            // which half of the 128 bytes (4 i keeps it)
+    int csl = 0, b = 0, piece = 0;
+    uint32_t cph = 0, ph = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const DItem d = d_item(a, tb, it, S);
+      const uint8_t* sc = a.sd + ((size_t)d.e * a.d_ff + d.j0 + r) * sb + d.c0 / 32;
+      const int left = d.j1 - d.j0 - r;                       // rows from this thread's on
+      uint32_t next[2];
+      auto ahead = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          next[i] = ks * kDK < left && (cb + 4 * i) * 32 < d.cw ? (uint32_t)__ldg(sc + (size_t)ks * kDK * sb + cb + 4 * i) : 0u;
+      };
+      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
+        ahead(0);
+        for (int ks = 0; ks < d.steps; ++ks) {
+          const uint32_t s[2] = {next[0], next[1]};
+          const bool there = ks * kDK < left;
+          ahead(ks + 1);
+          if (!(ok = g_wait(&s_cfull[csl], cph, &s_abort, a.status, 94))) break;
+          uint32_t v[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
+                         : "r"(scodes + (uint32_t)(csl * kDCodes) + src[i])
+                         : "memory");
+          if (!(ok = g_wait(&s_empty[b], ph ^ 1u, &s_abort, a.status, 95))) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // (rows behind the range are 0: what lies there may be anything)
+            const uint32_t lo = ((s[i] < 128u ? s[i] + 126u : 254u) << 7) * 0x10001u;
+            const uint32_t hi = (s[i] == 255u ? 0x7fc0u : (s[i] > 128u ? s[i] - 1u : 127u) << 7) * 0x10001u;
+            const bool big = s[i] > 128u;
+            const uint32_t to = base + (uint32_t)(b * kDB) + dst[i];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t p = there ? v[i][c] : 0u;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + ((part + (uint32_t)(c << 4)) ^ x7)),
+                           "r"(d_pair<0>(p, lo, hi, big)), "r"(d_pair<1>(p, lo, hi, big)), "r"(d_pair<2>(p, lo, hi, big)),
+                           "r"(d_pair<3>(p, lo, hi, big))
+                           : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&s_cempty[csl]);
+            mbar_arrive(&s_bfull[b]);
+          }
+          if (++csl == kDCodeStages) csl = 0, cph ^= 1u;
+          if ((b ^= 1) == 0) ph ^= 1u;
+        }
+        if (!ok || w >= 4) continue;
+        // ---- results: 10 tokens per quarter of the lanes, three rows each ----
+        if (!(ok = g_wait(&s_tfull, (uint32_t)piece & 1u, &s_abort, a.status, 96))) break;
+        g_after();
+        const int q = warp & 3, tok = t0 + q * kDTenth + lane / 3;
+        const bool mine = lane < 30 && lane % 3 == 0 && tok < d.cnt;
+        const size_t slots = (size_t)a.T * a.top_k;
+        float* o = a.parts + ((size_t)d.s * slots + d.slot0 + (mine ? tok : 0)) * a.d_model + d.c0;
+        if (t0 + q * kDTenth < d.cnt)
+          for (int c = 0; c < d.cw; c += 8) {
+            uint32_t u[8];
+            g_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, u);
+            g_ld_wait();
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float f = d.steps > 0 ? __uint_as_float(u[i]) : 0.0f;      // (a range without neurons)
+              y[i] = (__shfl_down_sync(0xffffffffu, f, 2) + __shfl_down_sync(0xffffffffu, f, 1)) + f;
+            }
+            if (mine) {
+              __stcg(reinterpret_cast<float4*>(o + c), make_float4(y[0], y[2], y[4], y[6]));
+              __stcg(reinterpret_cast<float4*>(o + c + 4), make_float4(y[1], y[3], y[5], y[7]));
+            }
+          }
+        g_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_tempty);
+      }
+    }
+  }
+  g_before();
+  __syncthreads();
+  if (warp == 1) {
+    g_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s) {
+  CUtensorMap mw, mh;
+  if (!g_map(&mw, a.wd, (uint64_t)(a.d_model / 2), (uint64_t)a.E * a.d_ff, kDK)) return cudaErrorInvalidValue;
+  auto fn = g_encode_fn();
+  cuuint64_t dims[2] = {(cuuint64_t)a.d_ff, (cuuint64_t)a.T * a.top_k * 3};
+  cuuint64_t strides[1] = {(cuuint64_t)a.d_ff * 2};
+  cuuint32_t box[2] = {kDK, 32}, estr[2] = {1, 1};
+  if (fn(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.h, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  static unsigned configured = 0;
+  cudaError_t e = ensure_smem_attr(moe_fp4_down_kernel, kDSmem, &configured);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(moe_fp4_down_kernel, dim3((unsigned)kNumSMs), dim3(kDThreads), (size_t)kDSmem, s, mw, mh, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace qs

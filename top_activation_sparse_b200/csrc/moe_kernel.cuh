@@ -1489,7 +1489,7 @@ __device__ void split_x(const MoeArgs& a, size_t v) {
 }
 
 // Blocks: the router's, of which the last to finish selects; x's powers; x's
-// terms, and what has to be cleared.
+// terms.
 __global__ void __launch_bounds__(kMThreads, 1) moe_route_kernel(const __grid_constant__ MoeArgs a) {
   Smem& sm = smem();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
@@ -1515,10 +1515,6 @@ __global__ void __launch_bounds__(kMThreads, 1) moe_route_kernel(const __grid_co
     const size_t step = (size_t)(gridDim.x - a.plan.router_items) * kMThreads;
     const int sb = a.d_model / 32, pitch = moe_xs_pitch(a.d_model), rest = pitch - sb;
     for (size_t i = i0; i < (size_t)a.T * rest; i += step) a.xs[i / rest * pitch + sb + i % rest] = 0;
-    // flags that several passes set
-    if (a.plan.tensor == 2 && a.T > 16)
-      for (size_t i = i0; i < (size_t)min(a.E, a.T * a.top_k) * (a.d_ff / 8); i += step)
-        reinterpret_cast<uint2*>(a.nz)[i] = make_uint2(0u, 0u);
   }
 }
 
@@ -1592,7 +1588,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         routed = true;
         if constexpr (!ONE) {
           S = down_splits(a, sm);
-          nD = down_items(a, sm, S);
+          nD = P.tensor == 2 ? 0 : down_items(a, sm, S);
         }
       }
       if (i < P.hidden_items) {
@@ -1678,9 +1674,10 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   p.stages = (kTail - p.x_bytes) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   // the down projection: tiles of the warps' strips
-  p.down_tokens = fp4 || T <= 8 ? 8 : 16;
+  p.down_tokens = p.tensor == 2 ? kMoeDownTokens : fp4 || T <= 8 ? 8 : 16;
   const int strips = p.down_tokens == 8 ? kStrips<fp4> : kStrips<fp4> / 2;
   p.tile_cols = kMWarps * strips * (fp4 ? 128 : 64);
+  if (p.tensor == 2) p.tile_cols = kMoeDownCols;
   if (p.tile_cols > d_model) p.tile_cols = d_model;
   p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
   // 32 mod 128: four rows' loads do not meet in a bank
@@ -1711,6 +1708,8 @@ cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
       e = launch_pdl(moe_route_kernel, dim3((unsigned)(a.plan.router_items + splits)), dim3(kMThreads), sizeof(Smem), s, a);
       if (e != cudaSuccess) return e;
       e = launch_moe_fp4_dense(a, s);
+      if (e != cudaSuccess) return e;
+      if (a.plan.tensor == 2) e = launch_moe_fp4_down(a, s);
       if (e != cudaSuccess) return e;
       b.plan.router_items = b.plan.x_items = 0;
     }
