@@ -76,6 +76,7 @@ cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_dense(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_fp4_sum(const MoeArgs& a, cudaStream_t s);
 constexpr int kMoeDownTokens = 40, kMoeDownCols = 512;    // moe_fp4_down.cu: per pass, per item
 constexpr int kMoeXTerms = 8;
 __host__ __device__ constexpr int moe_xs_pitch(int d_model) { return (d_model / 32 + 31) / 32 * 32; }

@@ -34,6 +34,7 @@ constexpr int kDB = kDK * kDCols * 2;           // 64 KB: eight boxes of 64 colu
 constexpr int kDBox = kDK * 128;                // 8 KB
 constexpr int kDA = 128 * kDK * 2;              // 16 KB
 constexpr int kDCodeStages = 3;
+constexpr int kDAhead = 4;                      // steps by which scales are loaded ahead
 constexpr int kDTenth = 10;                     // tokens per 32 rows (30 of them used)
 static_assert(kMoeDownTokens == 4 * kDTenth, "four quarters of 10 tokens");
 constexpr int kDSmem = 2 * (kDB + kDA) + kDCodeStages * kDCodes + 1024;
@@ -82,14 +83,27 @@ __device__ __forceinline__ void d_mma(uint32_t d, uint64_t ad, uint64_t bd, uint
 
 // nibbles c and c + 4 of a word as a pair of bf16 (see moe_kernel.cuh: the
 // magnitude read as value * 2^-126, one product for 2^126 and the scale)
-template <int C>
-__device__ __forceinline__ uint32_t d_pair(uint32_t p, uint32_t lo, uint32_t hi, bool big) {
+template <int C, bool BIG>
+__device__ __forceinline__ uint32_t d_pair(uint32_t p, uint32_t lo, uint32_t hi) {
   const uint32_t m = C == 0 ? p << 6 : C == 1 ? p << 2 : C == 2 ? p >> 2 : p >> 6;
   const uint32_t s = C == 3 ? p : p << (12 - 4 * C);
   uint32_t v = (m & 0x01c001c0u) | (s & 0x80008000u);
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(lo));
-  if (big) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(hi));
+  if constexpr (BIG) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(hi));
   return v;
+}
+
+// a block of 32 codes with scale byte s, to 64 bytes of a row
+template <bool BIG>
+__device__ __forceinline__ void d_expand(const uint32_t (&v)[4], uint32_t s, uint32_t to, uint32_t part, uint32_t x7) {
+  const uint32_t lo = ((!BIG || s < 128u ? s + 126u : 254u) << 7) * 0x10001u;
+  const uint32_t hi = (s == 255u ? 0x7fc0u : (s > 128u ? s - 1u : 127u) << 7) * 0x10001u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + ((part + (uint32_t)(c << 4)) ^ x7)),
+                 "r"(d_pair<0, BIG>(v[c], lo, hi)), "r"(d_pair<1, BIG>(v[c], lo, hi)), "r"(d_pair<2, BIG>(v[c], lo, hi)),
+                 "r"(d_pair<3, BIG>(v[c], lo, hi))
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kDThreads, 1)
@@ -225,18 +239,22 @@ __global__ void __launch_bounds__(kDThreads, 1)
       const DItem d = d_item(a, tb, it, S);
       const uint8_t* sc = a.sd + ((size_t)d.e * a.d_ff + d.j0 + r) * sb + d.c0 / 32;
       const int left = d.j1 - d.j0 - r;                       // rows from this thread's on
-      uint32_t next[2];
-      auto ahead = [&](int ks) {
+      // scales, some steps ahead of their use (from DRAM)
+      uint32_t next[kDAhead][2];
+      auto ahead = [&](int ks, uint32_t (&to)[2]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          next[i] = ks * kDK < left && (cb + 4 * i) * 32 < d.cw ? (uint32_t)__ldg(sc + (size_t)ks * kDK * sb + cb + 4 * i) : 0u;
+          to[i] = ks * kDK < left && (cb + 4 * i) * 32 < d.cw ? (uint32_t)__ldg(sc + (size_t)ks * kDK * sb + cb + 4 * i) : 0u;
       };
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
-        ahead(0);
+#pragma unroll
+        for (int i = 0; i < kDAhead; ++i) ahead(i, next[i]);
         for (int ks = 0; ks < d.steps; ++ks) {
-          const uint32_t s[2] = {next[0], next[1]};
+          const uint32_t s[2] = {next[0][0], next[0][1]};
           const bool there = ks * kDK < left;
-          ahead(ks + 1);
+#pragma unroll
+          for (int i = 0; i + 1 < kDAhead; ++i) next[i][0] = next[i + 1][0], next[i][1] = next[i + 1][1];
+          ahead(ks + kDAhead, next[kDAhead - 1]);
           if (!(ok = g_wait(&s_cfull[csl], cph, &s_abort, a.status, 94))) break;
           uint32_t v[2][4];
 #pragma unroll
@@ -246,21 +264,17 @@ __global__ void __launch_bounds__(kDThreads, 1)
                          : "r"(scodes + (uint32_t)(csl * kDCodes) + src[i])
                          : "memory");
           if (!(ok = g_wait(&s_empty[b], ph ^ 1u, &s_abort, a.status, 95))) break;
+          // (rows behind the range are 0: what lies there may be anything)
+          if (!there) v[0][0] = v[0][1] = v[0][2] = v[0][3] = v[1][0] = v[1][1] = v[1][2] = v[1][3] = 0u;
+          // scales above 2 take a second factor (seldom: a warp at a time)
+          if (__any_sync(0xffffffffu, max(s[0], s[1]) > 128u)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // (rows behind the range are 0: what lies there may be anything)
-            const uint32_t lo = ((s[i] < 128u ? s[i] + 126u : 254u) << 7) * 0x10001u;
-            const uint32_t hi = (s[i] == 255u ? 0x7fc0u : (s[i] > 128u ? s[i] - 1u : 127u) << 7) * 0x10001u;
-            const bool big = s[i] > 128u;
-            const uint32_t to = base + (uint32_t)(b * kDB) + dst[i];
+            for (int i = 0; i < 2; ++i)
+              d_expand<true>(v[i], s[i], base + (uint32_t)(b * kDB) + dst[i], part, x7);
+          } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t p = there ? v[i][c] : 0u;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + ((part + (uint32_t)(c << 4)) ^ x7)),
-                           "r"(d_pair<0>(p, lo, hi, big)), "r"(d_pair<1>(p, lo, hi, big)), "r"(d_pair<2>(p, lo, hi, big)),
-                           "r"(d_pair<3>(p, lo, hi, big))
-                           : "memory");
-            }
+            for (int i = 0; i < 2; ++i)
+              d_expand<false>(v[i], s[i], base + (uint32_t)(b * kDB) + dst[i], part, x7);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
@@ -309,7 +323,55 @@ __global__ void __launch_bounds__(kDThreads, 1)
   }
 }
 
+// y from the partial sums, in the order of the ranges and then of the choices:
+// 4 outputs per thread.
+constexpr int kSThreads = 128;
+__global__ void __launch_bounds__(kSThreads) moe_fp4_sum_kernel(const __grid_constant__ MoeArgs a) {
+  __shared__ MoeTables tb;
+  pdl_begin();
+  load_tables(a, tb, kMoeDownTokens, kSThreads);
+  __syncthreads();
+  const int S = d_splits(a, tb), n4 = a.d_model / 4;
+  const long long i = (long long)blockIdx.x * kSThreads + threadIdx.x;
+  if (i >= (long long)a.T * n4) return;
+  const int t = (int)(i / n4), c = (int)(i - (long long)t * n4) * 4;
+  const size_t slots = (size_t)a.T * a.top_k;
+  float4 y = make_float4(0, 0, 0, 0);
+  for (int j = 0; j < a.top_k; ++j) {
+    const int slot = __ldcg(a.table + kMtSlot + t * a.top_k + j);
+    const float p = __ldcg(a.share + t * a.top_k + j);
+    int ai = 0;
+    for (int step = kMoeMaxE / 2; step; step >>= 1)
+      if (ai + step < tb.active && tb.first[ai + step] <= slot) ai += step;
+    const int n = d_expert_splits(a, tb, ai, S);
+    const float* src = a.parts + (size_t)slot * a.d_model + c;
+    float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)s * slots * a.d_model));
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    y.x = fmaf(p, v.x, y.x), y.y = fmaf(p, v.y, y.y), y.z = fmaf(p, v.z, y.z), y.w = fmaf(p, v.w, y.w);
+  }
+  const size_t o = (size_t)t * a.d_model + c;
+  if (a.y_bf16) {
+    uint2 b;
+    b.x = (uint32_t)f32_to_bf16_bits(y.x) | ((uint32_t)f32_to_bf16_bits(y.y) << 16);
+    b.y = (uint32_t)f32_to_bf16_bits(y.z) | ((uint32_t)f32_to_bf16_bits(y.w) << 16);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.y) + o) = b;
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.y) + o) = y;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_moe_fp4_sum(const MoeArgs& a, cudaStream_t s) {
+  const size_t blocks = ((size_t)a.T * (a.d_model / 4) + kSThreads - 1) / kSThreads;
+  const cudaError_t e = launch_pdl(moe_fp4_sum_kernel, dim3((unsigned)blocks), dim3(kSThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
 
 cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s) {
   CUtensorMap mw, mh;

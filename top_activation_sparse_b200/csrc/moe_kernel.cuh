@@ -1588,7 +1588,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         routed = true;
         if constexpr (!ONE) {
           S = down_splits(a, sm);
-          nD = P.tensor == 2 ? 0 : down_items(a, sm, S);
+          nD = down_items(a, sm, S);
         }
       }
       if (i < P.hidden_items) {
@@ -1654,7 +1654,7 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   p.router_tokens = (long)T * n_experts <= kNumSMs * kMWarps ? 1 : 4;
   p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
   p.one_token = T == 1 && d_model <= 4096 && p.tensor != 2;
-  p.hidden_items = p.tensor == 2 ? 0 : p.grid;
+  p.hidden_items = p.grid;
   // tokens per pass: two groups of 8 where x of both fits the registers; with
   // 4-bit weights as many as fit 64 KB of shared memory
   p.hidden_tokens = fp4 ? (d_model <= 4096 ? 8 : 4) : (d_model <= 4096 ? 16 : 8);
@@ -1709,8 +1709,10 @@ cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
       if (e != cudaSuccess) return e;
       e = launch_moe_fp4_dense(a, s);
       if (e != cudaSuccess) return e;
-      if (a.plan.tensor == 2) e = launch_moe_fp4_down(a, s);
-      if (e != cudaSuccess) return e;
+      if (a.plan.tensor == 2) {
+        e = launch_moe_fp4_down(a, s);
+        return e != cudaSuccess ? e : launch_moe_fp4_sum(a, s);
+      }
       b.plan.router_items = b.plan.x_items = 0;
     }
   }
