@@ -184,39 +184,45 @@ __global__ void __launch_bounds__(kDThreads, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMAs ----
-      int b = 0, piece = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-        const DItem d = d_item(a, tb, it, S);
-        for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
-          if (piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
+    // ---- MMAs.  (The whole warp goes through the steps, one lane issues: what the
+    // instructions take is then uniform and need not be moved there lane by lane) ----
+    const bool issues = g_elect();
+    const uint64_t a0 = d_desc(sa, 16, 1024), b0 = d_desc(base, kDBox, 1024);
+    int b = 0, piece = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const DItem d = d_item(a, tb, it, S);
+      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
+        if (piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
+        g_after();
+        const uint32_t id0 = d_idesc((uint32_t)min(256, d.cw)), id1 = d_idesc((uint32_t)max(16, d.cw - 256));
+        for (int ks = 0; ks < d.steps; ++ks) {
+          // (h has arrived too: the first expanding warp has waited for it)
+          if (!(ok = g_wait(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
           g_after();
-          for (int ks = 0; ks < d.steps; ++ks) {
-            if (!(ok = g_wait(&s_afull[b], ph, &s_abort, a.status, 92))) break;
-            if (!(ok = g_wait(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
-            g_after();
+          const uint64_t ad = a0 + (uint64_t)(b * (kDA / 16)), bd = b0 + (uint64_t)(b * (kDB / 16));
+          if (issues) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const int n = min(256, d.cw - half * 256);
-              if (n <= 0) break;
+              if (half * 256 >= d.cw) break;
 #pragma unroll
               for (int kk = 0; kk < kDK / 16; ++kk)
-                d_mma(tmem + half * 256, d_desc(sa + (uint32_t)(b * kDA + kk * 32), 16, 1024),
-                      d_desc(base + (uint32_t)(b * kDB + half * 4 * kDBox + kk * 2048), kDBox, 1024), d_idesc((uint32_t)n),
-                      ks > 0 || kk > 0);
+                d_mma(tmem + half * 256, ad + kk * 2, bd + half * (4 * kDBox / 16) + kk * 128, half ? id1 : id0, ks > 0 || kk > 0);
             }
             g_commit(&s_empty[b]);
-            if ((b ^= 1) == 0) ph ^= 1u;
           }
-          if (ok) g_commit(&s_tfull);
+          __syncwarp();
+          if ((b ^= 1) == 0) ph ^= 1u;
         }
+        if (ok && issues) g_commit(&s_tfull);
       }
+    }
+    if (issues) {
       g_commit(&s_done);                    // every MMA issued has completed when this arrives
       mbar_wait(&s_done, 0u);
     }
+    __syncwarp();
   } else {
     // ---- expansion: rows (w & 7) * 8 + lane % 8 of a step, blocks of 32 columns
     // (w >> 3) * 8 + lane / 8 and 4 further ----
@@ -278,10 +284,10 @@ __global__ void __launch_bounds__(kDThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&s_cempty[csl]);
-            mbar_arrive(&s_bfull[b]);
-          }
+          if (lane == 0) mbar_arrive(&s_cempty[csl]);
+          // (one wait per step for the warp that issues the MMAs)
+          if (w == 0 && !(ok = g_wait(&s_afull[b], ph, &s_abort, a.status, 92))) break;
+          if (lane == 0) mbar_arrive(&s_bfull[b]);
           if (++csl == kDCodeStages) csl = 0, cph ^= 1u;
           if ((b ^= 1) == 0) ph ^= 1u;
         }
