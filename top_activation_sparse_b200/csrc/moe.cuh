@@ -16,7 +16,6 @@ struct MoePlan {
   int grid = 0;
   int local = 0;            // every CTA evaluates the router for itself
   int one_token = 0;        // a CTA goes on from its neurons to their down rows
-  int router_tokens = 1;    // tokens of a router task
   int router_items = 0;     // queue items of the router
   int x_items = 0;          // ... of which look for x's powers (4-bit weights)
   int hidden_items = 0;     // ... of the hidden layer

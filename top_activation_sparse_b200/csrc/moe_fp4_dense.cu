@@ -152,54 +152,59 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- scales to tensor memory, MMAs ----
-      int sl = 0, sfsl = 0, piece = 0;
-      uint32_t ph = 0, sfph = 0;
-      bool ok = true;
-      const uint32_t sfcols = tmem + (uint32_t)(f.nacc * MATS * f.acc);
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++piece) {
-        const FUnit x = f_unit(tb, u, mtiles);
-        const uint32_t n = (uint32_t)x.nt * 8u;
-        const int ab = piece % f.nacc;
-        if (piece >= f.nacc && !(ok = g_wait(&s_tempty[ab], (uint32_t)(piece / f.nacc - 1) & 1u, &s_abort, a.status, 65))) break;
+    // ---- scales to tensor memory, MMAs.  (The whole warp goes through the steps, one
+    // lane issues: what the instructions take is then uniform and need not be moved there
+    // lane by lane) ----
+    const bool issues = g_elect();
+    int sl = 0, sfsl = 0, piece = 0;
+    uint32_t ph = 0, sfph = 0;
+    bool ok = true;
+    const uint32_t sfcols = tmem + (uint32_t)(f.nacc * MATS * f.acc);
+    const uint64_t d0 = g_desc(base, 1024, 2), s0 = g_desc(sf0, 128, 0);
+    for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++piece) {
+      const FUnit x = f_unit(tb, u, mtiles);
+      const uint32_t id0 = f_idesc(0u, (uint32_t)x.nt * 8u), id1 = f_idesc(2u, (uint32_t)x.nt * 8u);
+      const int ab = piece % f.nacc;
+      if (piece >= f.nacc && !(ok = g_wait(&s_tempty[ab], (uint32_t)(piece / f.nacc - 1) & 1u, &s_abort, a.status, 65))) break;
+      g_after();
+      const uint32_t acc = tmem + (uint32_t)(ab * MATS * f.acc);
+      for (int ks = 0; ks < nk; ++ks) {
+        const int in = ks % kChunk;
+        if (in == 0 && !(ok = g_wait(&s_sffull[sfsl], sfph, &s_abort, a.status, 66))) break;
+        if (!(ok = g_wait(&s_full[sl], ph, &s_abort, a.status, 67))) break;
         g_after();
-        const uint32_t acc = tmem + (uint32_t)(ab * MATS * f.acc);
-        for (int ks = 0; ks < nk; ++ks) {
-          const int in = ks % kChunk;
-          if (in == 0 && !(ok = g_wait(&s_sffull[sfsl], sfph, &s_abort, a.status, 66))) break;
-          if (!(ok = g_wait(&s_full[sl], ph, &s_abort, a.status, 67))) break;
-          g_after();
-          const uint32_t st = base + (uint32_t)(sl * f.stage_bytes);
-          const uint32_t sfs = sf0 + (uint32_t)sfsl * kSfSlot + (uint32_t)(in * 2 * kSfTile);
-          const uint32_t sfc = sfcols + (uint32_t)(sl * (MATS + 1) * 8);
+        const uint64_t st = d0 + (uint64_t)(sl * (f.stage_bytes / 16));
+        const uint64_t sfs = s0 + (uint64_t)(sfsl * (int)(kSfSlot / 16) + in * (2 * kSfTile / 16));
+        const uint32_t sfc = sfcols + (uint32_t)(sl * (MATS + 1) * 8);
+        const int rest = a.d_model - ks * kGK;
+        if (issues) {
 #pragma unroll
           for (int o = 0; o <= MATS; ++o)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) g_cp_sf(sfc + o * 8 + t * 4, g_desc(sfs + o * kSfOp + t * kSfTile, 128, 0));
-          const int rest = a.d_model - ks * kGK;
+            for (int t = 0; t < 2; ++t) g_cp_sf(sfc + o * 8 + t * 4, sfs + o * (kSfOp / 16) + t * (kSfTile / 16));
 #pragma unroll
           for (int kk = 0; kk < kGK / 64; ++kk)
             if (kk * 64 < rest) {
-              const uint64_t bd = g_desc(st + MATS * kFABytes + kk * 32, 1024, 2);
-              const uint32_t id = f_idesc((uint32_t)(kk & 1) * 2u, n);
 #pragma unroll
               for (int o = 0; o < MATS; ++o)
-                g_mma<false>(acc + o * f.acc, g_desc(st + o * kFABytes + kk * 32, 1024, 2), bd, id, sfc + o * 8 + (kk >> 1) * 4,
-                             sfc + MATS * 8 + (kk >> 1) * 4, ks > 0 || kk > 0);
+                g_mma<false>(acc + o * f.acc, st + o * (kFABytes / 16) + kk * 2, st + MATS * (kFABytes / 16) + kk * 2,
+                             (kk & 1) ? id1 : id0, sfc + o * 8 + (kk >> 1) * 4, sfc + MATS * 8 + (kk >> 1) * 4, ks > 0 || kk > 0);
             }
           g_commit(&s_empty[sl]);
-          if (in == kChunk - 1 || ks == nk - 1) {
-            g_commit(&s_sfempty[sfsl]);
-            if (++sfsl == kSfRing) sfsl = 0, sfph ^= 1u;
-          }
-          if (++sl == f.stages) sl = 0, ph ^= 1u;
+          if (in == kChunk - 1 || ks == nk - 1) g_commit(&s_sfempty[sfsl]);
         }
-        if (ok) g_commit(&s_tfull[ab]);
+        __syncwarp();
+        if (in == kChunk - 1 || ks == nk - 1)
+          if (++sfsl == kSfRing) sfsl = 0, sfph ^= 1u;
+        if (++sl == f.stages) sl = 0, ph ^= 1u;
       }
+      if (ok && issues) g_commit(&s_tfull[ab]);
+    }
+    if (issues) {
       g_commit(&s_done);                    // every MMA issued has completed when this arrives
       mbar_wait(&s_done, 0u);
     }
+    __syncwarp();
   } else if (warp < 6) {
     // ---- results ----
     const int q = warp & 3;

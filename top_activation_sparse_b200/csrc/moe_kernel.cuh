@@ -15,7 +15,7 @@
 //
 // One launch, no grid barrier: CTAs draw items from one queue (an atomic
 // counter), in four kinds, in this order:
-//   router  logits of 8 experts x 8 tokens per item; the CTA that finishes the
+//   router  logits of 16 experts x 8 tokens per item; the CTA that finishes the
 //           last of them selects the experts and lists each expert's tokens;
 //   hidden  an equal share of the active experts' neurons: first factor, then
 //           the second for the open neurons, h, and a flag per neuron;
@@ -75,7 +75,7 @@ struct Smem {
       __nv_bfloat16 h[3][8 * kMaxNg * kHPitch];
       uint16_t list[kListD];
     } d;
-    int sel[kMoeMaxSlots];
+    int sel[kMoeMaxSlots + kMoeMaxE];            // choices by expert, then tokens per expert
   };
   float first[2][kBatch * 8];                    // first factors of two batches
   int rows[2][kBatch];                           // their open neurons
@@ -206,41 +206,39 @@ __device__ __forceinline__ bool ring_wait(uint64_t* b, uint32_t parity, Smem& sm
 }
 
 // ---- router ------------------------------------------------------------------
-// item: a task per warp, of one expert and router_tokens tokens
-__device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
-  const int nt = a.plan.router_tokens, groups = (a.T + nt - 1) / nt;
-  const int task = item * kMWarps + warp;
-  if (task >= a.E * groups) return;
-  const int e = task / groups, t0 = (task % groups) * nt;
-  const __nv_bfloat16* w = a.router + (size_t)e * a.d_model;
-  const __nv_bfloat16* px[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) px[t] = a.x + (size_t)min(t0 + min(t, nt - 1), a.T - 1) * a.d_model;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto add = [&](const uint4& wv, const uint4& xv, float& v) {
-    const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w}, xx[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v = fmaf(bf16lo(ww[i]), bf16lo(xx[i]), v);
-      v = fmaf(bf16hi(ww[i]), bf16hi(xx[i]), v);
-    }
-  };
-  if (nt == 1) {
+// Partial logits of 16 experts x 8 tokens (16 x 8 matrix instructions; the warps
+// share d_model) to part[expert * 8 + token] of each warp.
+__device__ __forceinline__ void router_tile(const MoeArgs& a, int e0, int t0, float* part, int lane, int warp) {
+  const int g = lane >> 2, q = lane & 3, units = a.d_model / 32;
+  const bool ok0 = e0 + g < a.E, ok1 = e0 + 8 + g < a.E, okx = t0 + g < a.T;
+  const __nv_bfloat16* w0 = a.router + (size_t)(ok0 ? e0 + g : 0) * a.d_model + q * 8;
+  const __nv_bfloat16* w1 = a.router + (size_t)(ok1 ? e0 + 8 + g : 0) * a.d_model + q * 8;
+  const __nv_bfloat16* x = a.x + (size_t)(okx ? t0 + g : 0) * a.d_model + q * 8;
+  float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+  const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 8
-    for (int k = lane * 8; k < a.d_model; k += 256) add(ld_x(w + k), ld_x(px[0] + k), s[0]);
-  } else {
-#pragma unroll 4
-    for (int k = lane * 8; k < a.d_model; k += 256) {
-      const uint4 wv = ld_x(w + k);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) add(wv, ld_x(px[t] + k), s[t]);
-    }
+  for (int u = warp; u < units; u += kMWarps) {
+    const uint4 v0 = ok0 ? ld_x(w0 + u * 32) : z, v1 = ok1 ? ld_x(w1 + u * 32) : z, b = okx ? ld_x(x + u * 32) : z;
+    mma_bf16(acc[0], v0.x, v1.x, v0.y, v1.y, b.x, b.y);
+    mma_bf16(acc[1], v0.z, v1.z, v0.w, v1.w, b.z, b.w);
   }
+  float* o = part + g * 8 + 2 * q;
+  *reinterpret_cast<float2*>(o) = make_float2(acc[0][0] + acc[1][0], acc[0][1] + acc[1][1]);
+  *reinterpret_cast<float2*>(o + 64) = make_float2(acc[0][2] + acc[1][2], acc[0][3] + acc[1][3]);
+}
+
+// item: one such tile, to the workspace
+__device__ __noinline__ void router_item(const MoeArgs& a, int item, int lane, int warp) {
+  Smem& sm = smem();
+  const int groups = (a.T + 7) / 8, e0 = item / groups * 16, t0 = item % groups * 8;
+  router_tile(a, e0, t0, sm.red + warp * 128, lane, warp);
+  csync();
+  const int e = e0 + (threadIdx.x >> 3), t = t0 + (threadIdx.x & 7);
+  if (threadIdx.x < 128 && e < a.E && t < a.T) {
+    float v = 0.0f;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s[t] += __shfl_xor_sync(0xffffffffu, s[t], o);
-    if (lane == 0 && t < nt && t0 + t < a.T) __stcg(a.logits + (size_t)(t0 + t) * a.E + e, s[t]);
+    for (int w = 0; w < kMWarps; ++w) v += sm.red[w * 128 + threadIdx.x];
+    __stcg(a.logits + (size_t)t * a.E + e, v);
   }
 }
 
@@ -263,53 +261,42 @@ __device__ __forceinline__ float x_power(const __nv_bfloat16* x, int d, int lane
   return __uint_as_float((uint32_t)(up + 127) << 23);
 }
 
-// larger float, larger key (NaN above all)
+// larger float, larger key (NaN above all), and back
 __device__ __forceinline__ uint32_t order_key(float f) {
   if (f != f) return 0xffffffffu;
   const uint32_t u = __float_as_uint(f == 0.0f ? 0.0f : f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
 
 // Experts and shares of every token from logits [T, E], then the experts' token
 // lists, into sm.  (logits may be the union's memory: they are read before a
-// barrier, the choices are written to it after.)
+// barrier, the choices are written to it after.)  Run once per call, by cold
+// code: short loops, not unrolled ones (26 K cycles -> MEASURE_S for 32 tokens).
 template <bool SHARED>
 __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logits, bool publish, int lane, int warp) {
   Smem& sm = smem();
-  const int K = a.top_k;
+  const int K = a.top_k, n = a.T * K;
+#pragma unroll 1
   for (int t = warp; t < a.T; t += kMWarps) {
-    float v[kMoeMaxE / 32];
-    uint32_t taken = 0;                       // bit i: this lane's value i is chosen
-#pragma unroll
-    for (int i = 0; i < kMoeMaxE / 32; ++i) {
-      const int e = lane + 32 * i;
-      v[i] = e < a.E ? (SHARED ? logits[t * a.E + e] : __ldcg(logits + (size_t)t * a.E + e)) : 0.0f;
-    }
+    uint32_t taken = 0;                       // bit i: this lane's expert lane + 32 i is chosen
     float best = 0.0f, sum = 0.0f, mine = 0.0f;
     int choice = 0;                           // lane j: choice j
+#pragma unroll 1
     for (int j = 0; j < K; ++j) {
-      uint64_t key = 0;                       // order, then the lower expert
-#pragma unroll
-      for (int i = 0; i < kMoeMaxE / 32; ++i) {
-        if (32 * i >= a.E) break;
-        const int e = lane + 32 * i;
-        if (e < a.E && !((taken >> i) & 1u)) {
-          const uint64_t k = ((uint64_t)order_key(v[i]) << 32) | (uint32_t)(kMoeMaxE - e);
-          key = k > key ? k : key;
-        }
+      uint32_t key = 0;                       // (a real key is never 0)
+      int at = kMoeMaxE;
+#pragma unroll 1
+      for (int e = lane; e < a.E; e += 32) {
+        const uint32_t k = order_key(SHARED ? logits[t * a.E + e] : __ldcg(logits + (size_t)t * a.E + e));
+        if (k > key && !((taken >> (e >> 5)) & 1u)) key = k, at = e;
       }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const uint64_t k = __shfl_xor_sync(0xffffffffu, key, o);
-        key = k > key ? k : key;
-      }
-      const int e = kMoeMaxE - (int)(uint32_t)key;
-      float l = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kMoeMaxE / 32; ++i)
-        if (i == (e >> 5)) l = v[i];
-      l = __shfl_sync(0xffffffffu, l, e & 31);
-      if (lane == (e & 31)) taken |= 1u << (e >> 5);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+      const int e = __reduce_min_sync(0xffffffffu, key == top ? at : kMoeMaxE);
+      if (at == e) taken |= 1u << (e >> 5);
+      const float l = key_value(top);
       if (j == 0) best = l;
       const float p = expf(l - best);
       sum += p;
@@ -326,17 +313,18 @@ __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logit
     }
   }
   csync();
-  const int n = a.T * K, e = threadIdx.x;
-  for (int i = threadIdx.x; i < n; i += kMThreads) sm.sel[i] = sm.slot[i];
+  int* cnt = sm.sel + kMoeMaxSlots;
+  for (int i = threadIdx.x; i < a.E; i += kMThreads) cnt[i] = 0;
   csync();
-  // thread e: its tokens in order; experts without tokens drop out
-  int cnt = 0;
-  if (e < a.E)
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) cnt += sm.sel[i] == e;
-  const int act = cnt > 0;
-  // sums over the experts: (active experts, slots), both below 2^16
-  const int v = (act << 16) | cnt;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kMThreads) {
+    sm.sel[i] = sm.slot[i];
+    atomicAdd(&cnt[sm.slot[i]], 1);
+  }
+  csync();
+  // experts without tokens drop out: sums over the experts before of (active
+  // experts, slots), both below 2^16
+  const int e = threadIdx.x, c = e < a.E ? cnt[e] : 0, v = ((c > 0) << 16) | c;
   int inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -346,26 +334,39 @@ __device__ __noinline__ void select_experts(const MoeArgs& a, const float* logit
   if (lane == 31) sm.scan[warp] = inc;
   csync();
   int before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < kMWarps; ++w) {
-    if (w < warp) before += sm.scan[w];
-    total += sm.scan[w];
+    const int s = sm.scan[w];
+    if (w < warp) before += s;
+    total += s;
   }
   const int ex = before + inc - v;
-  if (act) {
-    const int ai = ex >> 16, first = ex & 0xffff;
-    sm.expert[ai] = e;
-    sm.firsts[ai] = first;
-    sm.count[ai] = cnt;
-    int at = first;
-    for (int i = 0; i < n; ++i)
-      if (sm.sel[i] == e) {
-        sm.token[at] = (int16_t)(i / K);
-        sm.slot_expert[at] = (uint8_t)ai;
-        sm.slot[i] = (int16_t)at;
-        ++at;
-      }
+  if (c > 0) {
+    const int ai = ex >> 16;
+    sm.expert[ai] = (int16_t)e;
+    sm.firsts[ai] = (int16_t)(ex & 0xffff);
+    sm.count[ai] = (int16_t)c;
   }
   if (threadIdx.x == 0) sm.active = total >> 16;
+  csync();
+  // a warp per active expert: its tokens in order
+#pragma unroll 1
+  for (int ai = warp; ai < sm.active; ai += kMWarps) {
+    int at = sm.firsts[ai];
+    const int ee = sm.expert[ai];
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const bool is = i0 + lane < n && sm.sel[i0 + lane] == ee;
+      const unsigned m = __ballot_sync(0xffffffffu, is);
+      if (is) {
+        const int to = at + __popc(m & lanemask_lt());
+        sm.token[to] = (int16_t)((i0 + lane) / K);
+        sm.slot_expert[to] = (uint8_t)ai;
+        sm.slot[i0 + lane] = (int16_t)to;
+      }
+      at += __popc(m);
+    }
+  }
   csync();
 }
 
@@ -406,15 +407,19 @@ __device__ void fetch_routing(const MoeArgs& a, Smem& sm) {
   for (int i = tid; i < n; i += kMThreads) {
     sm.token[i] = (int16_t)__ldcg(a.table + kMtToken + i);
     sm.slot[i] = (int16_t)__ldcg(a.table + kMtSlot + i);
-    int ai = 0;                          // (active experts are few where slots are)
-    while (ai + 1 < A && __ldcg(a.table + kMtFirst + ai + 1) <= i) ++ai;
-    sm.slot_expert[i] = (uint8_t)ai;
     sm.share[i] = __ldcg(a.share + i);
   }
   if (a.fp4)
     for (int i = tid; i < a.T; i += kMThreads) sm.xup[i] = __ldcg(a.xup + i);
   if (tid == 0) sm.active = A;
   csync();
+  for (int i = tid; i < n; i += kMThreads) {
+    int ai = 0;
+#pragma unroll 1
+    for (int step = kMoeMaxE / 2; step; step >>= 1)
+      if (ai + step < A && sm.firsts[ai + step] <= i) ai += step;
+    sm.slot_expert[i] = (uint8_t)ai;
+  }
 }
 
 // Local routing: at most 8 tokens and a small router (at most 64 experts and 128
@@ -423,25 +428,10 @@ __device__ void fetch_routing(const MoeArgs& a, Smem& sm) {
 // instruction.
 __device__ __noinline__ void route_here(const MoeArgs& a, bool publish, int lane, int warp) {
   Smem& sm = smem();
-  const int g = lane >> 2, q = lane & 3, units = a.d_model / 32, pairs = a.E * a.T;
+  const int pairs = a.E * a.T;
   float* part = sm.red;                             // [warp][expert][8 tokens]: 64 x 8 x 8 at most
-  for (int e0 = 0; e0 < a.E; e0 += 16) {
-    const bool ok0 = e0 + g < a.E, ok1 = e0 + 8 + g < a.E;
-    const __nv_bfloat16* w0 = a.router + (size_t)(ok0 ? e0 + g : 0) * a.d_model + q * 8;
-    const __nv_bfloat16* w1 = a.router + (size_t)(ok1 ? e0 + 8 + g : 0) * a.d_model + q * 8;
-    const __nv_bfloat16* x = a.x + (size_t)(g < a.T ? g : 0) * a.d_model + q * 8;
-    float acc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll 8
-    for (int u = warp; u < units; u += kMWarps) {
-      const uint4 v0 = ok0 ? ld_x(w0 + u * 32) : z, v1 = ok1 ? ld_x(w1 + u * 32) : z, b = g < a.T ? ld_x(x + u * 32) : z;
-      mma_bf16(acc[0], v0.x, v1.x, v0.y, v1.y, b.x, b.y);
-      mma_bf16(acc[1], v0.z, v1.z, v0.w, v1.w, b.z, b.w);
-    }
-    float* o = part + warp * 512 + (e0 + g) * 8 + 2 * q;
-    *reinterpret_cast<float2*>(o) = make_float2(acc[0][0] + acc[1][0], acc[0][1] + acc[1][1]);
-    *reinterpret_cast<float2*>(o + 64) = make_float2(acc[0][2] + acc[1][2], acc[0][3] + acc[1][3]);
-  }
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 16) router_tile(a, e0, 0, part + warp * 512 + e0 * 8, lane, warp);
   if (a.fp4)
     for (int t = warp; t < a.T; t += kMWarps) {
       const float u = x_power(a.x + (size_t)t * a.d_model, a.d_model, lane);
@@ -1651,8 +1641,7 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   if (fp4 && used * d_ff * d_model / 2 >= ((long)V_MIN << 20)) p.tensor = T * top_k >= V_BOTH * n_experts ? 2 : 1;
   p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
   p.x_items = (!p.local && fp4 && p.tensor != 2) ? (T + kMWarps - 1) / kMWarps : 0;
-  p.router_tokens = (long)T * n_experts <= kNumSMs * kMWarps ? 1 : 4;
-  p.router_items = p.local ? 0 : (n_experts * ((T + p.router_tokens - 1) / p.router_tokens) + kMWarps - 1) / kMWarps + p.x_items;
+  p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
   p.one_token = T == 1 && d_model <= 4096 && p.tensor != 2;
   p.hidden_items = p.grid;
   // tokens per pass: two groups of 8 where x of both fits the registers; with
