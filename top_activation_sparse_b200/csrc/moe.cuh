@@ -28,9 +28,8 @@ struct MoePlan {
   int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
-  // 4-bit weights, kernels of their own before this one route, and compute (1) the
-  // first factors of all neurons (moe_fp4_dense.cu), or (2) h and the down projection's
-  // partial sums (moe_fp4_down.cu); 0: one kernel does all
+  // 4-bit weights: four kernels (routing; h, moe_fp4_factors.cu; the down projection
+  // and the sums, moe_fp4_down.cu) instead of one
   int tensor = 0;
 };
 MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k);
@@ -64,8 +63,7 @@ struct MoeArgs {
   float* xup = nullptr;                   // [T] power of two that takes x to float16 (4-bit weights)
   uint8_t* xt = nullptr;                  // [T, 8, d_model/2] x as eight 4-bit numbers (4-bit weights)
   uint8_t* xs = nullptr;                  // [T, moe_xs_pitch] scale bytes of the first of them
-  float* h = nullptr;                     // [T * top_k, d_ff] (plan.tensor 1: first factors, then h);
-                                          // plan.tensor 2: [T * top_k, 3, d_ff] bf16
+  float* h = nullptr;                     // [T * top_k, d_ff]; plan.tensor: [T * top_k, 3, d_ff] bf16
   uint8_t* nz = nullptr;                  // [min(E, T * top_k), d_ff]
   float* parts = nullptr;                 // [splits][T * top_k][d_model]
   DevStatus* status = nullptr;
@@ -73,7 +71,7 @@ struct MoeArgs {
 };
 cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
-cudaError_t launch_moe_fp4_dense(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_fp4_factors(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_sum(const MoeArgs& a, cudaStream_t s);
 constexpr int kMoeDownTokens = 40, kMoeDownCols = 512;    // moe_fp4_down.cu: per pass, per item

@@ -39,6 +39,7 @@ namespace {
 constexpr int kFM = 128;                        // neurons per unit
 constexpr int kFABytes = kFM * kGK / 2;
 constexpr int kFThreads = 320;
+constexpr int kMats = 2;                         // matrices: the first factor's, the second's
 constexpr int kFTokens = 16;                    // tokens per pass
 constexpr int kChunk = 4;                       // steps whose scales come at once
 constexpr int kSfOp = kChunk * 2 * kSfTile;     // their bytes per operand
@@ -50,7 +51,6 @@ struct FArgs {
   MoeArgs m;
   const uint8_t* xs;                            // [T, xs_pitch] scale bytes of the first terms
   int xs_pitch;
-  int mats;
   int tokens;                                   // most tokens of a pass
   int stages, stage_bytes;
   int acc, nacc;                                // accumulator columns per matrix, accumulators
@@ -82,9 +82,8 @@ __device__ __forceinline__ uint32_t f_idesc(uint32_t sf_id, uint32_t n) {
 
 __device__ __forceinline__ float f_relu(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
 
-template <int MATS>
 __global__ void __launch_bounds__(kFThreads, 1)
-    moe_fp4_dense_kernel(const __grid_constant__ CUtensorMap map_1, const __grid_constant__ CUtensorMap map_2,
+    moe_fp4_factors_kernel(const __grid_constant__ CUtensorMap map_1, const __grid_constant__ CUtensorMap map_2,
                          const __grid_constant__ CUtensorMap map_x, const __grid_constant__ FArgs f) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t s_full[kFMaxStages], s_empty[kFMaxStages];
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sf0 = base + (uint32_t)(f.stages * f.stage_bytes);       // the ring of scales
-  constexpr uint32_t kSfSlot = (MATS + 1) * kSfOp;
+  constexpr uint32_t kSfSlot = (kMats + 1) * kSfOp;
   const int nk = (a.d_model + kGK - 1) / kGK, nchunk = (nk + kChunk - 1) / kChunk;
   const int mtiles = (a.d_ff + kFM - 1) / kFM;
 
@@ -136,11 +135,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int ks = 0; ks < nk; ++ks, ++i) {
           if (!(ok = g_wait(&s_empty[sl], ph ^ 1u, &s_abort, a.status, 64))) break;
           const uint32_t st = base + (uint32_t)(sl * f.stage_bytes);
-          mbar_arrive_expect_tx(&s_full[sl], (uint32_t)(MATS * kFABytes + x.nt * 1024));
+          mbar_arrive_expect_tx(&s_full[sl], (uint32_t)(kMats * kFABytes + x.nt * 1024));
           g_tma(st, &map_1, ks * (kGK / 2), row, &s_full[sl]);
-          if (MATS == 2) g_tma(st + kFABytes, &map_2, ks * (kGK / 2), row, &s_full[sl]);
+          g_tma(st + kFABytes, &map_2, ks * (kGK / 2), row, &s_full[sl]);
           for (int c = 0; c < x.nt; ++c)
-            g_tma(st + MATS * kFABytes + c * 1024, &map_x, ks * (kGK / 2), tb.token[x.slot0 + c] * 8, &s_full[sl]);
+            g_tma(st + kMats * kFABytes + c * 1024, &map_x, ks * (kGK / 2), tb.token[x.slot0 + c] * 8, &s_full[sl]);
           if (++sl == f.stages) sl = 0, ph ^= 1u;
         }
       }
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     int sl = 0, sfsl = 0, piece = 0;
     uint32_t ph = 0, sfph = 0;
     bool ok = true;
-    const uint32_t sfcols = tmem + (uint32_t)(f.nacc * MATS * f.acc);
+    const uint32_t sfcols = tmem + (uint32_t)(f.nacc * kMats * f.acc);
     const uint64_t d0 = g_desc(base, 1024, 2), s0 = g_desc(sf0, 128, 0);
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++piece) {
       const FUnit x = f_unit(tb, u, mtiles);
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int ab = piece % f.nacc;
       if (piece >= f.nacc && !(ok = g_wait(&s_tempty[ab], (uint32_t)(piece / f.nacc - 1) & 1u, &s_abort, a.status, 65))) break;
       g_after();
-      const uint32_t acc = tmem + (uint32_t)(ab * MATS * f.acc);
+      const uint32_t acc = tmem + (uint32_t)(ab * kMats * f.acc);
       for (int ks = 0; ks < nk; ++ks) {
         const int in = ks % kChunk;
         if (in == 0 && !(ok = g_wait(&s_sffull[sfsl], sfph, &s_abort, a.status, 66))) break;
@@ -175,20 +174,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
         g_after();
         const uint64_t st = d0 + (uint64_t)(sl * (f.stage_bytes / 16));
         const uint64_t sfs = s0 + (uint64_t)(sfsl * (int)(kSfSlot / 16) + in * (2 * kSfTile / 16));
-        const uint32_t sfc = sfcols + (uint32_t)(sl * (MATS + 1) * 8);
+        const uint32_t sfc = sfcols + (uint32_t)(sl * (kMats + 1) * 8);
         const int rest = a.d_model - ks * kGK;
         if (issues) {
 #pragma unroll
-          for (int o = 0; o <= MATS; ++o)
+          for (int o = 0; o <= kMats; ++o)
 #pragma unroll
             for (int t = 0; t < 2; ++t) g_cp_sf(sfc + o * 8 + t * 4, sfs + o * (kSfOp / 16) + t * (kSfTile / 16));
 #pragma unroll
           for (int kk = 0; kk < kGK / 64; ++kk)
             if (kk * 64 < rest) {
 #pragma unroll
-              for (int o = 0; o < MATS; ++o)
-                g_mma<false>(acc + o * f.acc, st + o * (kFABytes / 16) + kk * 2, st + MATS * (kFABytes / 16) + kk * 2,
-                             (kk & 1) ? id1 : id0, sfc + o * 8 + (kk >> 1) * 4, sfc + MATS * 8 + (kk >> 1) * 4, ks > 0 || kk > 0);
+              for (int o = 0; o < kMats; ++o)
+                g_mma<false>(acc + o * f.acc, st + o * (kFABytes / 16) + kk * 2, st + kMats * (kFABytes / 16) + kk * 2,
+                             (kk & 1) ? id1 : id0, sfc + o * 8 + (kk >> 1) * 4, sfc + kMats * 8 + (kk >> 1) * 4, ks > 0 || kk > 0);
             }
           g_commit(&s_empty[sl]);
           if (in == kChunk - 1 || ks == nk - 1) g_commit(&s_sfempty[sfsl]);
@@ -214,43 +213,37 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int ab = piece % f.nacc, j = x.m * kFM + q * 32 + lane;
       const bool mine = j < a.d_ff;
       const size_t bi = (size_t)x.e * a.d_ff + (mine ? j : 0);
-      const float b1 = a.b1 ? __ldg(a.b1 + bi) : 0.0f, b2 = MATS == 2 && a.b2 ? __ldg(a.b2 + bi) : 0.0f;
+      const float b1 = a.b1 ? __ldg(a.b1 + bi) : 0.0f, b2 = a.b2 ? __ldg(a.b2 + bi) : 0.0f;
       if (!g_wait(&s_tfull[ab], (uint32_t)(piece / f.nacc) & 1u, &s_abort, a.status, 68)) break;
       g_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * MATS * f.acc);
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * kMats * f.acc);
       for (int c = 0; c < x.nt; ++c) {
-        uint32_t v[MATS][8];
+        uint32_t v[kMats][8];
 #pragma unroll
-        for (int o = 0; o < MATS; ++o) g_ld8(acc + (uint32_t)(o * f.acc + c * 8), v[o]);
+        for (int o = 0; o < kMats; ++o) g_ld8(acc + (uint32_t)(o * f.acc + c * 8), v[o]);
         g_ld_wait();
-        float s[MATS];
+        float s[kMats];
 #pragma unroll
-        for (int o = 0; o < MATS; ++o) {
+        for (int o = 0; o < kMats; ++o) {
           s[o] = __uint_as_float(v[o][7]);
 #pragma unroll
           for (int i = 6; i >= 0; --i) s[o] += __uint_as_float(v[o][i]);
         }
         float h = f_relu(s[0] + b1);
         if (!a.drelu) h *= h;
-        if constexpr (MATS == 2) {
-          // (a closed first factor is 0 whatever the other is)
-          float g = s[1] + b2;
-          if (a.drelu) g = f_relu(g);
-          h = h == 0.0f ? 0.0f : h * g;
-        }
-        if constexpr (MATS == 1) {
-          if (mine) __stcg(a.h + (size_t)(x.slot0 + c) * a.d_ff + j, h);
-        } else {
-          // h as the sum of three bf16 numbers, for the down projection (an
-          // infinity or a NaN has no rest)
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.h) + (size_t)(x.slot0 + c) * 3 * a.d_ff + j;
-          const bool finite = fabsf(h) <= 3.0e38f;
+        // (a closed first factor is 0 whatever the other is)
+        float g = s[1] + b2;
+        if (a.drelu) g = f_relu(g);
+        h = h == 0.0f ? 0.0f : h * g;
+        // h as the sum of three bf16 numbers, for the down projection (an
+        // infinity or a NaN has no rest)
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.h) + (size_t)(x.slot0 + c) * 3 * a.d_ff + j;
+        const bool finite = fabsf(h) <= 3.0e38f;
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(h);
-            if (mine) o[(size_t)i * a.d_ff] = b;
-            h = finite ? h - __bfloat162float(b) : 0.0f;
-          }
+        for (int i = 0; i < 3; ++i) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(h);
+          if (mine) o[(size_t)i * a.d_ff] = b;
+          h = finite ? h - __bfloat162float(b) : 0.0f;
         }
       }
       g_before();
@@ -268,15 +261,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       const FUnit x = f_unit(tb, u, mtiles);
       const int j = x.m * kFM + r, c = r >> 3;
-      const uint8_t* rows[MATS];
+      const uint8_t* rows[kMats];
       rows[0] = a.s1 + ((size_t)x.e * a.d_ff + j) * sb;
-      if constexpr (MATS == 2) rows[1] = a.s2 + ((size_t)x.e * a.d_ff + j) * sb;
+      rows[1] = a.s2 + ((size_t)x.e * a.d_ff + j) * sb;
       const uint8_t* xs = f.xs + (size_t)(c < x.nt ? tb.token[x.slot0 + c] : 0) * f.xs_pitch;
       const uint32_t less = (uint32_t)(3 * (r & 7)) * 0x01010101u;
       for (int ch = 0; ch < nchunk; ++ch) {
-        uint32_t w[MATS + 1][8];
+        uint32_t w[kMats + 1][8];
 #pragma unroll
-        for (int o = 0; o < MATS; ++o)
+        for (int o = 0; o < kMats; ++o)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const int b = ch * 32 + half * 16;
@@ -298,13 +291,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int half = 0; half < 2; ++half) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (c < x.nt) v = __ldcg(reinterpret_cast<const uint4*>(xs + ch * 32 + half * 16));
-          w[MATS][half * 4] = __vsubus4(v.x, less), w[MATS][half * 4 + 1] = __vsubus4(v.y, less);
-          w[MATS][half * 4 + 2] = __vsubus4(v.z, less), w[MATS][half * 4 + 3] = __vsubus4(v.w, less);
+          w[kMats][half * 4] = __vsubus4(v.x, less), w[kMats][half * 4 + 1] = __vsubus4(v.y, less);
+          w[kMats][half * 4 + 2] = __vsubus4(v.z, less), w[kMats][half * 4 + 3] = __vsubus4(v.w, less);
         }
         if (!(ok = g_wait(&s_sfempty[sfsl], sfph ^ 1u, &s_abort, a.status, 69))) break;
         const uint32_t dst = sf0 + (uint32_t)sfsl * kSfSlot + at;
 #pragma unroll
-        for (int o = 0; o <= MATS; ++o)
+        for (int o = 0; o <= kMats; ++o)
 #pragma unroll
           for (int b = 0; b < 8; ++b)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + (uint32_t)(o * kSfOp + b * kSfTile)), "r"(w[o][b]) : "memory");
@@ -322,40 +315,33 @@ __global__ void __launch_bounds__(kFThreads, 1)
   }
 }
 
-template <int MATS>
-cudaError_t f_launch(const CUtensorMap& m1, const CUtensorMap& m2, const CUtensorMap& mx, const FArgs& f, int smem,
-                     cudaStream_t s) {
-  static unsigned configured = 0;
-  cudaError_t e = ensure_smem_attr(moe_fp4_dense_kernel<MATS>, kFSmemCap, &configured);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(moe_fp4_dense_kernel<MATS>, dim3((unsigned)kNumSMs), dim3(kFThreads), (size_t)smem, s, m1, m2, mx, f);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
-}
-
 }  // namespace
 
-cudaError_t launch_moe_fp4_dense(const MoeArgs& a, cudaStream_t s) {
+cudaError_t launch_moe_fp4_factors(const MoeArgs& a, cudaStream_t s) {
   FArgs f;
   f.m = a;
   f.xs = a.xs;
   f.xs_pitch = moe_xs_pitch(a.d_model);
-  f.mats = a.plan.tensor == 2 ? 2 : 1;
   f.tokens = a.T < kFTokens ? a.T : kFTokens;
-  f.stage_bytes = f.mats * kFABytes + f.tokens * 1024;
-  const int sf = kSfRing * (f.mats + 1) * kSfOp;
+  f.stage_bytes = kMats * kFABytes + f.tokens * 1024;
+  const int sf = kSfRing * (kMats + 1) * kSfOp;
   f.stages = (kFSmemCap - 1024 - sf) / f.stage_bytes;
   if (f.stages > kFMaxStages) f.stages = kFMaxStages;
   // two accumulators where tensor memory (512 columns) has them beside the scales
   f.acc = f.tokens * 8 < 32 ? 32 : (f.tokens * 8 + 31) / 32 * 32;
-  f.nacc = 2 * f.mats * f.acc + f.stages * (f.mats + 1) * 8 <= 512 ? 2 : 1;
+  f.nacc = 2 * kMats * f.acc + f.stages * (kMats + 1) * 8 <= 512 ? 2 : 1;
   CUtensorMap m1, m2, mx;
   const uint64_t pitch = (uint64_t)(a.d_model / 2), rows = (uint64_t)a.E * a.d_ff;
   if (!g_map(&m1, a.w1, pitch, rows, kFM) || !g_map(&m2, a.w2, pitch, rows, kFM) ||
       !g_map(&mx, a.xt, pitch, (uint64_t)a.T * 8, 8))
     return cudaErrorInvalidValue;
   const int smem = f.stages * f.stage_bytes + sf + 1024;
-  return f.mats == 2 ? f_launch<2>(m1, m2, mx, f, smem, s) : f_launch<1>(m1, m2, mx, f, smem, s);
+  static unsigned configured = 0;
+  cudaError_t e = ensure_smem_attr(moe_fp4_factors_kernel, kFSmemCap, &configured);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(moe_fp4_factors_kernel, dim3((unsigned)kNumSMs), dim3(kFThreads), (size_t)smem, s, m1, m2, mx, f);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 }  // namespace qs

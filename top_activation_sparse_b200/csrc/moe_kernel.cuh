@@ -133,31 +133,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// ---- 4-bit weights as bf16 ---------------------------------------------------
-// A code's three magnitude bits, put where bf16 has its lowest exponent bits
-// and its highest mantissa bit, read as value * 2^-126 (subnormals included);
-// one product brings in 2^126 and the block's scale: 2^126 2^(s-127) = 2^(s-1)
-// for scales up to 2, a second product the rest of larger ones.
-struct Scale2 {
-  uint32_t lo, hi;     // factors (bf16 pairs); hi is applied where s > 128
-};
-__device__ __forceinline__ uint32_t scale_lo(uint32_t s) { return (s < 128u ? s + 126u : 254u) << 7; }
-__device__ __forceinline__ uint32_t scale_hi(uint32_t s) { return s == 255u ? 0x7fc0u : (s > 128u ? s - 1u : 127u) << 7; }
-
-// bits 4c..4c+3 of each half of p -> a pair of bf16 magnitudes times 2^-126
-template <int C>
-__device__ __forceinline__ uint32_t code_pair(uint32_t p) {
-  const uint32_t m = C == 0 ? p << 6 : C == 1 ? p << 2 : C == 2 ? p >> 2 : p >> 6;
-  const uint32_t s = C == 3 ? p : p << (12 - 4 * C);
-  return (m & 0x01c001c0u) | (s & 0x80008000u);
-}
-template <int C>
-__device__ __forceinline__ uint32_t weight_pair(uint32_t p, uint32_t lo, uint32_t hi, bool big) {
-  uint32_t v = mul_bf16x2(code_pair<C>(p), lo);
-  if (big) v = mul_bf16x2(v, hi);
-  return v;
-}
-
 // ---- queue and waits ---------------------------------------------------------
 __device__ __forceinline__ int ld_acquire(const int32_t* p) {
   int v;
@@ -818,7 +793,7 @@ __device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, 
   const ExpertMats M = expert_mats<FP4>(a, u.e);
   const int nb = (u.j1 - u.j0 + u.batch - 1) / u.batch;
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
-    if (b < nb && !(FP4 && a.plan.tensor)) {
+    if (b < nb) {
       const int jb = u.j0 + b * u.batch;
       send_rows(R, at, sm, a.status, M.w1, M.s1, nullptr, jb, min(u.batch, u.j1 - jb), lane);
     }
@@ -868,7 +843,6 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
   constexpr int kStep = kMThreads / kTok;                // rows between a thread's places
   const float back = FP4 && c < u.nt ? 1.0f / sm.xup[sm.tok[c]] : 1.0f;
   const float share = ONE ? choice_share(a, sm, u.slot0) : 0.0f;
-  const bool given = FP4 && a.plan.tensor;               // the first factors are in a.h
   for (int b = 0; b < nb + (ONE ? 2 : 1); ++b) {
     // (one body for both factors: the code of two does not stay in the
     // instruction cache)
@@ -888,8 +862,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         j[k] = r < n ? (list ? list[r] : jb + r) : -1;
         bias[k] = bs && j[k] >= 0 ? __ldg(bs + j[k]) : 0.0f;
       }
-      if (given && !second) {}
-      else if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
+      if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
       else dot_rows_bf16<KU, NG>(a, R, at, sm, P, x, n, lane);
       csync();
       if (!second) {
@@ -898,12 +871,8 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         for (int k = 0; k < kPer; ++k) {
           float v = 0.0f;
           if (j[k] >= 0 && c < u.nt) {
-            if (given) {
-              v = __ldcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j[k]);
-            } else {
-              v = relu_nan(dot_sum(sm, P, tid + k * kMThreads) * back + bias[k]);
-              if (!a.drelu) v *= v;
-            }
+            v = relu_nan(dot_sum(sm, P, tid + k * kMThreads) * back + bias[k]);
+            if (!a.drelu) v *= v;
           }
           sm.first[s][tid + k * kMThreads] = v;
           const unsigned any = __ballot_sync(0xffffffffu, v != 0.0f);
@@ -1040,14 +1009,14 @@ __device__ __forceinline__ void run_tokens(Smem& sm, const Run& u) {
 
 // (a function of its own per instance: inlined together they share the
 // registers of the largest and spill)
-template <bool FP4, int KU, int NG>
+template <int KU, int NG>
 __device__ __noinline__ void compute_pass(const MoeArgs& a, const Ring& R, RingAt& at, const Run& u, int lane, int warp) {
   Smem& sm = smem();
   float none[kVec][8];
   RingAt here = at;                     // in registers
   const Ring ring = R;
   const Run run = u;
-  compute_run<FP4, KU, NG, false>(a, ring, here, sm, run, none, lane, warp);
+  compute_run<false, KU, NG, false>(a, ring, here, sm, run, none, lane, warp);
   at = here;
 }
 
@@ -1074,13 +1043,9 @@ __device__ __forceinline__ void hidden_item(const MoeArgs& a, const Ring& R, Rin
     if constexpr (ONE) {
       compute_run<FP4, kUnits, 1, true>(a, R, at, sm, u, y, lane, warp);
     } else {
-      if constexpr (FP4) {
-        compute_pass<true, kUnits, 1>(a, R, at, u, lane, warp);
-      } else {
-        if (a.d_model > 4096) compute_pass<false, 2 * kUnits, 1>(a, R, at, u, lane, warp);
-        else if (u.nt <= 8) compute_pass<false, kUnits, 1>(a, R, at, u, lane, warp);
-        else compute_pass<false, kUnits, 2>(a, R, at, u, lane, warp);
-      }
+      if (a.d_model > 4096) compute_pass<2 * kUnits, 1>(a, R, at, u, lane, warp);
+      else if (u.nt <= 8) compute_pass<kUnits, 1>(a, R, at, u, lane, warp);
+      else compute_pass<kUnits, 2>(a, R, at, u, lane, warp);
     }
   });
   if constexpr (ONE) {
@@ -1141,21 +1106,19 @@ __device__ __forceinline__ DownItem down_place(const MoeArgs& a, const Smem& sm,
   d.cw = min(a.plan.tile_cols, a.d_model - d.c0);
   return d;
 }
-template <bool FP4>
 __device__ __forceinline__ DownRing down_ring(const MoeArgs& a, const DownItem& d) {
   DownRing r;
-  r.pb = FP4 ? d.cw / 2 : d.cw * 2;
+  r.pb = d.cw * 2;
   r.pitch = a.plan.down_pitch;
   r.stages = a.plan.down_stages;
   r.off = 0;
   return r;
 }
 
-template <bool FP4>
 __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem& d, int passes, int lane) {
-  const DownRing R = down_ring<FP4>(a, d);
-  const size_t rb = FP4 ? (size_t)(a.d_model / 2) : (size_t)a.d_model * 2;
-  const uint8_t* w = a.wd + (size_t)d.e * a.d_ff * rb + (FP4 ? d.c0 / 2 : d.c0 * 2);
+  const DownRing R = down_ring(a, d);
+  const size_t rb = (size_t)a.d_model * 2;
+  const uint8_t* w = a.wd + (size_t)d.e * a.d_ff * rb + d.c0 * 2;
   for (int p = 0; p < passes; ++p)
     for (int jl = d.j0; jl < d.j1; jl += kListD) {
       list_wait(sm, at, 2, a.status);
@@ -1179,19 +1142,18 @@ __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem
     }
 }
 
-template <bool FP4, int NG, int STR>
+template <int NG, int STR>
 __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const DownItem& d_, int slot0, int nt, int lane, int warp) {
   Smem& sm = smem();
   RingAt at = at_;
   const DownItem d = d_;
-  const DownRing R = down_ring<FP4>(a, d);
-  constexpr int kCols = FP4 ? 16 : 8;                // columns of a lane
+  const DownRing R = down_ring(a, d);
+  constexpr int kCols = 8;                           // columns of a lane
   constexpr int kMma = kCols / 2;                    // MMAs per 16 neurons and token group
   const int g = lane >> 2, q = lane & 3, tid = threadIdx.x;
   int col[STR];
 #pragma unroll
   for (int x = 0; x < STR; ++x) col[x] = (x * kMWarps + warp) * (8 * kCols) + g * kCols;
-  const uint8_t* sc = FP4 ? a.sd + (size_t)d.e * a.d_ff * (a.d_model / 32) + d.c0 / 32 : nullptr;
   float acc[STR][kMma][NG][4];
 #pragma unroll
   for (int x = 0; x < STR; ++x)
@@ -1251,28 +1213,7 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
         }
       }
       csync();
-      // 4-bit weights: the scales of this lane's rows and strips, a stage ahead
-      uint32_t ns[STR][4];
-      auto ahead = [&](int st) {
-        if constexpr (FP4) {
-          const int left = n - st * 16;
-          if (left > 0)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint8_t* p = sc + (size_t)(jl + sm.d.list[l0 + st * 16 + (4 * i + q < left ? 4 * i + q : 0)]) * (a.d_model / 32);
-#pragma unroll
-              for (int x = 0; x < STR; ++x) ns[x][i] = __ldg(p + (col[x] < d.cw ? col[x] : 0) / 32);
-            }
-        }
-      };
-      ahead(0);
       for (int st = 0; st < np / 16; ++st) {
-        uint32_t cs[STR][4];
-#pragma unroll
-        for (int x = 0; x < STR; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) cs[x][i] = FP4 ? ns[x][i] : 0u;
-        ahead(st + 1);
         const int nr = min(kRowsStage, n - st * 16);
         ring_wait(&sm.dfull[at.sl], at.ph, sm, a.status, 81);
         const unsigned char* stage = sm.tail + R.off + (size_t)at.sl * kRowsStage * R.pitch;
@@ -1297,38 +1238,17 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
 #pragma unroll
               for (int v = 0; v < 3; ++v) mma_bf16(acc[x][m][t], a0, a1, a2, a3, b[t][v].x, b[t][v].y);
           };
-          if constexpr (!FP4) {
-            uint4 u[4];
+          uint4 u[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(row[i] + cl * 2);
-            const uint32_t* u0 = reinterpret_cast<const uint32_t*>(&u[0]);
-            const uint32_t* u1 = reinterpret_cast<const uint32_t*>(&u[1]);
-            const uint32_t* u2 = reinterpret_cast<const uint32_t*>(&u[2]);
-            const uint32_t* u3 = reinterpret_cast<const uint32_t*>(&u[3]);
+          for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(row[i] + cl * 2);
+          const uint32_t* u0 = reinterpret_cast<const uint32_t*>(&u[0]);
+          const uint32_t* u1 = reinterpret_cast<const uint32_t*>(&u[1]);
+          const uint32_t* u2 = reinterpret_cast<const uint32_t*>(&u[2]);
+          const uint32_t* u3 = reinterpret_cast<const uint32_t*>(&u[3]);
 #pragma unroll
-            for (int m = 0; m < kMma; ++m)
-              mmas(m, __byte_perm(u0[m], u1[m], 0x5410), __byte_perm(u0[m], u1[m], 0x7632),
-                   __byte_perm(u2[m], u3[m], 0x5410), __byte_perm(u2[m], u3[m], 0x7632));
-          } else {
-            uint2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint2*>(row[i] + cl / 2);
-            const uint32_t(&s)[4] = cs[x];
-            // pairs of neurons (0, 1) and (2, 3), one code of each per half
-            const uint32_t lo01 = scale_lo(s[0]) | (scale_lo(s[1]) << 16), lo23 = scale_lo(s[2]) | (scale_lo(s[3]) << 16);
-            const uint32_t hi01 = scale_hi(s[0]) | (scale_hi(s[1]) << 16), hi23 = scale_hi(s[2]) | (scale_hi(s[3]) << 16);
-            const bool b01 = s[0] > 128u || s[1] > 128u, b23 = s[2] > 128u || s[3] > 128u;
-#pragma unroll
-            for (int half = 0; half < 4; ++half) {     // four columns each
-              const uint32_t sel = (half & 1) ? 0x7632 : 0x5410;
-              const uint32_t p01 = half < 2 ? __byte_perm(v[0].x, v[1].x, sel) : __byte_perm(v[0].y, v[1].y, sel);
-              const uint32_t p23 = half < 2 ? __byte_perm(v[2].x, v[3].x, sel) : __byte_perm(v[2].y, v[3].y, sel);
-              mmas(2 * half, weight_pair<0>(p01, lo01, hi01, b01), weight_pair<1>(p01, lo01, hi01, b01),
-                   weight_pair<0>(p23, lo23, hi23, b23), weight_pair<1>(p23, lo23, hi23, b23));
-              mmas(2 * half + 1, weight_pair<2>(p01, lo01, hi01, b01), weight_pair<3>(p01, lo01, hi01, b01),
-                   weight_pair<2>(p23, lo23, hi23, b23), weight_pair<3>(p23, lo23, hi23, b23));
-            }
-          }
+          for (int m = 0; m < kMma; ++m)
+            mmas(m, __byte_perm(u0[m], u1[m], 0x5410), __byte_perm(u0[m], u1[m], 0x7632),
+                 __byte_perm(u2[m], u3[m], 0x5410), __byte_perm(u2[m], u3[m], 0x7632));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.dempty[at.sl]);
@@ -1357,26 +1277,22 @@ __device__ __noinline__ void down_rows(const MoeArgs& a, RingAt& at_, const Down
   at_ = at;
 }
 
-// strips per warp: with at most 8 tokens their sums take 64 or 32 registers, with 16
-// (bf16; the 4-bit form takes 8 tokens at a time) half the strips do
-template <bool FP4>
-constexpr int kStrips = FP4 ? 1 : 4;
+// strips per warp: with at most 8 tokens their sums take 64 registers, with 16
+// half the strips do
+constexpr int kStrips = 4;
 
-template <bool FP4>
 __device__ void down_item(const MoeArgs& a, RingAt& at, Smem& sm, int item, int S, int lane, int warp) {
   const DownItem d = down_place(a, sm, item, S);
   const int first = sm.firsts[d.ai], cnt = sm.count[d.ai], pass = a.plan.down_tokens;
   if (warp == kMWarps) {
-    send_down<FP4>(a, at, sm, d, (cnt + pass - 1) / pass, lane);
+    send_down(a, at, sm, d, (cnt + pass - 1) / pass, lane);
     return;
   }
   for (int t0 = 0; t0 < cnt; t0 += pass) {
     const int nt = min(pass, cnt - t0);
-    if (FP4 || pass == 8) down_rows<FP4, 1, kStrips<FP4>>(a, at, d, first + t0, nt, lane, warp);
-    else if constexpr (!FP4) {
-      if (nt <= 8) down_rows<FP4, 1, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
-      else down_rows<FP4, 2, kStrips<FP4> / 2>(a, at, d, first + t0, nt, lane, warp);
-    }
+    if (pass == 8) down_rows<1, kStrips>(a, at, d, first + t0, nt, lane, warp);
+    else if (nt <= 8) down_rows<1, kStrips / 2>(a, at, d, first + t0, nt, lane, warp);
+    else down_rows<2, kStrips / 2>(a, at, d, first + t0, nt, lane, warp);
   }
 }
 
@@ -1436,7 +1352,7 @@ __device__ void sum_item(const MoeArgs& a, Smem& sm, int item, int S) {
 }
 
 // ---- ahead of the tensor-core products (4-bit weights) ---------------------------
-// x as eight 4-bit numbers (moe_fp4_dense.cu): 8 values per thread, the four
+// x as eight 4-bit numbers (moe_fp4_factors.cu): 8 values per thread, the four
 // threads of a block share its largest magnitude.
 __device__ void split_x(const MoeArgs& a, size_t v) {
   const size_t n8 = (size_t)a.T * a.d_model / 8;
@@ -1478,12 +1394,10 @@ __device__ void split_x(const MoeArgs& a, size_t v) {
   }
 }
 
-// Blocks: the router's, of which the last to finish selects; x's powers; x's
-// terms.
+// Blocks: the router's, of which the last to finish selects; x's terms.
 __global__ void __launch_bounds__(kMThreads, 1) moe_route_kernel(const __grid_constant__ MoeArgs a) {
   Smem& sm = smem();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
-  const int routers = a.plan.router_items - a.plan.x_items;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x, routers = a.plan.router_items;
   pdl_begin();
   if (b < routers) {
     router_item(a, b, lane, warp);
@@ -1493,16 +1407,10 @@ __global__ void __launch_bounds__(kMThreads, 1) moe_route_kernel(const __grid_co
       publish_routing(a, sm);
       if (threadIdx.x == 0) a.ctl[MC_ROUTED] = 0;
     }
-  } else if (b < a.plan.router_items) {
-    const int t = (b - routers) * kMWarps + warp;
-    if (t < a.T) {
-      const float u = x_power(a.x + (size_t)t * a.d_model, a.d_model, lane);
-      if (lane == 0) __stcg(a.xup + t, u);
-    }
   } else {
-    const size_t i0 = (size_t)(b - a.plan.router_items) * kMThreads + threadIdx.x;
+    const size_t i0 = (size_t)(b - routers) * kMThreads + threadIdx.x;
     split_x(a, i0);
-    const size_t step = (size_t)(gridDim.x - a.plan.router_items) * kMThreads;
+    const size_t step = (size_t)(gridDim.x - routers) * kMThreads;
     const int sb = a.d_model / 32, pitch = moe_xs_pitch(a.d_model), rest = pitch - sb;
     for (size_t i = i0; i < (size_t)a.T * rest; i += step) a.xs[i / rest * pitch + sb + i % rest] = 0;
   }
@@ -1565,7 +1473,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
         if (computes) {
           if (P.local) {
             route_here(a, item == 0, lane, warp);
-          } else if (P.tensor || wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) {
+          } else if (wait_for(a.ctl + MC_READY, 1, a.status, 70, sm)) {
             fetch_routing(a, sm);
           } else if (threadIdx.x == 0) {
             sm.active = 0;              // no tables to go by
@@ -1587,10 +1495,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
       } else if ((i -= P.hidden_items) < nD) {
         if constexpr (!ONE) {
           if (computes) wait_for(a.ctl + MC_HIDDEN, P.hidden_items, a.status, 71, sm);
-          // (the copying warp waits for the first list of rows; with 4-bit weights
-          // its copies go where x lay)
-          if (FP4 && computes) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          down_item<FP4>(a, atd, sm, i, S, lane, warp);
+          // (the copying warp waits for the first list of rows)
+          down_item(a, atd, sm, i, S, lane, warp);
           if (computes) finish(a.ctl + MC_DOWN, sm);
         }
       } else if ((i -= nD) < P.out_items) {
@@ -1627,28 +1533,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
 }
 
-#ifndef V_MIN
-#define V_MIN 4
-#endif
-#ifndef V_BOTH
-#define V_BOTH 2
-#endif
+// 4-bit weights: one token's layer (d_model <= 4096) in this kernel, everything else
+// by the tensor-core kernels, which read all weights but expand none of them in
+// registers.  8 experts of 4096 x 11008, 2 per token, dReLU without bias: 1 token 55
+// against 73 us, 2 tokens 120 against 106, 8: 244 against 172, 64: 1089 against 249; 60 of
+// 2048 x 1408, 4 per token: 34 / 44, 58 / 44, 104 / 69, 286 / 135.
 MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
   p.grid = kNumSMs;
-  const long used = n_experts < T * top_k ? n_experts : T * top_k;
-  if (fp4 && used * d_ff * d_model / 2 >= ((long)V_MIN << 20)) p.tensor = T * top_k >= V_BOTH * n_experts ? 2 : 1;
+  p.one_token = T == 1 && d_model <= 4096;
+  p.tensor = fp4 && !p.one_token;
   p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
-  p.x_items = (!p.local && fp4 && p.tensor != 2) ? (T + kMWarps - 1) / kMWarps : 0;
+  p.x_items = !p.local && fp4 && !p.tensor;
   p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
-  p.one_token = T == 1 && d_model <= 4096 && p.tensor != 2;
   p.hidden_items = p.grid;
-  // tokens per pass: two groups of 8 where x of both fits the registers; with
-  // 4-bit weights as many as fit 64 KB of shared memory
-  p.hidden_tokens = fp4 ? (d_model <= 4096 ? 8 : 4) : (d_model <= 4096 ? 16 : 8);
-  p.x_bytes = fp4 ? (T < p.hidden_tokens ? T : p.hidden_tokens) * ((d_model * 2 + 63) / 128 * 128 + 64) : 0;
-  p.x_bytes = (p.x_bytes + 127) / 128 * 128;
+  // tokens per pass: two groups of 8 where x of both fits the registers; 4-bit
+  // weights: one token, x in shared memory
+  p.hidden_tokens = fp4 ? 1 : d_model <= 4096 ? 16 : 8;
+  p.x_bytes = fp4 ? (d_model * 2 + 63) / 128 * 128 + 128 : 0;
   // the ring: stages of about 36 KB, whole tiles of 8 or 16 rows where rows are
   // short
   p.row_bytes = fp4 ? d_model / 2 : d_model * 2;
@@ -1662,50 +1565,58 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   p.stage_bytes = (p.stage_rows * (p.pitch + p.scale_bytes) + 127) / 128 * 128;
   p.stages = (kTail - p.x_bytes) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  // the down projection: tiles of the warps' strips
-  p.down_tokens = p.tensor == 2 ? kMoeDownTokens : fp4 || T <= 8 ? 8 : 16;
-  const int strips = p.down_tokens == 8 ? kStrips<fp4> : kStrips<fp4> / 2;
-  p.tile_cols = kMWarps * strips * (fp4 ? 128 : 64);
-  if (p.tensor == 2) p.tile_cols = kMoeDownCols;
-  if (p.tile_cols > d_model) p.tile_cols = d_model;
-  p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
-  // 32 mod 128: four rows' loads do not meet in a bank
-  p.down_pitch = ((fp4 ? p.tile_cols / 2 : p.tile_cols * 2) + 95) / 128 * 128 + 32;
-  p.down_stages = kTail / (kRowsStage * p.down_pitch);
-  if (p.down_stages > kMaxStages) p.down_stages = kMaxStages;
+  if (p.tensor) {
+    p.down_tokens = kMoeDownTokens;
+    p.tile_cols = kMoeDownCols;
+    p.col_tiles = (d_model + kMoeDownCols - 1) / kMoeDownCols;
+  } else {
+    // the down projection: tiles of the warps' strips
+    p.down_tokens = T <= 8 ? 8 : 16;
+    p.tile_cols = kMWarps * (p.down_tokens == 8 ? kStrips : kStrips / 2) * 64;
+    if (p.tile_cols > d_model) p.tile_cols = d_model;
+    p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
+    // 32 mod 128: four rows' loads do not meet in a bank
+    p.down_pitch = (p.tile_cols * 2 + 95) / 128 * 128 + 32;
+    p.down_stages = kTail / (kRowsStage * p.down_pitch);
+    if (p.down_stages > kMaxStages) p.down_stages = kMaxStages;
+  }
   const long vecs = ((long)T * (d_model / 4) + 15) / 16;
   p.out_items = (int)(vecs < p.grid ? vecs : p.grid);
   p.max_splits = kMoePartRows / (T * top_k);
   if (p.max_splits < 1) p.max_splits = 1;
   if (p.max_splits > p.grid) p.max_splits = p.grid;
+  // (tensor cores: at least four steps of 64 neurons)
+  if (p.tensor && p.max_splits > d_ff / 256) p.max_splits = d_ff < 512 ? 1 : d_ff / 256;
   return p;
 }
 
 cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
-  static unsigned done[2] = {0, 0};
-  const bool one = a.plan.one_token != 0;
-  auto k = one ? moe_kernel<kFp4, true> : moe_kernel<kFp4, false>;
-  cudaError_t e = ensure_smem_attr(k, (int)sizeof(Smem), &done[one ? 1 : 0]);
-  if (e != cudaSuccess) return e;
-  MoeArgs b = a;
+  cudaError_t e;
   if constexpr (kFp4) {
     if (a.plan.tensor) {
-      static unsigned done_route = 0;
-      e = ensure_smem_attr(moe_route_kernel, (int)sizeof(Smem), &done_route);
+      static unsigned done = 0;
+      e = ensure_smem_attr(moe_route_kernel, (int)sizeof(Smem), &done);
       if (e != cudaSuccess) return e;
       const size_t splits = ((size_t)a.T * a.d_model / 8 + kMThreads - 1) / kMThreads;
       e = launch_pdl(moe_route_kernel, dim3((unsigned)(a.plan.router_items + splits)), dim3(kMThreads), sizeof(Smem), s, a);
-      if (e != cudaSuccess) return e;
-      e = launch_moe_fp4_dense(a, s);
-      if (e != cudaSuccess) return e;
-      if (a.plan.tensor == 2) {
-        e = launch_moe_fp4_down(a, s);
-        return e != cudaSuccess ? e : launch_moe_fp4_sum(a, s);
-      }
-      b.plan.router_items = b.plan.x_items = 0;
+      if (e == cudaSuccess) e = launch_moe_fp4_factors(a, s);
+      if (e == cudaSuccess) e = launch_moe_fp4_down(a, s);
+      if (e == cudaSuccess) e = launch_moe_fp4_sum(a, s);
+      return e != cudaSuccess ? e : cudaGetLastError();
     }
   }
-  e = launch_pdl(k, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, b);
+  auto run = [&](auto kernel, unsigned* done) {
+    const cudaError_t r = ensure_smem_attr(kernel, (int)sizeof(Smem), done);
+    if (r != cudaSuccess) return r;
+    return launch_pdl(kernel, dim3((unsigned)a.plan.grid), dim3(kThreads), sizeof(Smem), s, a);
+  };
+  static unsigned done_one = 0;
+  if constexpr (kFp4) {
+    e = run(moe_kernel<true, true>, &done_one);
+  } else {
+    static unsigned done_many = 0;
+    e = a.plan.one_token ? run(moe_kernel<false, true>, &done_one) : run(moe_kernel<false, false>, &done_many);
+  }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
