@@ -453,8 +453,8 @@ size_t qs_fp4_scale_bytes(int64_t R, int d, int format, int scale_layout);
  *   matrices are multiplied on the tensor cores (block scales applied there,
  *   float32 accumulators):
  *     y[t, j] = g_x g_w sum_i (qx sx)[t, i] (qw sw)[j, i]
- *   The weight is read whole, once per 256 tokens: at 4.25 or 4.5 bits a value
- *   that is less than 70% of its rows in 8 bits.  Results do not depend on
+ *   The weight is read whole, once per 128 tokens (256 where they fill the GPU):
+ *   at 4.25 or 4.5 bits a value that is less than 70% of its rows in 8 bits.  Results do not depend on
  *   timing: the same call gives the same bits.
  *
  *   x         [T, d_in] `dtype` (bf16 or f32).     k  0..d_in.
@@ -477,8 +477,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
                                void* const* phase_events, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * qs_moe_ffn -- a mixture-of-experts FFN layer, router included, as one kernel
- *   (per 64 tokens).
+ * qs_moe_ffn -- a mixture-of-experts FFN layer, router included: one kernel per
+ *   64 tokens (4-bit weights: four, but for one token with d_model <= 4096).
  *   Source: Turbo Sparse summary (blog.csdn.net): the method applied to a
  *   model of experts, of which each token uses 2 of 8, and Eq. 2 (dReLU); the
  *   squared-ReLU form is that of qs_sparse_ffn.  The pages give no router; the
@@ -491,8 +491,10 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   ReLU: up) is 0 for every token of its expert is not computed further, and
  *   a down row is read only where some token's h is not 0: exact skipping, as
  *   in qs_sparse_ffn_gate_first.  Weights of experts that no token uses are
- *   not read.  Each expert weight is read once per 16 of its tokens
- *   (8 where d_model > 4096).
+ *   not read.  Each expert weight is read once per 16 of its tokens (8 where
+ *   d_model > 4096).  4-bit weights of experts with several tokens, of which
+ *   few neurons are closed for all, are read whole, for 16 tokens at a time
+ *   (down: 40): same results, a closed neuron contributes 0.
  *
  *   x         [T, d_model] bf16.
  *   w_router  [n_experts, d_model] bf16.
@@ -501,8 +503,11 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *             s_gate, s_up, s_down all NULL: bf16.  All given: 4-bit codes
  *             [n_experts, d_ff, d_model/2] and scales [n_experts, d_ff,
  *             d_model/32] (qs_fp4_quantize of these matrices, QS_FP4_MX,
- *             QS_FP4_SCALES_ROWS); they enter as the numbers they stand for,
- *             x is not quantised.
+ *             QS_FP4_SCALES_ROWS); they enter as the numbers they stand for
+ *             (one token: a scale of 2^-127, the least there is, counts as 0).
+ *             x is not quantised: it enters with 24 bits below the largest of
+ *             its block of 32 (one token: float16 with all of bf16's bits, down
+ *             to 2^-39 of the token's largest).
  *   b_gate, b_up  [n_experts, d_ff] f32 or NULL (= 0); QS_ACT_DRELU only.
  *   y         [T, d_model] `y_dtype` (bf16 or f32) out.
  *   experts   [T, top_k] int32 out or NULL: e_1..e_K, largest l first.

@@ -26,8 +26,10 @@
 // order of the steps (results do not depend on timing, and no partial sum
 // leaves the chip).  An earlier form dealt the steps of all tiles out evenly
 // over 148 CTAs with the partial sums in global memory, handed over by
-// tickets: its fences, tickets and re-reads cost more than the data (one token,
-// 4096 -> 11008: 18.9 us against MEASURE_A now).  Every wait is bounded.
+// tickets: its fences, tickets and re-reads cost more than the data (the whole call,
+// 8 tokens, NV, 11008 -> 4096 dense: 23.5 us against 15.2 now; the weight alone takes
+// 4.0 at the memory's rate.  What is left is latency: quantisation 2 us, launch, the first
+// steps' copies, two cluster barriers).  Every wait is bounded.
 #include <mutex>
 
 #include "fp4.cuh"

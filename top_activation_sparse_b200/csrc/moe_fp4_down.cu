@@ -9,15 +9,18 @@
 // three rows per token; N = 512 columns, whose sums fill tensor memory).
 //   * warp 0 copies the codes of 64 neurons x 512 columns per step, warp 2 the
 //     rows of h (2-D TMA, 128-byte swizzle);
-//   * warps 3 to 18 expand: a thread takes a block of 32 codes (16 bytes), 20
+//   * warps 3 to 18 expand: a thread takes two blocks of 32 codes (16 bytes each), 20
 //     instructions per 8 weights, and stores bf16 rows as the MMA reads them (N
 //     contiguous, swizzled).  The columns of a group of 8 are stored in the order
 //     0 4 1 5 2 6 3 7: a word's nibbles i and i + 4 make a pair without moves;
-//   * one thread of warp 1 issues the MMAs;
+//   * one lane of warp 1 issues the MMAs;
 //   * warps 3 to 6 add a token's three rows and store.
-// Bound by the expansion and by the tensor cores, both at about 1100 cycles a
-// step of 16 KB.  (In registers for mma.sync, 8 tokens at a time, moe_kernel.cuh:
-// 297 us for 32 tokens, 8 experts of 11008 x 4096; MEASURE_D here.)  Every wait is
+// 32 tokens, 2 of 8 experts of 11008 x 4096 each: 103 us, 1.8 TB/s of the 190 MB.
+// Bound by the step's chain: the expansion (1200 cycles of issue) and the MMAs (900)
+// overlap, but each hand-over through a barrier takes 300 to 400 cycles while the
+// expansion's stores fill the queue that barriers go through.  Smaller steps with four
+// places (128 us) and scales through shared memory (114 us) hand over more often.
+// (Expanding in registers for mma.sync, 8 tokens at a time: 297 us.)  Every wait is
 // bounded.
 #include "fp4_mma.cuh"
 #include "moe_tables.cuh"

@@ -1,4 +1,4 @@
-// First (and second) factors of 4-bit experts on the tensor cores.
+// Both factors of 4-bit experts, and h, on the tensor cores.
 //
 //   v[t, j] = sum_b s[j, b] sum_{i in block b} q[j, i] x[t, i]
 //
@@ -9,24 +9,24 @@
 //   s_0 = 2^(floor(log2 amax) - 1), s_{i+1} = s_i / 8
 // (per block of 32; |r_i / s_i| <= 4, where e2m1's steps are at most 1, so that
 // |r_{i+1}| <= s_i / 2: three bits a term).  The rest after 8 terms is at most
-// 2^-24 of twice the block's largest; bf16 values above 2^-15 of that largest are
-// exact.  A token takes 8 columns of the product, whose sums are added in
-// float32, smallest first.
+// s_7 / 2 = 2^-23 2^floor(log2 amax); a bf16 number not below 2^-15 amax has no rest.
+// A token takes 8 columns of the product, whose sums are added in float32, smallest
+// first.
 //
 // Bound by the weights' bytes: 128 neurons x 256 inputs are 16 KB, a token's
-// eight columns of the same inputs 1 KB.  (Expanding codes in registers for
-// mma.sync, moe_kernel.cuh, takes an SM ten times as long as reading them.)
-//   * warp 0 copies steps of 256 inputs into a ring: 128 rows of one or both
-//     matrices and the 8 rows of each of the pass's tokens (2-D TMA, 128-byte
-//     swizzle);
+// eight columns of the same inputs 1 KB.  32 tokens, 2 of 8 experts of 11008 x 4096
+// each: 78 us, 4.9 TB/s of the two matrices' 383 MB.  (Expanding the codes in registers
+// for mma.sync took 290 us, ten times the copies.)  Both matrices are read whole: with
+// several tokens per expert few neurons are closed for all of them.
+//   * warp 0 copies steps of 256 inputs into a ring: 128 rows of both matrices and
+//     the 8 rows of each of the pass's tokens (2-D TMA, 128-byte swizzle);
 //   * warps 6 to 9 bring the scales of 1024 inputs at a time into the form that
 //     tensor memory takes (the weights' lie row by row, a token's 8 columns
 //     have one row of scales, three less per term);
-//   * one thread of warp 1 copies a step's scales to tensor memory and issues
+//   * one lane of warp 1 copies a step's scales to tensor memory and issues
 //     its MMAs (N = 8 columns per token: tokens that a pass does not have cost
 //     nothing);
-//   * warps 2 to 5 add the terms and store: with one matrix the first factor,
-//     activated; with both h, as three bf16 numbers.
+//   * warps 2 to 5 add the terms, form h and store it as three bf16 numbers.
 // Units of work (an expert, 128 of its neurons, up to 16 of its tokens) are dealt
 // out in turn; the passes of one tile are neighbours, so that the later ones
 // find the rows in L2.  Every wait is bounded.
@@ -39,7 +39,7 @@ namespace {
 constexpr int kFM = 128;                        // neurons per unit
 constexpr int kFABytes = kFM * kGK / 2;
 constexpr int kFThreads = 320;
-constexpr int kMats = 2;                         // matrices: the first factor's, the second's
+constexpr int kMats = 2;                        // matrices: the first factor's, the second's
 constexpr int kFTokens = 16;                    // tokens per pass
 constexpr int kChunk = 4;                       // steps whose scales come at once
 constexpr int kSfOp = kChunk * 2 * kSfTile;     // their bytes per operand
