@@ -28,8 +28,8 @@ struct MoePlan {
   int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
-  // 4-bit weights: four kernels (routing; h, moe_fp4_factors.cu; the down projection
-  // and the sums, moe_fp4_down.cu) instead of one
+  // four kernels (routing; h; the down projection; the sums) on the tensor cores
+  // instead of one: moe_fp4_factors.cu and moe_fp4_down.cu, or moe_bf16_tensor.cu
   int tensor = 0;
 };
 MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k);
@@ -73,8 +73,10 @@ cudaError_t launch_moe_bf16(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_factors(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_fp4_down(const MoeArgs& a, cudaStream_t s);
-cudaError_t launch_moe_fp4_sum(const MoeArgs& a, cudaStream_t s);
-constexpr int kMoeDownTokens = 40, kMoeDownCols = 512;    // moe_fp4_down.cu: per pass, per item
+cudaError_t launch_moe_bf16_tensor(const MoeArgs& a, cudaStream_t s);
+cudaError_t launch_moe_sum(const MoeArgs& a, cudaStream_t s);
+constexpr int kMoeDownTokens = 40;                        // tensor-core down projections: per pass
+constexpr int kMoeDownCols = 512, kMoeDownColsBf16 = 256; // ... columns per item
 constexpr int kMoeXTerms = 8;
 __host__ __device__ constexpr int moe_xs_pitch(int d_model) { return (d_model / 32 + 31) / 32 * 32; }
 

@@ -42,33 +42,6 @@ constexpr int kDTenth = 10;                     // tokens per 32 rows (30 of the
 static_assert(kMoeDownTokens == 4 * kDTenth, "four quarters of 10 tokens");
 constexpr int kDSmem = 2 * (kDB + kDA) + kDCodeStages * kDCodes + 1024;
 
-struct DItem {
-  int e, ai, s, j0, j1, c0, cw, slot0, cnt, steps;
-};
-
-// The items: (expert, range of neurons, tile of columns), the split as in sum_item
-__device__ __forceinline__ int d_splits(const MoeArgs& a, const MoeTables& t) {
-  return max(1, a.plan.grid / (t.cum[t.active] * a.plan.col_tiles));
-}
-__device__ __forceinline__ int d_expert_splits(const MoeArgs& a, const MoeTables& t, int ai, int S) {
-  return min(S * (t.cum[ai + 1] - t.cum[ai]), a.plan.max_splits);
-}
-__device__ __forceinline__ DItem d_item(const MoeArgs& a, const MoeTables& t, int item, int S) {
-  DItem d;
-  int rest = item / a.plan.col_tiles, n = d_expert_splits(a, t, 0, S);
-  for (d.ai = 0; rest >= n; n = d_expert_splits(a, t, ++d.ai, S)) rest -= n;
-  d.s = rest;
-  d.e = t.expert[d.ai];
-  d.j0 = (int)((long long)(a.d_ff / 8) * d.s / n) * 8;
-  d.j1 = (int)((long long)(a.d_ff / 8) * (d.s + 1) / n) * 8;
-  d.c0 = item % a.plan.col_tiles * kDCols;
-  d.cw = min(kDCols, a.d_model - d.c0);
-  d.slot0 = t.first[d.ai];
-  d.cnt = t.count[d.ai];
-  d.steps = (d.j1 - d.j0 + kDK - 1) / kDK;
-  return d;
-}
-
 __device__ __forceinline__ uint32_t d_idesc(uint32_t n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
@@ -143,10 +116,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
   __syncthreads();
   g_after();
   const uint32_t tmem = s_tmem;
-  const int S = d_splits(a, tb);
-  int items = 0;
-  for (int i = 0; i < tb.active; ++i) items += d_expert_splits(a, tb, i, S);
-  items *= a.plan.col_tiles;
+  const int S = moe_splits(a, tb), items = moe_split_sum(a, tb, S) * a.plan.col_tiles;
 
   if (warp == 0 || warp == 2) {
     if (lane == 0) {
@@ -159,7 +129,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-        const DItem d = d_item(a, tb, it, S);
+        const MoeDownItem d = moe_down_item(a, tb, it, S, kDCols, kDK);
         for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
           const int nt = min(kMoeDownTokens, d.cnt - t0), quarters = (nt + kDTenth - 1) / kDTenth;
           for (int ks = 0; ks < d.steps; ++ks, ++n) {
@@ -195,7 +165,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-      const DItem d = d_item(a, tb, it, S);
+      const MoeDownItem d = moe_down_item(a, tb, it, S, kDCols, kDK);
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
         if (piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
         g_after();
@@ -245,7 +215,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     uint32_t cph = 0, ph = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-      const DItem d = d_item(a, tb, it, S);
+      const MoeDownItem d = moe_down_item(a, tb, it, S, kDCols, kDK);
       const uint8_t* sc = a.sd + ((size_t)d.e * a.d_ff + d.j0 + r) * sb + d.c0 / 32;
       const int left = d.j1 - d.j0 - r;                       // rows from this thread's on
       // scales, some steps ahead of their use (from DRAM)
@@ -335,12 +305,12 @@ __global__ void __launch_bounds__(kDThreads, 1)
 // y from the partial sums, in the order of the ranges and then of the choices:
 // 4 outputs per thread.
 constexpr int kSThreads = 128;
-__global__ void __launch_bounds__(kSThreads) moe_fp4_sum_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kSThreads) moe_sum_kernel(const __grid_constant__ MoeArgs a) {
   __shared__ MoeTables tb;
   pdl_begin();
   load_tables(a, tb, kMoeDownTokens, kSThreads);
   __syncthreads();
-  const int S = d_splits(a, tb), n4 = a.d_model / 4;
+  const int S = moe_splits(a, tb), n4 = a.d_model / 4;
   const long long i = (long long)blockIdx.x * kSThreads + threadIdx.x;
   if (i >= (long long)a.T * n4) return;
   const int t = (int)(i / n4), c = (int)(i - (long long)t * n4) * 4;
@@ -352,7 +322,7 @@ __global__ void __launch_bounds__(kSThreads) moe_fp4_sum_kernel(const __grid_con
     int ai = 0;
     for (int step = kMoeMaxE / 2; step; step >>= 1)
       if (ai + step < tb.active && tb.first[ai + step] <= slot) ai += step;
-    const int n = d_expert_splits(a, tb, ai, S);
+    const int n = moe_expert_splits(a, tb, ai, S);
     const float* src = a.parts + (size_t)slot * a.d_model + c;
     float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll 4
@@ -375,9 +345,9 @@ __global__ void __launch_bounds__(kSThreads) moe_fp4_sum_kernel(const __grid_con
 
 }  // namespace
 
-cudaError_t launch_moe_fp4_sum(const MoeArgs& a, cudaStream_t s) {
+cudaError_t launch_moe_sum(const MoeArgs& a, cudaStream_t s) {
   const size_t blocks = ((size_t)a.T * (a.d_model / 4) + kSThreads - 1) / kSThreads;
-  const cudaError_t e = launch_pdl(moe_fp4_sum_kernel, dim3((unsigned)blocks), dim3(kSThreads), 0, s, a);
+  const cudaError_t e = launch_pdl(moe_sum_kernel, dim3((unsigned)blocks), dim3(kSThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

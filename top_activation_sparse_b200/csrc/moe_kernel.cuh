@@ -1541,17 +1541,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
   }
 }
 
+// One kernel or the tensor-core ones.
 // 4-bit weights: one token's layer (d_model <= 4096) in this kernel, everything else
 // by the tensor-core kernels, which read all weights but expand none of them in
 // registers.  8 experts of 4096 x 11008, 2 per token, dReLU without bias: 1 token 55
 // against 73 us, 2 tokens 120 against 106, 8: 244 against 172, 64: 1089 against 249; 60 of
 // 2048 x 1408, 4 per token: 34 / 44, 58 / 44, 104 / 69, 286 / 135.
+// bf16 weights: reading every row costs no more than picking the open ones once two
+// tokens share an expert, or where an expert's rows take less time than the batches'
+// waits.  The same layers, one kernel / tensor cores: 8 experts 2 tokens 157 / 191, 8: 329 /
+// 326 (squared ReLU 443 / 328), 64: 913 / 369; 60 experts 2 tokens 59 / 51, 8: 105 / 102, 64:
+// 370 / 242; 16 of 512 x 512, 2 per token: 4 tokens 36 / 26.
 MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
   p.grid = kNumSMs;
   p.one_token = T == 1 && d_model <= 4096;
-  p.tensor = fp4 && !p.one_token;
+  const long used = n_experts < T * top_k ? n_experts : T * top_k;
+  p.tensor = fp4 ? !p.one_token : T > 1 && (T * top_k >= 2 * n_experts || used * d_ff * d_model * 6 < (256l << 20));
   p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
   p.x_items = !p.local && fp4 && !p.tensor;
   p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
@@ -1575,8 +1582,8 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   if (p.tensor) {
     p.down_tokens = kMoeDownTokens;
-    p.tile_cols = kMoeDownCols;
-    p.col_tiles = (d_model + kMoeDownCols - 1) / kMoeDownCols;
+    p.tile_cols = fp4 ? kMoeDownCols : kMoeDownColsBf16;
+    p.col_tiles = (d_model + p.tile_cols - 1) / p.tile_cols;
   } else {
     // the down projection: tiles of the warps' strips
     p.down_tokens = T <= 8 ? 8 : 16;
@@ -1600,18 +1607,20 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
 
 cudaError_t launch(const MoeArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if constexpr (kFp4) {
-    if (a.plan.tensor) {
-      static unsigned done = 0;
-      e = ensure_smem_attr(moe_route_kernel, (int)sizeof(Smem), &done);
-      if (e != cudaSuccess) return e;
-      const size_t splits = ((size_t)a.T * a.d_model / 8 + kMThreads - 1) / kMThreads;
-      e = launch_pdl(moe_route_kernel, dim3((unsigned)(a.plan.router_items + splits)), dim3(kMThreads), sizeof(Smem), s, a);
+  if (a.plan.tensor) {
+    static unsigned done = 0;
+    e = ensure_smem_attr(moe_route_kernel, (int)sizeof(Smem), &done);
+    if (e != cudaSuccess) return e;
+    const size_t splits = kFp4 ? ((size_t)a.T * a.d_model / 8 + kMThreads - 1) / kMThreads : 0;
+    e = launch_pdl(moe_route_kernel, dim3((unsigned)(a.plan.router_items + splits)), dim3(kMThreads), sizeof(Smem), s, a);
+    if constexpr (kFp4) {
       if (e == cudaSuccess) e = launch_moe_fp4_factors(a, s);
       if (e == cudaSuccess) e = launch_moe_fp4_down(a, s);
-      if (e == cudaSuccess) e = launch_moe_fp4_sum(a, s);
-      return e != cudaSuccess ? e : cudaGetLastError();
+    } else {
+      if (e == cudaSuccess) e = launch_moe_bf16_tensor(a, s);
     }
+    if (e == cudaSuccess) e = launch_moe_sum(a, s);
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
   auto run = [&](auto kernel, unsigned* done) {
     const cudaError_t r = ensure_smem_attr(kernel, (int)sizeof(Smem), done);

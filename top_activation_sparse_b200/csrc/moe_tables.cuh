@@ -33,4 +33,40 @@ __device__ __forceinline__ void load_tables(const MoeArgs& a, MoeTables& t, int 
   }
 }
 
+// The down projection's items: (expert, range of neurons, tile of columns).  Ranges: S
+// per pass over an expert's weights, about one item per CTA in all; the buffers hold
+// max_splits.  (cum: by passes of kMoeDownTokens.)
+struct MoeDownItem {
+  int e, s, j0, j1, c0, cw, slot0, cnt, steps;   // columns [c0, c0 + cw), neurons [j0, j1)
+};
+__device__ __forceinline__ int moe_splits(const MoeArgs& a, const MoeTables& t) {
+  return max(1, a.plan.grid / (t.cum[t.active] * a.plan.col_tiles));
+}
+__device__ __forceinline__ int moe_expert_splits(const MoeArgs& a, const MoeTables& t, int ai, int S) {
+  return min(S * (t.cum[ai + 1] - t.cum[ai]), a.plan.max_splits);
+}
+__device__ __forceinline__ int moe_split_sum(const MoeArgs& a, const MoeTables& t, int S) {
+  int n = 0;
+  for (int ai = 0; ai < t.active; ++ai) n += moe_expert_splits(a, t, ai, S);
+  return n;
+}
+// (whole steps of `step` neurons)
+__device__ __forceinline__ MoeDownItem moe_down_item(const MoeArgs& a, const MoeTables& t, int item, int S, int cols, int step) {
+  MoeDownItem d;
+  int rest = item / a.plan.col_tiles, ai = 0, n = moe_expert_splits(a, t, 0, S);
+  for (; rest >= n; n = moe_expert_splits(a, t, ++ai, S)) rest -= n;
+  d.s = rest;
+  d.e = t.expert[ai];
+  const int all = (a.d_ff + step - 1) / step;
+  const int s0 = (int)((long long)all * rest / n), s1 = (int)((long long)all * (rest + 1) / n);
+  d.j0 = s0 * step;
+  d.j1 = min(s1 * step, a.d_ff);
+  d.steps = s1 - s0;
+  d.c0 = item % a.plan.col_tiles * cols;
+  d.cw = min(cols, a.d_model - d.c0);
+  d.slot0 = t.first[ai];
+  d.cnt = t.count[ai];
+  return d;
+}
+
 }  // namespace qs
