@@ -478,7 +478,7 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
 
 /*
  * qs_moe_ffn -- a mixture-of-experts FFN layer, router included: one kernel per
- *   64 tokens (4-bit weights: four, but for one token with d_model <= 4096).
+ *   64 tokens, or four where all rows of the experts used are read (see below).
  *   Source: Turbo Sparse summary (blog.csdn.net): the method applied to a
  *   model of experts, of which each token uses 2 of 8, and Eq. 2 (dReLU); the
  *   squared-ReLU form is that of qs_sparse_ffn.  The pages give no router; the
@@ -492,9 +492,10 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   a down row is read only where some token's h is not 0: exact skipping, as
  *   in qs_sparse_ffn_gate_first.  Weights of experts that no token uses are
  *   not read.  Each expert weight is read once per 16 of its tokens (8 where
- *   d_model > 4096).  4-bit weights of experts with several tokens, of which
- *   few neurons are closed for all, are read whole, for 16 tokens at a time
- *   (down: 40): same results, a closed neuron contributes 0.
+ *   d_model > 4096).  Where that is faster (small experts, several tokens per
+ *   expert, f32 results, 4-bit weights of more than one token) the experts'
+ *   rows are all read instead, on the tensor cores: same results, a closed neuron
+ *   contributes 0.
  *
  *   x         [T, d_model] bf16.
  *   w_router  [n_experts, d_model] bf16.

@@ -317,3 +317,41 @@ def test_operators_together_eager_and_captured():
         assert torch.equal(u2, u) and torch.equal(r2.y, r.y)
     torch.cuda.synchronize()
     assert torch.equal(gr.y, r.y)
+
+
+@pytest.mark.parametrize("T,dm,dff,E,top_k,one", [(3, 4096, 1832, 8, 2, False), (4, 8192, 688, 16, 2, False),
+                                                  (20, 2048, 1368, 16, 1, True)])
+def test_several_tokens_of_large_bf16_experts(T, dm, dff, E, top_k, one):
+    """Experts large enough that only open rows are read; all tokens of one expert
+    (two passes); no neuron open."""
+    need_gpu()
+    a, vals = make(T + dm, T, dm, dff, E, "drelu", False)
+    if one:
+        a["x"][:, 0] = 40.0
+        a["w_router"][:, 0] = 0.0
+        a["w_router"][5, 0] = 4.0
+    call = lambda: qs.qs_moe_ffn(top_k=top_k, act="drelu", experts=True, weights=True, **a)  # noqa: E731
+    r = call()
+    check(r, reference(a, vals, top_k, "drelu"), dm, torch.bfloat16)
+    if one:
+        assert int((r.experts != 5).sum()) == 0
+    assert torch.equal(call().y, r.y)
+    a["b_gate"][:] = -1000.0
+    assert torch.count_nonzero(call().y).item() == 0
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_f32_results_of_long_sums(fp4):
+    """h of both signs over 9000 neurons: the error stays that of float32 sums, 2^-24
+    sqrt(number of additions) of the result, where sums cut off at every step of the
+    matrix instructions would lose 2^-25 per step (here over 500 steps, 1.7e-5)."""
+    need_gpu()
+    T, dm, dff, E = 6, 512, 9000, 2
+    a, vals = make(77, T, dm, dff, E, "relu2_glu", fp4)
+    r = qs.qs_moe_ffn(top_k=1, act="relu2_glu", y_dtype=torch.float32, **a)
+    want = reference(a, vals, 1, "relu2_glu")["y"]
+    err = np.linalg.norm(to_np(r.y) - want, axis=1) / np.linalg.norm(want, axis=1)
+    # three factors of h, each a sum over 512, and the sum over 9000, all as float32
+    # sums with half a step per addition: 2^-24 (3 sqrt(512) + sqrt(9000)) = 1e-5 at worst,
+    # a third of it for signs that cancel
+    assert np.all(err <= 2.0 ** -24 * (3 * 512 ** 0.5 + 9000 ** 0.5) / 3), float(err.max())

@@ -980,7 +980,7 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
     a.y = (unsigned char*)y + (size_t)t0 * d_model * elem_bytes(y_dtype);
     a.experts = experts ? experts + (size_t)t0 * top_k : nullptr;
     a.weights = weights ? weights + (size_t)t0 * top_k : nullptr;
-    a.plan = (fp4 ? plan_moe_fp4 : plan_moe_bf16)(a.T, d_model, d_ff, n_experts, top_k);
+    a.plan = (fp4 ? plan_moe_fp4 : plan_moe_bf16)(a.T, d_model, d_ff, n_experts, top_k, y_dtype == QS_BF16);
     QS_TRY_CUDA((fp4 ? launch_moe_fp4 : launch_moe_bf16)(a, (cudaStream_t)stream));
   }
   return QS_OK;

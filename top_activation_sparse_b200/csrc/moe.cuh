@@ -7,7 +7,7 @@ namespace qs {
 
 constexpr int kMoeMaxT = 64;          // tokens per launch
 constexpr int kMoeMaxModel = QS_MOE_MAX_MODEL;
-constexpr int kMoePartRows = 1024;    // rows of partial sums (splits x tokens x experts per token)
+constexpr int kMoePartRows = 2048;    // rows of partial sums (splits x tokens x experts per token)
 
 // counters, zero between calls
 enum MoeCtl { MC_QUEUE = 0, MC_ROUTED = 1, MC_READY = 2, MC_HIDDEN = 3, MC_DOWN = 4, MC_EXIT = 5, MC_COUNT = 8 };
@@ -28,12 +28,13 @@ struct MoePlan {
   int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
+  int min_splits = 1;       // ... that keep a sum on the tensor cores short enough for f32 results
   // four kernels (routing; h; the down projection; the sums) on the tensor cores
   // instead of one: moe_fp4_factors.cu and moe_fp4_down.cu, or moe_bf16_tensor.cu
   int tensor = 0;
 };
-MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k);
-MoePlan plan_moe_fp4(int T, int d_model, int d_ff, int n_experts, int top_k);
+MoePlan plan_moe_bf16(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16);
+MoePlan plan_moe_fp4(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16);
 
 struct MoeArgs {
   const __nv_bfloat16* x = nullptr;       // [T, d_model]

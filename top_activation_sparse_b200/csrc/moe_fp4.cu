@@ -8,8 +8,8 @@ constexpr bool kFp4 = true;
 #include "moe_kernel.cuh"
 
 namespace qs {
-MoePlan plan_moe_fp4(int T, int d_model, int d_ff, int n_experts, int top_k) {
-  return make_plan(T, d_model, d_ff, n_experts, top_k);
+MoePlan plan_moe_fp4(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16) {
+  return make_plan(T, d_model, d_ff, n_experts, top_k, y_bf16);
 }
 cudaError_t launch_moe_fp4(const MoeArgs& a, cudaStream_t s) { return launch(a, s); }
 }  // namespace qs

@@ -1,7 +1,7 @@
-// A whole mixture-of-experts FFN layer in one kernel: bf16 weights for up to 64
-// tokens, 4-bit weights for one.  Included by moe_bf16.cu and moe_fp4.cu, which say with
-// what weights (kFp4).  (4-bit weights for more tokens: the routing kernel below,
-// moe_fp4_factors.cu, moe_fp4_down.cu.)
+// A whole mixture-of-experts FFN layer in one kernel: one token, or several of large
+// bf16 experts (make_plan says when).  Included by moe_bf16.cu and moe_fp4.cu, which say with
+// what weights (kFp4).  (Everything else: the routing kernel below, then
+// moe_bf16_tensor.cu, or moe_fp4_factors.cu and moe_fp4_down.cu.)
 //
 //   logits = x W_r^T;  each token's top_k largest (ties: lower expert) are its
 //   experts, p = softmax over them;  for each (token, expert e):
@@ -48,8 +48,8 @@
 //
 // 1 token, 2 of 8 dReLU experts of 14336 x 4096: bf16 76 us (46 at the memory's rate),
 // 4-bit 66 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
-// about 7 us of routing, 4 for the first rows, 8 for the last sums).  8 tokens, squared ReLU, 8 experts of
-// 11008 x 4096, bf16: 447 us (259), 3.7 TB/s of the rows that are open.
+// about 7 us of routing, 4 for the first rows, 8 for the last sums).  2 tokens, 8 experts of
+// 11008 x 4096, bf16: 157 us.
 #pragma once
 
 #include "fp4.cuh"
@@ -1552,13 +1552,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 // waits.  The same layers, one kernel / tensor cores: 8 experts 2 tokens 157 / 191, 8: 329 /
 // 326 (squared ReLU 443 / 328), 64: 913 / 369; 60 experts 2 tokens 59 / 51, 8: 105 / 102, 64:
 // 370 / 242; 16 of 512 x 512, 2 per token: 4 tokens 36 / 26.
-MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
+// f32 results: matrix instructions cut a sum off at each step, 3e-8 of it.  This kernel's
+// down sums (200 steps and more) put y off by 3e-6, the bf16 tensor-core kernels' (which
+// add up every 128 neurons) by 5e-7: those for every call of several tokens.  4-bit
+// weights: ranges of at most 2048 neurons (11008 neurons in two ranges: 2.5e-6).
+MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
   p.grid = kNumSMs;
   p.one_token = T == 1 && d_model <= 4096;
   const long used = n_experts < T * top_k ? n_experts : T * top_k;
-  p.tensor = fp4 ? !p.one_token : T > 1 && (T * top_k >= 2 * n_experts || used * d_ff * d_model * 6 < (256l << 20));
+  p.tensor = fp4 ? !p.one_token
+                 : T > 1 && (!y_bf16 || T * top_k >= 2 * n_experts || used * d_ff * d_model * 6 < (256l << 20));
   p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
   p.x_items = !p.local && fp4 && !p.tensor;
   p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
@@ -1602,6 +1607,7 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k) {
   if (p.max_splits > p.grid) p.max_splits = p.grid;
   // (tensor cores: at least four steps of 64 neurons)
   if (p.tensor && p.max_splits > d_ff / 256) p.max_splits = d_ff < 512 ? 1 : d_ff / 256;
+  if (fp4 && !y_bf16) p.min_splits = (d_ff + 2047) / 2048;
   return p;
 }
 
