@@ -600,12 +600,13 @@ def _fp4_code(table, name):
     return table[name] if isinstance(name, str) else int(name)
 
 
-def _out8(spec, shape, like):
-    """A uint8 output on `like`'s device: spec as for _out, checked for placement."""
+def _out_like(spec, shape, dtype, like):
+    """An output on `like`'s device: spec as for _out, checked for placement."""
     if spec is True:
-        return like.new_empty(shape, dtype=torch.uint8)
-    out = _out(spec, shape, torch.uint8, like.device)
-    _need_cuda(like, out)
+        return like.new_empty(shape, dtype=dtype)
+    out = _out(spec, shape, dtype, like.device)
+    if out is not None:
+        _need_cuda(like, out)
     return out
 
 
@@ -637,12 +638,10 @@ def qs_fp4_quantize(x: torch.Tensor, format="mx", scale_layout="tiled", tensor_s
         raise QSError("qs_fp4_quantize", QS_ERR_ALIGNMENT)
     R, lead = x.numel() // d, x.shape[:-1]
     with _call_context(dev, stream, x, tensor_scale, codes, scales, values):
-        codes = _out8(codes, (*lead, d // 2), x)
-        scales = _out8(scales, (*lead, d // (32 if fmt == QS_FP4_MX else 16)) if lay == QS_FP4_SCALES_ROWS else
-                       (qs_fp4_scale_bytes(R, d, fmt, lay),), x)
-        values = torch.empty_like(x) if values is True else _out(values, x.shape, x.dtype, dev)
-        if values is not None:
-            _need_cuda(x, values)
+        codes = _out_like(codes, (*lead, d // 2), torch.uint8, x)
+        scales = _out_like(scales, (*lead, d // (32 if fmt == QS_FP4_MX else 16)) if lay == QS_FP4_SCALES_ROWS else
+                           (qs_fp4_scale_bytes(R, d, fmt, lay),), torch.uint8, x)
+        values = torch.empty_like(x) if values is True else _out_like(values, x.shape, x.dtype, x)
         _check("qs_fp4_quantize", lib().qs_fp4_quantize(
             x.data_ptr(), _dtype_code(x), R, d, fmt, _ptr(tensor_scale), lay, _ptr(codes),
             _ptr(scales), _ptr(values), _current_stream_ptr(dev)))
@@ -666,8 +665,7 @@ def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch
     if w_scales.dtype != torch.uint8 or w_scales.numel() != qs_fp4_scale_bytes(d_out, d_in, fmt, QS_FP4_SCALES_TILED):
         raise ValueError("w_scales must be the tiled uint8 scales of W [d_out, d_in]")
     with _call_context(dev, stream, x, w_codes, w_scales, x_scale, w_scale, y):
-        y = _out(y if y is not None else True, (T, d_out), y.dtype if y is not None else (y_dtype or x.dtype), dev)
-        _need_cuda(x, y)
+        y = _out_like(True if y is None else y, (T, d_out), (y_dtype or x.dtype) if y is None else y.dtype, x)
         ws = _stream_workspace(ws, QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, dev)
         _check("qs_fp4_sparse_linear", lib().qs_fp4_sparse_linear(
             x.data_ptr(), _dtype_code(x), T, d_in, d_out, k, fmt, _ptr(x_scale), w_codes.data_ptr(),
@@ -709,10 +707,9 @@ def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, 
     act_code = _ACTS[act] if isinstance(act, str) else int(act)
     with _call_context(dev, stream, x, w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, b_gate, b_up, y,
                        experts, weights):
-        y = _out(y if y is not None else True, (T, d_model), y.dtype if y is not None else (y_dtype or x.dtype), dev)
-        experts = _out(experts, (T, top_k), torch.int32, dev)
-        weights = _out(weights, (T, top_k), torch.float32, dev)
-        _need_cuda(x, y, experts, weights)
+        y = _out_like(True if y is None else y, (T, d_model), (y_dtype or x.dtype) if y is None else y.dtype, x)
+        experts = _out_like(experts, (T, top_k), torch.int32, x)
+        weights = _out_like(weights, (T, top_k), torch.float32, x)
         ws = _stream_workspace(ws, QS_OP_MOE_FFN, T, d_model, d_ff, top_k, dev)
         _check("qs_moe_ffn", lib().qs_moe_ffn(
             x.data_ptr(), T, d_model, d_ff, E, top_k, act_code, w_router.data_ptr(), w_gate.data_ptr(),
