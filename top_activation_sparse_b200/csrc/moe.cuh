@@ -28,7 +28,7 @@ struct MoePlan {
   int x_bytes = 0;          // shared memory of x (4-bit weights)
   int row_bytes = 0, scale_bytes = 0, stage_bytes = 0, pitch = 0, stage_rows = 0, stages = 0;   // the ring
   int max_splits = 0;       // splits of an expert's neurons the buffers hold
-  int min_splits = 1;       // ... that keep a sum on the tensor cores short enough for f32 results
+  int sum_steps = 0;        // 4-bit down projection: steps of 64 neurons per sum in tensor memory
   // four kernels (routing; h; the down projection; the sums) on the tensor cores
   // instead of one: moe_fp4_factors.cu and moe_fp4_down.cu, or moe_bf16_tensor.cu
   int tensor = 0;

@@ -14,8 +14,13 @@
 //     contiguous, swizzled).  The columns of a group of 8 are stored in the order
 //     0 4 1 5 2 6 3 7: a word's nibbles i and i + 4 make a pair without moves;
 //   * one lane of warp 1 issues the MMAs;
-//   * warps 3 to 6 add a token's three rows and store.
-// 32 tokens, 2 of 8 experts of 11008 x 4096 each: 103 us, 1.8 TB/s of the 190 MB.
+//   * the expanding warps add a token's three rows, and what they add up to onto the
+//     sums before.
+// The tensor core cuts its sums off instead of rounding them, which adds up with their
+// number: after sum_steps steps a sum leaves tensor memory, whatever the range's length
+// (64 tokens, 16 of 16 experts of 28672 x 1024 each, f32 results: y off by 4.7e-7 of itself with 16
+// steps, 8.7e-7 with 32, 7.6e-6 with a whole range of 14336 neurons).
+// 32 tokens, 2 of 8 experts of 11008 x 4096 each: 112 us, 1.7 TB/s of the 190 MB (4 us of it per sum).
 // Bound by the step's chain: the expansion (1200 cycles of issue) and the MMAs (900)
 // overlap, but each hand-over through a barrier takes 300 to 400 cycles while the
 // expansion's stores fill the queue that barriers go through.  Smaller steps with four
@@ -82,6 +87,12 @@ __device__ __forceinline__ void d_expand(const uint32_t (&v)[4], uint32_t s, uin
                  : "memory");
 }
 
+// (an address is added to by one thread only, so that the order is fixed; a reduction at
+// L2, for which nothing waits: loading, adding and storing took 30 us per sum more)
+__device__ __forceinline__ void d_add4(float* p, float x, float y, float z, float w) {
+  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+
 __global__ void __launch_bounds__(kDThreads, 1)
     moe_fp4_down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
                         const __grid_constant__ MoeArgs a) {
@@ -100,7 +111,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
     for (int i = 0; i < kDCodeStages; ++i) mbar_init(&s_cfull[i], 1), mbar_init(&s_cempty[i], kDExpand);
     for (int i = 0; i < 2; ++i) mbar_init(&s_afull[i], 1), mbar_init(&s_bfull[i], kDExpand), mbar_init(&s_empty[i], 1);
     mbar_init(&s_tfull, 1);
-    mbar_init(&s_tempty, 4);
+    mbar_init(&s_tempty, kDExpand);
     mbar_init(&s_done, 1);
     mbar_fence_init();
     s_abort = 0;
@@ -166,29 +177,31 @@ __global__ void __launch_bounds__(kDThreads, 1)
     bool ok = true;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const MoeDownItem d = moe_down_item(a, tb, it, S, kDCols, kDK);
-      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
-        if (piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
-        g_after();
+      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
         const uint32_t id0 = d_idesc((uint32_t)min(256, d.cw)), id1 = d_idesc((uint32_t)max(16, d.cw - 256));
-        for (int ks = 0; ks < d.steps; ++ks) {
+        for (int ks = 0, in = 0; ks < d.steps; ++ks) {         // in: this step's place in its sum
+          if (in == 0 && piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
           // (h has arrived too: the first expanding warp has waited for it)
           if (!(ok = g_wait(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
           g_after();
           const uint64_t ad = a0 + (uint64_t)(b * (kDA / 16)), bd = b0 + (uint64_t)(b * (kDB / 16));
+          const bool last = in == a.plan.sum_steps - 1 || ks == d.steps - 1;
           if (issues) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               if (half * 256 >= d.cw) break;
 #pragma unroll
               for (int kk = 0; kk < kDK / 16; ++kk)
-                d_mma(tmem + half * 256, ad + kk * 2, bd + half * (4 * kDBox / 16) + kk * 128, half ? id1 : id0, ks > 0 || kk > 0);
+                d_mma(tmem + half * 256, ad + kk * 2, bd + half * (4 * kDBox / 16) + kk * 128, half ? id1 : id0, in > 0 || kk > 0);
             }
             g_commit(&s_empty[b]);
+            if (last) g_commit(&s_tfull);
           }
           __syncwarp();
+          if (last) ++piece, in = 0;
+          else ++in;
           if ((b ^= 1) == 0) ph ^= 1u;
         }
-        if (ok && issues) g_commit(&s_tfull);
       }
     }
     if (issues) {
@@ -225,10 +238,14 @@ __global__ void __launch_bounds__(kDThreads, 1)
         for (int i = 0; i < 2; ++i)
           to[i] = ks * kDK < left && (cb + 4 * i) * 32 < d.cw ? (uint32_t)__ldg(sc + (size_t)ks * kDK * sb + cb + 4 * i) : 0u;
       };
-      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens, ++piece) {
+      for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
+        // results: 10 tokens per quarter of the lanes, three rows each
+        const int q = warp & 3, tok = t0 + q * kDTenth + lane / 3;
+        const bool mine = lane < 30 && lane % 3 == 0 && tok < d.cnt;
+        float* o = a.parts + ((size_t)d.s * a.T * a.top_k + d.slot0 + (mine ? tok : 0)) * a.d_model + d.c0;
 #pragma unroll
         for (int i = 0; i < kDAhead; ++i) ahead(i, next[i]);
-        for (int ks = 0; ks < d.steps; ++ks) {
+        for (int ks = 0, in = 0; ks < d.steps; ++ks) {
           const uint32_t s[2] = {next[0][0], next[0][1]};
           const bool there = ks * kDK < left;
 #pragma unroll
@@ -263,34 +280,42 @@ __global__ void __launch_bounds__(kDThreads, 1)
           if (lane == 0) mbar_arrive(&s_bfull[b]);
           if (++csl == kDCodeStages) csl = 0, cph ^= 1u;
           if ((b ^= 1) == 0) ph ^= 1u;
-        }
-        if (!ok || w >= 4) continue;
-        // ---- results: 10 tokens per quarter of the lanes, three rows each ----
-        if (!(ok = g_wait(&s_tfull, (uint32_t)piece & 1u, &s_abort, a.status, 96))) break;
-        g_after();
-        const int q = warp & 3, tok = t0 + q * kDTenth + lane / 3;
-        const bool mine = lane < 30 && lane % 3 == 0 && tok < d.cnt;
-        const size_t slots = (size_t)a.T * a.top_k;
-        float* o = a.parts + ((size_t)d.s * slots + d.slot0 + (mine ? tok : 0)) * a.d_model + d.c0;
-        if (t0 + q * kDTenth < d.cnt)
-          for (int c = 0; c < d.cw; c += 8) {
-            uint32_t u[8];
-            g_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, u);
-            g_ld_wait();
-            float y[8];
+          if (++in < a.plan.sum_steps && ks < d.steps - 1) continue;
+          in = 0;
+          // ---- the sum's results, onto those of the range's sums before it: four
+          // warps per quarter of the lanes, 32 columns in turn ----
+          if (!(ok = g_wait(&s_tfull, (uint32_t)piece++ & 1u, &s_abort, a.status, 96))) break;
+          g_after();
+          if (t0 + q * kDTenth < d.cnt)
+            for (int c = (w >> 2) * 32; c < d.cw; c += kDExpand / 4 * 32) {
+              uint32_t u[4][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float f = d.steps > 0 ? __uint_as_float(u[i]) : 0.0f;      // (a range without neurons)
-              y[i] = (__shfl_down_sync(0xffffffffu, f, 2) + __shfl_down_sync(0xffffffffu, f, 1)) + f;
+              for (int g = 0; g < 4; ++g) g_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c + 8 * g), u[g]);
+              g_ld_wait();
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float f = __uint_as_float(u[g][i]);
+                  y[i] = (__shfl_down_sync(0xffffffffu, f, 2) + __shfl_down_sync(0xffffffffu, f, 1)) + f;
+                }
+                if (mine) {
+                  float* to = o + c + 8 * g;
+                  if (ks >= a.plan.sum_steps) {
+                    d_add4(to, y[0], y[2], y[4], y[6]);
+                    d_add4(to + 4, y[1], y[3], y[5], y[7]);
+                  } else {
+                    __stcg(reinterpret_cast<float4*>(to), make_float4(y[0], y[2], y[4], y[6]));
+                    __stcg(reinterpret_cast<float4*>(to) + 1, make_float4(y[1], y[3], y[5], y[7]));
+                  }
+                }
+              }
             }
-            if (mine) {
-              __stcg(reinterpret_cast<float4*>(o + c), make_float4(y[0], y[2], y[4], y[6]));
-              __stcg(reinterpret_cast<float4*>(o + c + 4), make_float4(y[1], y[3], y[5], y[7]));
-            }
-          }
-        g_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_tempty);
+          g_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_tempty);
+        }
       }
     }
   }

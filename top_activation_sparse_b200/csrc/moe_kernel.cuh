@@ -1555,7 +1555,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 // f32 results: matrix instructions cut a sum off at each step, 3e-8 of it.  This kernel's
 // down sums (200 steps and more) put y off by 3e-6, the bf16 tensor-core kernels' (which
 // add up every 128 neurons) by 5e-7: those for every call of several tokens.  4-bit
-// weights: ranges of at most 2048 neurons (11008 neurons in two ranges: 2.5e-6).
+// weights: sums of 1024 neurons (4e-7, as of a plain float32 product), of 2048 for bf16 results
+// (8e-7; the 32-token layer 202 instead of 214 us).
 MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
@@ -1607,7 +1608,7 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y
   if (p.max_splits > p.grid) p.max_splits = p.grid;
   // (tensor cores: at least four steps of 64 neurons)
   if (p.tensor && p.max_splits > d_ff / 256) p.max_splits = d_ff < 512 ? 1 : d_ff / 256;
-  if (fp4 && !y_bf16) p.min_splits = (d_ff + 2047) / 2048;
+  p.sum_steps = y_bf16 ? 32 : 16;
   return p;
 }
 

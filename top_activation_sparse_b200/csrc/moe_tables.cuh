@@ -43,7 +43,7 @@ __device__ __forceinline__ int moe_splits(const MoeArgs& a, const MoeTables& t) 
   return max(1, a.plan.grid / (t.cum[t.active] * a.plan.col_tiles));
 }
 __device__ __forceinline__ int moe_expert_splits(const MoeArgs& a, const MoeTables& t, int ai, int S) {
-  return min(max(S * (t.cum[ai + 1] - t.cum[ai]), a.plan.min_splits), a.plan.max_splits);
+  return min(S * (t.cum[ai + 1] - t.cum[ai]), a.plan.max_splits);
 }
 __device__ __forceinline__ int moe_split_sum(const MoeArgs& a, const MoeTables& t, int S) {
   int n = 0;
