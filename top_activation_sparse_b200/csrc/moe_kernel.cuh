@@ -1553,8 +1553,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 // 326 (squared ReLU 443 / 328), 64: 913 / 369; 60 experts 2 tokens 59 / 51, 8: 105 / 102, 64:
 // 370 / 242; 16 of 512 x 512, 2 per token: 4 tokens 36 / 26.
 // f32 results: matrix instructions cut a sum off at each step, 3e-8 of it.  This kernel's
-// down sums (200 steps and more) put y off by 3e-6, the bf16 tensor-core kernels' (which
-// add up every 128 neurons) by 5e-7: those for every call of several tokens.  4-bit
+// sums over d_model and its down sums (200 steps and more) put y off by 2e-6 to 3e-6, the bf16
+// tensor-core kernels' (which add up every 128 terms) by 6e-7: those for every call of several
+// tokens or of d_model above 4096 (one token, whose results are bf16 or whose d_model is at most
+// 4096, stays here: 2 of 4 experts of 11008 x 8192, f32: 330 / 210 us, of 64 of 1024 x 8192: 69 / 78).  4-bit
 // weights: sums of 1024 neurons (4e-7, as of a plain float32 product), of 2048 for bf16 results
 // (8e-7; the 32-token layer 202 instead of 214 us).
 MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16) {
@@ -1564,7 +1566,8 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y
   p.one_token = T == 1 && d_model <= 4096;
   const long used = n_experts < T * top_k ? n_experts : T * top_k;
   p.tensor = fp4 ? !p.one_token
-                 : T > 1 && (!y_bf16 || T * top_k >= 2 * n_experts || used * d_ff * d_model * 6 < (256l << 20));
+                 : !p.one_token &&
+                       (!y_bf16 || (T > 1 && (T * top_k >= 2 * n_experts || used * d_ff * d_model * 6 < (256l << 20))));
   p.local = !p.tensor && T <= 8 && n_experts <= 64 && n_experts * d_model <= 65536;
   p.x_items = !p.local && fp4 && !p.tensor;
   p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
