@@ -29,6 +29,8 @@
  *             counters at zero again when its kernels finish, so a workspace is
  *             reused without clearing.  Calls that share one workspace must be
  *             ordered (same stream, or event-ordered): overlapping them races.
+ *             A call may enqueue several kernels, so two host threads must not be
+ *             inside calls with one workspace at the same time, on one stream either.
  *   Errors.   Argument errors are detected on the host, before anything is
  *             enqueued, and returned as a qs_status; a failed launch returns
  *             QS_ERR_CUDA.  Conditions only the device can see (a bounded wait

@@ -15,6 +15,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 from typing import NamedTuple
 
 import torch
@@ -219,21 +220,6 @@ def new_workspace(op: int, T: int, d_in: int, d_out: int, k: int, device) -> tor
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-_ws_cache: dict = {}
-
-
-def _workspace(ws, op, T, d_in, d_out, k, device):
-    if ws is not None:
-        return ws
-    need = qs_workspace_size(op, T, d_in, d_out, k)
-    key = (device, op)
-    cur = _ws_cache.get(key)
-    if cur is None or cur.numel() < need:
-        cur = torch.zeros(max(need, 1), dtype=torch.uint8, device=device)
-        _ws_cache[key] = cur
-    return cur
-
-
 def _current_stream_ptr(dev) -> int:
     """The device's current stream as the library takes it, without building a
     Stream object (a third of a small call's time on the host)."""
@@ -259,30 +245,47 @@ def _call_context(dev, stream, *tensors):
     return _HERE_CONTEXT
 
 
-_ws_need: dict = {}
-_stream_ws: dict = {}
+_kept = threading.local()                # .ws: this thread's workspaces
 _WS_COUNTER_BYTES = 256 + 64 * 1024      # the part that has to be zero before a first use
 
 
-def _stream_workspace(ws, op, T, d_in, d_out, k, device):
-    """The caller's workspace, or one kept per device, stream and op, so that
-    calls on two streams do not share one.  During a stream capture the graph
-    gets one of its own, cleared at each replay."""
+@functools.lru_cache(maxsize=4096)
+def _workspace_need(op, T, d_in, d_out, k) -> int:
+    return qs_workspace_size(op, T, d_in, d_out, k)
+
+
+def _stream_workspace(ws, op, T, d_in, d_out, k, device, zeroed=_WS_COUNTER_BYTES):
+    """The caller's workspace, or one kept per thread, device, stream and op.  (A
+    call enqueues several kernels that hand data over through the workspace, and
+    the library is called without the interpreter's lock: with one workspace for two threads
+    on one stream, kernels of one call could land between those of the other.)
+    During a stream capture the graph gets one of its own, whose first `zeroed`
+    bytes are cleared at each replay."""
     if ws is not None:
         return ws
-    size = (op, T, d_in, d_out, k)
-    need = _ws_need.get(size)
-    if need is None:
-        need = _ws_need[size] = qs_workspace_size(*size)
+    need = _workspace_need(op, T, d_in, d_out, k)
     if torch.cuda.is_current_stream_capturing():
         cur = torch.empty(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
-        cur[:_WS_COUNTER_BYTES].zero_()
+        cur[:zeroed].zero_()
         return cur
+    try:
+        kept = _kept.ws
+    except AttributeError:
+        kept = _kept.ws = {}
     key = (device, _current_stream_ptr(device), op)
-    cur = _stream_ws.get(key)
+    cur = kept.get(key)
     if cur is None or cur.numel() < need:
-        cur = _stream_ws[key] = torch.zeros(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
+        cur = kept[key] = torch.zeros(max(need, _WS_COUNTER_BYTES), dtype=torch.uint8, device=device)
     return cur
+
+
+def _workspace(ws, op, T, d_in, d_out, k, device, stream=None):
+    """_stream_workspace for `stream`, or the current one, for the ops that also
+    add into sums which the call before has left at zero."""
+    if ws is not None:
+        return ws
+    with _call_context(device, stream):
+        return _stream_workspace(ws, op, T, d_in, d_out, k, device, zeroed=None)
 
 
 def qs_device_status(ws: torch.Tensor, stream=None) -> int:
@@ -364,7 +367,7 @@ def qs_topk_mask(x: torch.Tensor, k: int, idx=True, val=None, mask=None, xs=None
     mask = _out(mask, (T, d), torch.uint8, dev)
     xs = _out(xs, (T, d), x.dtype, dev)
     _need_cuda(idx, val, mask, xs)
-    ws = _workspace(ws, QS_OP_TOPK_MASK, T, d, 0, k, dev)
+    ws = _workspace(ws, QS_OP_TOPK_MASK, T, d, 0, k, dev, stream)
     _check("qs_topk_mask", lib().qs_topk_mask(
         x.data_ptr(), _dtype_code(x), T, d, k, _ptr(idx), _ptr(val), _ptr(mask), _ptr(xs),
         ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
@@ -390,7 +393,7 @@ def qs_sparse_linear(x: torch.Tensor, wt: torch.Tensor, k: int, y=None, phase_ev
         raise ValueError("wt must be [d_in, d_out] with x's dtype")
     y = _out(y if y is not None else True, (T, d_out), x.dtype, dev)
     _need_cuda(y)
-    ws = _workspace(ws, QS_OP_SPARSE_LINEAR, T, d_in, d_out, k, dev)
+    ws = _workspace(ws, QS_OP_SPARSE_LINEAR, T, d_in, d_out, k, dev, stream)
     ev = _events(phase_events, QS_LINEAR_PHASE_EVENTS)
     if block == 1:
         _check("qs_sparse_linear", lib().qs_sparse_linear(
@@ -443,7 +446,7 @@ def qs_sparse_linear_backward(x, wt, grad_y, k: int, grad_x=True, grad_wt=True, 
         grad_wt = torch.zeros(d_in, d_out, dtype=torch.float32, device=dev)
     grad_wt = _out(grad_wt, (d_in, d_out), torch.float32, dev)
     _need_cuda(grad_x, grad_wt)
-    ws = _workspace(ws, QS_OP_SPARSE_LINEAR, T, d_in, d_out, k, dev)
+    ws = _workspace(ws, QS_OP_SPARSE_LINEAR, T, d_in, d_out, k, dev, stream)
     _check("qs_sparse_linear_backward", lib().qs_sparse_linear_backward(
         x.data_ptr(), _dtype_code(x), T, d_in, d_out, k, int(block), wt.data_ptr(),
         grad_y.data_ptr(), _ptr(grad_x), _ptr(grad_wt), ws.data_ptr(), ws.numel(),
@@ -477,7 +480,7 @@ def qs_sparse_ffn(x, wt_up, wt_gate, wt_down, act, k_in: int, k_h: int, b_up=Non
     idx_h_out = _out(idx_h_out, (T, k_h), torch.int32, dev)
     _need_cuda(y, h_out, idx_h_out)
     ev = _events(phase_events, QS_FFN_PHASE_EVENTS)
-    ws = _workspace(ws, QS_OP_SPARSE_FFN, T, d_model, d_ff, k_h, dev)
+    ws = _workspace(ws, QS_OP_SPARSE_FFN, T, d_model, d_ff, k_h, dev, stream)
     if block == 1:
         _check("qs_sparse_ffn", lib().qs_sparse_ffn(
             x.data_ptr(), _dtype_code(x), T, d_model, d_ff, act_code, k_in, k_h,
@@ -512,7 +515,7 @@ def qs_sparse_ffn_gate_first(x, wt_gate, w_up, wt_down, k_h: int, b_up=None, b_g
     idx_h_out = _out(idx_h_out, (T, k_h), torch.int32, dev)
     _need_cuda(y, h_out, idx_h_out)
     ev = _events(phase_events, QS_FFN_PHASE_EVENTS)
-    ws = _workspace(ws, QS_OP_SPARSE_FFN_GATE_FIRST, T, d_model, d_ff, k_h, dev)
+    ws = _workspace(ws, QS_OP_SPARSE_FFN_GATE_FIRST, T, d_model, d_ff, k_h, dev, stream)
     _check("qs_sparse_ffn_gate_first", lib().qs_sparse_ffn_gate_first(
         x.data_ptr(), _dtype_code(x), T, d_model, d_ff, k_h, wt_gate.data_ptr(), w_up.data_ptr(),
         _ptr(b_up), _ptr(b_gate), wt_down.data_ptr(), y.data_ptr(), _ptr(h_out), _ptr(idx_h_out),
@@ -542,7 +545,7 @@ def qs_quant_sparse_linear(x, wt_packed, alpha: float, k: int, eps: float = 1e-5
     q = _out(q, (T, d_in), torch.int8, dev)
     idx = _out(idx, (T, k), torch.int32, dev)
     _need_cuda(y, acc, q, idx)
-    ws = _workspace(ws, QS_OP_QUANT_SPARSE_LINEAR, T, d_in, d_out, k, dev)
+    ws = _workspace(ws, QS_OP_QUANT_SPARSE_LINEAR, T, d_in, d_out, k, dev, stream)
     ev = _events(phase_events, QS_LINEAR_PHASE_EVENTS)
     if block == 1:
         _check("qs_quant_sparse_linear", lib().qs_quant_sparse_linear(
@@ -580,7 +583,7 @@ def qs_quant_sparse_ffn(x, wp_up, alpha_up: float, wp_gate, alpha_gate: float, w
     y = _out(y if y is not None else True, (T, d_model), torch.float32, dev)
     h_out = _out(h_out, (T, d_ff), torch.float32, dev)
     _need_cuda(y, h_out)
-    ws = _workspace(ws, QS_OP_QUANT_SPARSE_FFN, T, d_model, d_ff, k_h, dev)
+    ws = _workspace(ws, QS_OP_QUANT_SPARSE_FFN, T, d_model, d_ff, k_h, dev, stream)
     _check("qs_quant_sparse_ffn", lib().qs_quant_sparse_ffn(
         x.data_ptr(), _dtype_code(x), T, d_model, d_ff, act_code, k_in, k_h, int(block),
         wp_up.data_ptr(), float(alpha_up), wp_gate.data_ptr(), float(alpha_gate),
@@ -732,7 +735,7 @@ def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_ou
     wt_packed = _out(wt_packed if wt_packed is not None else True, (d_in, d_out // 16),
                      torch.int32, dev)
     alpha_out = _out(alpha_out if alpha_out is not None else True, (1,), torch.float32, dev)
-    ws = _workspace(ws, QS_OP_TERNARY_PACK, 0, d_in, d_out, 0, dev)
+    ws = _workspace(ws, QS_OP_TERNARY_PACK, 0, d_in, d_out, 0, dev, stream)
     _check("qs_ternary_pack", lib().qs_ternary_pack(
         w.data_ptr(), d_out, d_in, float(eps), wt_packed.data_ptr(), alpha_out.data_ptr(),
         ws.data_ptr(), ws.numel(), _stream_ptr(stream)))
