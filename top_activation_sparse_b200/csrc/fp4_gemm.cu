@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
       const int len = gmin(left, nk - w.ks);
       const int col = w.mt * kGM + q * 32 + lane;
       const int tok0 = w.nt * NT, ntok = gmin(NT, a.T - tok0);
-      const bool ok = g_wait(&s_tfull[piece % S::kNacc], (uint32_t)(piece / S::kNacc) & 1u, &s_abort, a.status, 63);
+      const bool ok = g_wait_warp(&s_tfull[piece % S::kNacc], (uint32_t)(piece / S::kNacc) & 1u, &s_abort, a.status, 63);
       g_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((piece % S::kNacc) * S::kAcc);
       // a shared tile's partial sums: [token][output] in the ring, which every

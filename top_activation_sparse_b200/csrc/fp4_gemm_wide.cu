@@ -138,6 +138,10 @@ __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, int* abor
   atomicExch(abort_flag, 1);
   return false;
 }
+// the same for a warp that goes on as a whole: its lanes agree
+__device__ __forceinline__ bool w_wait_warp(uint64_t* bar, uint32_t parity, int* abort_flag, DevStatus* st, uint32_t where) {
+  return __all_sync(0xffffffffu, w_wait(bar, parity, abort_flag, st, where));
+}
 
 struct WMaps {
   CUtensorMap xc, wc, xs, ws, y;
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
     for (int lt = 0; lt < mine; ++lt) {
       const int t = pair + lt * npairs;
       const int m0 = (t % mtiles) * 256 + (int)rank * kWRows, n0 = (t / mtiles) * 256;
-      const bool ok = w_wait(&s_tfull, (uint32_t)lt & 1u, &s_abort, a.status, 93);
+      const bool ok = w_wait_warp(&s_tfull, (uint32_t)lt & 1u, &s_abort, a.status, 93);
       w_after();
 #pragma unroll
       for (int half = 0; half < (BF16 ? 1 : 2); ++half) {

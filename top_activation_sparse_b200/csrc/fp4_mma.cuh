@@ -90,6 +90,21 @@ __device__ __forceinline__ bool g_wait(uint64_t* bar, uint32_t parity, int* abor
   atomicExch(abort_flag, 1);
   return false;
 }
+// the same for a warp that goes on as a whole (aligned instructions, votes, shuffles): its
+// lanes agree, where some have seen the barrier and others the flag or the limit.  (Polling
+// by one lane takes longer: 8 tokens of bf16 experts 357 instead of 347 us.)
+__device__ __forceinline__ bool g_wait_warp(uint64_t* bar, uint32_t parity, int* abort_flag, DevStatus* st, uint32_t where) {
+  return __all_sync(0xffffffffu, g_wait(bar, parity, abort_flag, st, where));
+}
+// for two barriers, half of the lanes each; what a lane has seen is ordered before what the
+// others do by the barrier of the warp
+__device__ __forceinline__ bool g_wait_warp(uint64_t* bar, uint32_t parity, uint64_t* bar1, uint32_t parity1, int* abort_flag,
+                                            DevStatus* st, uint32_t where) {
+  const bool odd = threadIdx.x & 1;
+  const bool ok = __all_sync(0xffffffffu, g_wait(odd ? bar1 : bar, odd ? parity1 : parity, abort_flag, st, where));
+  __syncwarp();
+  return ok;
+}
 
 inline PFN_cuTensorMapEncodeTiled_v12000 g_encode_fn() {
   static std::once_flag once;

@@ -167,9 +167,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
       for (int ks = 0; ks < nk; ++ks) {
         const int ab = piece & 1;
-        if (ks % kTChunk == 0 && piece >= 2 && !(ok = g_wait(&s.tempty[ab], (uint32_t)(piece / 2 - 1) & 1u, &s.abort, a.status, 101)))
+        if (ks % kTChunk == 0 && piece >= 2 && !(ok = g_wait_warp(&s.tempty[ab], (uint32_t)(piece / 2 - 1) & 1u, &s.abort, a.status, 101)))
           break;
-        if (!(ok = g_wait(&s.full[sl], ph, &s.abort, a.status, 102))) break;
+        if (!(ok = g_wait_warp(&s.full[sl], ph, &s.abort, a.status, 102))) break;
         g_after();
         const uint64_t st = d0 + (uint64_t)(sl * (f.stage_bytes / 16));
         const bool last = ks % kTChunk == kTChunk - 1 || ks == nk - 1;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (int t = 0; t < ROWS; ++t) v[0][t] = v[1][t] = 0.0f;
       for (int ks = 0; ks < nk; ks += kTChunk, ++piece) {
         const int ab = piece & 1;
-        if (!(ok = g_wait(&s.tfull[ab], (uint32_t)(piece / 2) & 1u, &s.abort, a.status, 103))) break;
+        if (!(ok = g_wait_warp(&s.tfull[ab], (uint32_t)(piece / 2) & 1u, &s.abort, a.status, 103))) break;
         g_after();
         const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * 128);
 #pragma unroll
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(kTDThreads, 1)
         for (int ks = 0; ks < d.steps; ++ks) {
           const int ab = piece & 1;
           if (ks % kTChunk == 0 && piece >= 2 &&
-              !(ok = g_wait(&s.tempty[ab], (uint32_t)(piece / 2 - 1) & 1u, &s.abort, a.status, 105)))
+              !(ok = g_wait_warp(&s.tempty[ab], (uint32_t)(piece / 2 - 1) & 1u, &s.abort, a.status, 105)))
             break;
-          if (!(ok = g_wait(&s.full[sl], ph, &s.abort, a.status, 106))) break;
+          if (!(ok = g_wait_warp(&s.full[sl], ph, &s.abort, a.status, 106))) break;
           g_after();
           const uint64_t ad = a0 + (uint64_t)(sl * (f.stage_bytes / 16)), bd = b0 + (uint64_t)(sl * (f.stage_bytes / 16));
           const bool last = ks % kTChunk == kTChunk - 1 || ks == d.steps - 1;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kTDThreads, 1)
         for (int i = 0; i < 128; ++i) y[i] = 0.0f;
         for (int ks = 0; ks < d.steps; ks += kTChunk, ++piece) {
           const int ab = piece & 1;
-          if (!(ok = g_wait(&s.tfull[ab], (uint32_t)(piece / 2) & 1u, &s.abort, a.status, 107))) break;
+          if (!(ok = g_wait_warp(&s.tfull[ab], (uint32_t)(piece / 2) & 1u, &s.abort, a.status, 107))) break;
           g_after();
           if (used) {
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * 256 + half);

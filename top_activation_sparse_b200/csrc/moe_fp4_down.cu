@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kDThreads, 1)
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
         const uint32_t id0 = d_idesc((uint32_t)min(256, d.cw)), id1 = d_idesc((uint32_t)max(16, d.cw - 256));
         for (int ks = 0, in = 0; ks < d.steps; ++ks) {         // in: this step's place in its sum
-          if (in == 0 && piece > 0 && !(ok = g_wait(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
+          if (in == 0 && piece > 0 && !(ok = g_wait_warp(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
           // (h has arrived too: the first expanding warp has waited for it)
-          if (!(ok = g_wait(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
+          if (!(ok = g_wait_warp(&s_bfull[b], ph, &s_abort, a.status, 93))) break;
           g_after();
           const uint64_t ad = a0 + (uint64_t)(b * (kDA / 16)), bd = b0 + (uint64_t)(b * (kDB / 16));
           const bool last = in == a.plan.sum_steps - 1 || ks == d.steps - 1;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
 #pragma unroll
           for (int i = 0; i + 1 < kDAhead; ++i) next[i][0] = next[i + 1][0], next[i][1] = next[i + 1][1];
           ahead(ks + kDAhead, next[kDAhead - 1]);
-          if (!(ok = g_wait(&s_cfull[csl], cph, &s_abort, a.status, 94))) break;
+          if (!(ok = g_wait_warp(&s_cfull[csl], cph, &s_empty[b], ph ^ 1u, &s_abort, a.status, 94))) break;
           uint32_t v[2][4];
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(kDThreads, 1)
                          : "=r"(v[i][0]), "=r"(v[i][1]), "=r"(v[i][2]), "=r"(v[i][3])
                          : "r"(scodes + (uint32_t)(csl * kDCodes) + src[i])
                          : "memory");
-          if (!(ok = g_wait(&s_empty[b], ph ^ 1u, &s_abort, a.status, 95))) break;
           // (rows behind the range are 0: what lies there may be anything)
           if (!there) v[0][0] = v[0][1] = v[0][2] = v[0][3] = v[1][0] = v[1][1] = v[1][2] = v[1][3] = 0u;
           // scales above 2 take a second factor (seldom: a warp at a time)
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_cempty[csl]);
           // (one wait per step for the warp that issues the MMAs)
-          if (w == 0 && !(ok = g_wait(&s_afull[b], ph, &s_abort, a.status, 92))) break;
+          if (w == 0 && !(ok = g_wait_warp(&s_afull[b], ph, &s_abort, a.status, 92))) break;
           if (lane == 0) mbar_arrive(&s_bfull[b]);
           if (++csl == kDCodeStages) csl = 0, cph ^= 1u;
           if ((b ^= 1) == 0) ph ^= 1u;
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
           in = 0;
           // ---- the sum's results, onto those of the range's sums before it: four
           // warps per quarter of the lanes, 32 columns in turn ----
-          if (!(ok = g_wait(&s_tfull, (uint32_t)piece++ & 1u, &s_abort, a.status, 96))) break;
+          if (!(ok = g_wait_warp(&s_tfull, (uint32_t)piece++ & 1u, &s_abort, a.status, 96))) break;
           g_after();
           if (t0 + q * kDTenth < d.cnt)
             for (int c = (w >> 2) * 32; c < d.cw; c += kDExpand / 4 * 32) {

@@ -164,13 +164,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const FUnit x = f_unit(tb, u, mtiles);
       const uint32_t id0 = f_idesc(0u, (uint32_t)x.nt * 8u), id1 = f_idesc(2u, (uint32_t)x.nt * 8u);
       const int ab = piece % f.nacc;
-      if (piece >= f.nacc && !(ok = g_wait(&s_tempty[ab], (uint32_t)(piece / f.nacc - 1) & 1u, &s_abort, a.status, 65))) break;
+      if (piece >= f.nacc && !(ok = g_wait_warp(&s_tempty[ab], (uint32_t)(piece / f.nacc - 1) & 1u, &s_abort, a.status, 65))) break;
       g_after();
       const uint32_t acc = tmem + (uint32_t)(ab * kMats * f.acc);
       for (int ks = 0; ks < nk; ++ks) {
         const int in = ks % kChunk;
-        if (in == 0 && !(ok = g_wait(&s_sffull[sfsl], sfph, &s_abort, a.status, 66))) break;
-        if (!(ok = g_wait(&s_full[sl], ph, &s_abort, a.status, 67))) break;
+        if (in == 0 && !(ok = g_wait_warp(&s_sffull[sfsl], sfph, &s_abort, a.status, 66))) break;
+        if (!(ok = g_wait_warp(&s_full[sl], ph, &s_abort, a.status, 67))) break;
         g_after();
         const uint64_t st = d0 + (uint64_t)(sl * (f.stage_bytes / 16));
         const uint64_t sfs = s0 + (uint64_t)(sfsl * (int)(kSfSlot / 16) + in * (2 * kSfTile / 16));
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const bool mine = j < a.d_ff;
       const size_t bi = (size_t)x.e * a.d_ff + (mine ? j : 0);
       const float b1 = a.b1 ? __ldg(a.b1 + bi) : 0.0f, b2 = a.b2 ? __ldg(a.b2 + bi) : 0.0f;
-      if (!g_wait(&s_tfull[ab], (uint32_t)(piece / f.nacc) & 1u, &s_abort, a.status, 68)) break;
+      if (!g_wait_warp(&s_tfull[ab], (uint32_t)(piece / f.nacc) & 1u, &s_abort, a.status, 68)) break;
       g_after();
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * kMats * f.acc);
       for (int c = 0; c < x.nt; ++c) {
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
           w[kMats][half * 4] = __vsubus4(v.x, less), w[kMats][half * 4 + 1] = __vsubus4(v.y, less);
           w[kMats][half * 4 + 2] = __vsubus4(v.z, less), w[kMats][half * 4 + 3] = __vsubus4(v.w, less);
         }
-        if (!(ok = g_wait(&s_sfempty[sfsl], sfph ^ 1u, &s_abort, a.status, 69))) break;
+        if (!(ok = g_wait_warp(&s_sfempty[sfsl], sfph ^ 1u, &s_abort, a.status, 69))) break;
         const uint32_t dst = sf0 + (uint32_t)sfsl * kSfSlot + at;
 #pragma unroll
         for (int o = 0; o <= kMats; ++o)

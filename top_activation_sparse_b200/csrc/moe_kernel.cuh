@@ -472,8 +472,11 @@ __device__ __forceinline__ void list_written(Smem& sm, RingAt& at, int i) {     
   if (threadIdx.x < kBatch) mbar_arrive(&sm.listed[i]);
   at.lists ^= 1u << i;
 }
-__device__ __forceinline__ void list_wait(Smem& sm, const RingAt& at, int i, DevStatus* st) {
-  ring_wait(&sm.listed[i], (at.lists >> i) & 1u, sm, st, 77);
+// the number of rows on the list (none, for the whole warp, after a wait that gave up: the
+// list may not have been written)
+__device__ __forceinline__ int list_wait(Smem& sm, const RingAt& at, int i, const int& n, DevStatus* st) {
+  const bool ok = ring_wait(&sm.listed[i], (at.lists >> i) & 1u, sm, st, 77);
+  return __all_sync(0xffffffffu, ok) ? *(volatile const int*)&n : 0;
 }
 __device__ __forceinline__ void list_taken(Smem& sm, RingAt& at, int i, int lane) {
   __syncwarp();
@@ -486,7 +489,8 @@ __device__ __forceinline__ void send_rows(const Ring& R, RingAt& at, Smem& sm, D
                                           const int* list, int j0, int n, int lane) {
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
-    const bool ok = ring_wait(&sm.empty[at.sl], at.ph ^ 1u, sm, st, 74);
+    // (after a give-up nothing more is sent: the last copies' places follow from their number)
+    const bool ok = ring_wait(&sm.empty[at.sl], at.ph ^ 1u, sm, st, 74) && !*(volatile int*)&sm.abort;
     if (__all_sync(0xffffffffu, ok)) {
       if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.sl], (uint32_t)(nr * (R.rb + R.sb)));
       __syncwarp();
@@ -807,14 +811,14 @@ __device__ void send_run(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, 
     }
     if (b >= 1 && b - 1 < nb) {
       const int s = (b - 1) & 1;
-      list_wait(sm, at, s, a.status);
-      send_rows(R, at, sm, a.status, M.w2, M.s2, sm.rows[s], 0, *(volatile int*)&sm.nrows[s], lane);
+      const int n = list_wait(sm, at, s, sm.nrows[s], a.status);
+      send_rows(R, at, sm, a.status, M.w2, M.s2, sm.rows[s], 0, n, lane);
       list_taken(sm, at, s, lane);
     }
     if (ONE && b >= 2) {
       const int s = b & 1;
-      list_wait(sm, at, 2 + s, a.status);
-      send_rows(R, at, sm, a.status, M.wd, M.sd, sm.drows[s], 0, *(volatile int*)&sm.ndrows[s], lane);
+      const int n = list_wait(sm, at, 2 + s, sm.ndrows[s], a.status);
+      send_rows(R, at, sm, a.status, M.wd, M.sd, sm.drows[s], 0, n, lane);
       list_taken(sm, at, 2 + s, lane);
     }
   }
@@ -1129,11 +1133,10 @@ __device__ void send_down(const MoeArgs& a, RingAt& at, Smem& sm, const DownItem
   const uint8_t* w = a.wd + (size_t)d.e * a.d_ff * rb + d.c0 * 2;
   for (int p = 0; p < passes; ++p)
     for (int jl = d.j0; jl < d.j1; jl += kListD) {
-      list_wait(sm, at, 2, a.status);
-      const int total = *(volatile int*)&sm.ndrows[0];
+      const int total = list_wait(sm, at, 2, sm.ndrows[0], a.status);
       for (int i0 = 0; i0 < total; i0 += kRowsStage) {
         const int nr = min(kRowsStage, total - i0);
-        const bool ok = ring_wait(&sm.dempty[at.sl], at.ph ^ 1u, sm, a.status, 80);
+        const bool ok = ring_wait(&sm.dempty[at.sl], at.ph ^ 1u, sm, a.status, 80) && !*(volatile int*)&sm.abort;
         if (__all_sync(0xffffffffu, ok)) {
           if (lane == 0) mbar_arrive_expect_tx(&sm.dfull[at.sl], (uint32_t)(nr * R.pb));
           __syncwarp();
