@@ -20,7 +20,7 @@
 // number: after sum_steps steps a sum leaves tensor memory, whatever the range's length
 // (64 tokens, 16 of 16 experts of 28672 x 1024 each, f32 results: y off by 4.7e-7 of itself with 16
 // steps, 8.7e-7 with 32, 7.6e-6 with a whole range of 14336 neurons).
-// 32 tokens, 2 of 8 experts of 11008 x 4096 each: 112 us, 1.7 TB/s of the 190 MB (4 us of it per sum).
+// 32 tokens, 2 of 8 experts of 11008 x 4096 each: 114 us, 1.7 TB/s of the 190 MB (3 us of it per sum).
 // Bound by the step's chain: the expansion (1200 cycles of issue) and the MMAs (900)
 // overlap, but each hand-over through a barrier takes 300 to 400 cycles while the
 // expansion's stores fill the queue that barriers go through.  Smaller steps with four
@@ -239,9 +239,11 @@ __global__ void __launch_bounds__(kDThreads, 1)
           to[i] = ks * kDK < left && (cb + 4 * i) * 32 < d.cw ? (uint32_t)__ldg(sc + (size_t)ks * kDK * sb + cb + 4 * i) : 0u;
       };
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
-        // results: 10 tokens per quarter of the lanes, three rows each
+        // results: 10 tokens per quarter of the lanes, three rows each; which lanes the two
+        // other rows of this lane's token are in
         const int q = warp & 3, tok = t0 + q * kDTenth + lane / 3;
-        const bool mine = lane < 30 && lane % 3 == 0 && tok < d.cnt;
+        const bool mine = lane < 30 && tok < d.cnt;
+        const int r3 = lane % 3, from1 = r3 == 0 ? lane + 2 : lane - 1, from2 = r3 == 2 ? lane - 2 : lane + 1;
         float* o = a.parts + ((size_t)d.s * a.T * a.top_k + d.slot0 + (mine ? tok : 0)) * a.d_model + d.c0;
 #pragma unroll
         for (int i = 0; i < kDAhead; ++i) ahead(i, next[i]);
@@ -282,32 +284,35 @@ __global__ void __launch_bounds__(kDThreads, 1)
           if (++in < a.plan.sum_steps && ks < d.steps - 1) continue;
           in = 0;
           // ---- the sum's results, onto those of the range's sums before it: four
-          // warps per quarter of the lanes, 32 columns in turn ----
+          // warps per quarter of the lanes, 24 columns in turn, of which each of a token's three
+          // lanes adds up 8 (two shuffles for three columns: a quarter's warps share one
+          // scheduler, whose shuffles take four cycles each) ----
           if (!(ok = g_wait_warp(&s_tfull, (uint32_t)piece++ & 1u, &s_abort, a.status, 96))) break;
           g_after();
           if (t0 + q * kDTenth < d.cnt)
-            for (int c = (w >> 2) * 32; c < d.cw; c += kDExpand / 4 * 32) {
-              uint32_t u[4][8];
+            for (int c = (w >> 2) * 24; c < d.cw; c += kDExpand / 4 * 24) {
+              uint32_t u[3][8];
 #pragma unroll
-              for (int g = 0; g < 4; ++g) g_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c + 8 * g), u[g]);
+              for (int g = 0; g < 3; ++g)
+                if (c + 8 * g < kDCols) g_ld8(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c + 8 * g), u[g]);
               g_ld_wait();
+              float y[8];
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float f = __uint_as_float(u[g][i]);
-                  y[i] = (__shfl_down_sync(0xffffffffu, f, 2) + __shfl_down_sync(0xffffffffu, f, 1)) + f;
-                }
-                if (mine) {
-                  float* to = o + c + 8 * g;
-                  if (ks >= a.plan.sum_steps) {
-                    d_add4(to, y[0], y[2], y[4], y[6]);
-                    d_add4(to + 4, y[1], y[3], y[5], y[7]);
-                  } else {
-                    __stcg(reinterpret_cast<float4*>(to), make_float4(y[0], y[2], y[4], y[6]));
-                    __stcg(reinterpret_cast<float4*>(to) + 1, make_float4(y[1], y[3], y[5], y[7]));
-                  }
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t own = r3 == 0 ? u[0][i] : r3 == 1 ? u[1][i] : u[2][i];
+                const uint32_t one = r3 == 0 ? u[1][i] : r3 == 1 ? u[2][i] : u[0][i];
+                const uint32_t two = r3 == 0 ? u[2][i] : r3 == 1 ? u[0][i] : u[1][i];
+                y[i] = (__uint_as_float(__shfl_sync(0xffffffffu, one, from1)) + __uint_as_float(__shfl_sync(0xffffffffu, two, from2))) +
+                       __uint_as_float(own);
+              }
+              if (mine && c + 8 * r3 < d.cw) {
+                float* to = o + c + 8 * r3;
+                if (ks >= a.plan.sum_steps) {
+                  d_add4(to, y[0], y[2], y[4], y[6]);
+                  d_add4(to + 4, y[1], y[3], y[5], y[7]);
+                } else {
+                  __stcg(reinterpret_cast<float4*>(to), make_float4(y[0], y[2], y[4], y[6]));
+                  __stcg(reinterpret_cast<float4*>(to) + 1, make_float4(y[1], y[3], y[5], y[7]));
                 }
               }
             }
