@@ -496,8 +496,8 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   not read.  Each expert weight is read once per 16 of its tokens (8 where
  *   d_model > 4096).  Where that is faster (small experts, several tokens per
  *   expert, f32 results, 4-bit weights of more than one token) the experts'
- *   rows are all read instead, on the tensor cores: same results, a closed neuron
- *   contributes 0.
+ *   rows are all read instead, on the tensor cores: with finite weights a closed
+ *   neuron contributes 0 there.
  *
  *   x         [T, d_model] bf16.
  *   w_router  [n_experts, d_model] bf16.
@@ -518,8 +518,12 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *   ws        qs_workspace_size(QS_OP_MOE_FFN, T, d_model, d_ff, top_k) bytes.
  *   h enters the down projection as the sum of three bf16 numbers, i.e. with
  *   all 24 bits.  Sums are taken in a fixed order: the same call gives the
- *   same bits.  Non-finite values propagate where they are computed with (a
- *   closed neuron's other weights are not).
+ *   same bits.  Values that are not finite: a token's (and with 4-bit weights
+ *   its infinities, as NaNs) reach that token's results only.  A gate or up
+ *   weight's (4-bit: a scale of 255) reach the tokens for which they are
+ *   computed with; a first factor of 0 makes h 0 whatever the second is.  A down
+ *   row's may reach every token of its expert, open neuron or not: whether a row
+ *   is skipped for an h of 0 depends on the kernels a call takes.
  *   d_model must be a multiple of 32, d_ff of 8.
  *   Errors: INVALID_ARG (also: some but not all scales given, top_k >
  *   n_experts), ALIGNMENT, WORKSPACE, UNSUPPORTED (d_model above

@@ -927,7 +927,9 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         if (j[k] >= 0 && c < u.nt) {
           float v = dot_sum(sm, P, tid + k * kMThreads) * back + bias[k];
           if (a.drelu) v = relu_nan(v);
-          h = sm.first[s][(j[k] - jb) * kTok + c] * v;
+          // (a closed first factor is 0 whatever the other is: another token has opened the neuron)
+          const float f = sm.first[s][(j[k] - jb) * kTok + c];
+          h = f == 0.0f ? 0.0f : f * v;
           if constexpr (!ONE) __stcg(a.h + (size_t)(u.slot0 + c) * a.d_ff + j[k], h);
         }
         if constexpr (!ONE) {
