@@ -76,3 +76,25 @@ def test_projection_and_ffn(T):
     both([lambda x=x: qs.qs_sparse_linear(x, wt, 700) for x in xs], near)
     up, gate, down = (rnd(4 + i, *s, std=0.03).to(torch.bfloat16) for i, s in enumerate(((d, dff), (d, dff), (dff, d))))
     both([lambda x=x: qs.qs_sparse_ffn(x, up, gate, down, "relu2_glu", 700, 1400).y for x in xs], near)
+
+
+def test_a_dropped_workspace_is_not_handed_out_while_its_call_runs():
+    need_gpu()
+    dm, dff, E, T = 256, 512, 8, 6
+    a = {"x": rnd(1, T, dm).to(torch.bfloat16), "w_router": rnd(2, E, dm, std=0.1).to(torch.bfloat16)}
+    a.update({"w_" + n: rnd(3 + i, E, dff, dm, std=0.06).to(torch.bfloat16) for i, n in enumerate(("gate", "up", "down"))})
+    call = lambda **k: qs.qs_moe_ffn(top_k=2, act="relu2_glu", y_dtype=torch.float32, **k, **a).y  # noqa: E731
+    want = call()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        ws = qs.new_workspace(qs.QS_OP_MOE_FFN, T, dm, dff, 2, DEV)
+        size = ws.numel()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)
+        y = call(ws=ws, stream=s)
+        del ws
+        other = torch.full((size,), 0x7f, dtype=torch.uint8, device=DEV)     # the memory, if it were free
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del other

@@ -63,3 +63,38 @@ def test_a_captured_call_has_one_of_its_own(current, op):
     assert len({w.data_ptr() for w in (kept, a, b)}) == 3
     assert workspace(op) is kept
     assert int(a[:256 + 65536].count_nonzero()) == 0
+
+
+class _Anything:
+    """A library whose functions take anything and succeed."""
+
+    def __getattr__(self, name):
+        return lambda *args: 0
+
+
+def test_a_callers_tensors_are_held_for_the_stream_of_the_call(current, monkeypatch):
+    """Every tensor that the enqueued kernels use, the workspace too: a caller who drops it
+    after the call must not get its memory again before that stream is done."""
+    held = []
+    monkeypatch.setattr(qs, "_call_context", lambda dev, stream, *t: held.extend(t) or contextlib.nullcontext())
+    monkeypatch.setattr(qs, "_need_cuda", lambda *t: torch.device("cpu"))
+    monkeypatch.setattr(qs, "lib", lambda: _Anything())
+    monkeypatch.setattr(qs, "qs_fp4_scale_bytes", lambda *a: 512)
+    z = lambda *s, dtype=torch.uint8: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    bf = torch.bfloat16
+    f = torch.float32
+
+    def check(call, given):
+        held.clear()
+        call(stream=3, **given)
+        assert {n for n, t in given.items() if isinstance(t, torch.Tensor) and not any(t is h for h in held)} == set()
+
+    check(lambda **k: qs.qs_fp4_quantize(**k),
+          dict(x=z(2, 64, dtype=bf), tensor_scale=z(1, dtype=f), codes=z(2, 32), scales=z(512), values=z(2, 64, dtype=bf)))
+    check(lambda **k: qs.qs_fp4_sparse_linear(k=8, **k),
+          dict(x=z(2, 64, dtype=bf), w_codes=z(8, 32), w_scales=z(512), x_scale=z(1, dtype=f), w_scale=z(1, dtype=f),
+               y=z(2, 8, dtype=bf), ws=z(1024)))
+    check(lambda **k: qs.qs_moe_ffn(top_k=1, act="drelu", **k),
+          dict(x=z(2, 32, dtype=bf), w_router=z(3, 32, dtype=bf), w_gate=z(3, 8, 16), w_up=z(3, 8, 16), w_down=z(3, 8, 16),
+               s_gate=z(3, 8, 1), s_up=z(3, 8, 1), s_down=z(3, 8, 1), b_gate=z(3, 8, dtype=f), b_up=z(3, 8, dtype=f),
+               y=z(2, 32, dtype=bf), experts=z(2, 1, dtype=torch.int32), weights=z(2, 1, dtype=f), ws=z(1024)))

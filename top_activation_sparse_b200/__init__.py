@@ -667,7 +667,7 @@ def qs_fp4_sparse_linear(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch
         raise ValueError("w_codes must be [d_out, d_in/2] uint8")
     if w_scales.dtype != torch.uint8 or w_scales.numel() != qs_fp4_scale_bytes(d_out, d_in, fmt, QS_FP4_SCALES_TILED):
         raise ValueError("w_scales must be the tiled uint8 scales of W [d_out, d_in]")
-    with _call_context(dev, stream, x, w_codes, w_scales, x_scale, w_scale, y):
+    with _call_context(dev, stream, x, w_codes, w_scales, x_scale, w_scale, y, ws):
         y = _out_like(True if y is None else y, (T, d_out), (y_dtype or x.dtype) if y is None else y.dtype, x)
         ws = _stream_workspace(ws, QS_OP_FP4_SPARSE_LINEAR, T, d_in, d_out, k, dev)
         _check("qs_fp4_sparse_linear", lib().qs_fp4_sparse_linear(
@@ -709,7 +709,7 @@ def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, 
             raise ValueError("biases must be [E, d_ff] float32")
     act_code = _ACTS[act] if isinstance(act, str) else int(act)
     with _call_context(dev, stream, x, w_router, w_gate, w_up, w_down, s_gate, s_up, s_down, b_gate, b_up, y,
-                       experts, weights):
+                       experts, weights, ws):
         y = _out_like(True if y is None else y, (T, d_model), (y_dtype or x.dtype) if y is None else y.dtype, x)
         experts = _out_like(experts, (T, top_k), torch.int32, x)
         weights = _out_like(weights, (T, top_k), torch.float32, x)
