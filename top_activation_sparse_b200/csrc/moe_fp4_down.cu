@@ -62,8 +62,10 @@ __device__ __forceinline__ void d_mma(uint32_t d, uint64_t ad, uint64_t bd, uint
       : "memory");
 }
 
-// nibbles c and c + 4 of a word as a pair of bf16 (see moe_kernel.cuh: the
-// magnitude read as value * 2^-126, one product for 2^126 and the scale)
+// Nibbles c and c + 4 of a word as a pair of bf16.  A code's two exponent bits (bias 1) and
+// its mantissa bit, moved to the two lowest exponent bits and the highest mantissa bit of a bf16
+// number (bias 127), read as the code's value times 2^-126, subnormal codes too; one product
+// brings in 2^126 and the scale.
 template <int C, bool BIG>
 __device__ __forceinline__ uint32_t d_pair(uint32_t p, uint32_t lo, uint32_t hi) {
   const uint32_t m = C == 0 ? p << 6 : C == 1 ? p << 2 : C == 2 ? p >> 2 : p >> 6;

@@ -47,7 +47,7 @@
 // error below 2^-24).  4-bit weights are expanded in registers, exactly.
 //
 // 1 token, 2 of 8 dReLU experts of 14336 x 4096: bf16 76 us (46 at the memory's rate),
-// 4-bit 66 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
+// 4-bit 64 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
 // about 7 us of routing, 4 for the first rows, 8 for the last sums).  2 tokens, 8 experts of
 // 11008 x 4096, bf16: 157 us.
 #pragma once
@@ -132,12 +132,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // ---- queue and waits ---------------------------------------------------------
@@ -556,21 +550,19 @@ __device__ __forceinline__ void load_x(const MoeArgs& a, const Smem& sm, const S
 // instructions of e4m3, into which codes go by two shifts, were three times slower
 // than those of float16.)  x, times the power of two that brings its token's
 // largest into [2^14, 2^15), is float16, exact down to 2^-39 of that largest.
-__device__ __forceinline__ int x_pitch(int d) { return (d * 2 + 63) / 128 * 128 + 64; }   // 64 mod 128
-__device__ __forceinline__ void stage_x(const MoeArgs& a, Smem& sm, int nt) {
-  const int per = a.d_model / 8, pitch = x_pitch(a.d_model);
-  for (int i = threadIdx.x; i < nt * per; i += kMThreads) {
-    const int n = i / per, k = (i - n * per) * 8, t = sm.tok[n];
+__device__ __forceinline__ void stage_x(const MoeArgs& a, Smem& sm) {
+  const int t = sm.tok[0];
+  const float up = sm.xup[t];
+  for (int k = threadIdx.x * 8; k < a.d_model; k += kMThreads * 8) {
     const uint4 v = ld_x(a.x + (size_t)t * a.d_model + k);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    const float up = sm.xup[t];
     uint32_t r[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const __half2 h = __floats2half2_rn(bf16lo(u[c]) * up, bf16hi(u[c]) * up);
       r[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(sm.tail + n * pitch + k * 2) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(sm.tail + k * 2) = make_uint4(r[0], r[1], r[2], r[3]);
   }
 }
 
@@ -638,15 +630,15 @@ __device__ __forceinline__ void dot_rows_bf16(const MoeArgs& a, const Ring& R, R
   }
 }
 
-// 4-bit weights: the neurons are the matrix's 16 rows, the tokens its 8 columns;
-// a unit is one block of 32: its sum times its scale, four blocks at a time (a
+// 4-bit weights, one token: the neurons are the matrix's 16 rows, the token the first of its
+// 8 columns; a unit is one block of 32: its sum times its scale, four blocks at a time (a
 // block's second product waits for its first).
-__device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P, int nt,
+__device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, RingAt& at, Smem& sm, const Split& P,
                                              const uint8_t* sc, const int* list, int j0, int n, int lane) {
   const int g = lane >> 2, q = lane & 3, first = P.part * P.per, sb = a.d_model / 32;
   float* red = sm.red + (size_t)P.part * kBatch * 8;
-  const unsigned char* xs = sm.tail + (g < nt ? g : 0) * x_pitch(a.d_model) + first * 64 + q * 16;
-  const bool has = g < nt, whole = R.sb && P.per == 16;     // 16 scales of a row in one load
+  const unsigned char* xs = sm.tail + first * 64 + q * 16;
+  const bool whole = R.sb && P.per == 16;             // 16 scales of a row in one load
   int tile = 0;
   for (int i0 = 0; i0 < n; i0 += R.rps) {
     const int nr = min(R.rps, n - i0);
@@ -667,7 +659,7 @@ __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, Ri
         pa = sc + (size_t)(list ? list[i0 + ra] : j0 + i0 + ra) * sb + first;
         pb = sc + (size_t)(list ? list[i0 + rc] : j0 + i0 + rc) * sb + first;
       }
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float acc[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int h = 0; h < 16; h += 4) {
         if (h >= P.n) break;
@@ -690,7 +682,7 @@ __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, Ri
           const int k = h + i < P.n ? h + i : h;
           va[i] = *reinterpret_cast<const uint32_t*>(wa + k * 16);
           vb[i] = *reinterpret_cast<const uint32_t*>(wb + k * 16);
-          x[i] = has && h + i < P.n ? *reinterpret_cast<const uint4*>(xs + k * 64) : make_uint4(0, 0, 0, 0);
+          x[i] = g == 0 && h + i < P.n ? *reinterpret_cast<const uint4*>(xs + k * 64) : make_uint4(0, 0, 0, 0);
         }
         float d[4][4];
         uint32_t ha[4][4], hb[4][4];
@@ -707,17 +699,14 @@ __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, Ri
         for (int i = 0; i < 4; ++i) {
           // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
           // of its codes, all 0)
-          const float f0 = __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), f1 = __uint_as_float(((sbw >> (8 * i)) & 0xffu) << 23);
-          acc[0] = fmaf(d[i][0], f0, acc[0]);
-          acc[1] = fmaf(d[i][1], f0, acc[1]);
-          acc[2] = fmaf(d[i][2], f1, acc[2]);
-          acc[3] = fmaf(d[i][3], f1, acc[3]);
+          acc[0] = fmaf(d[i][0], __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), acc[0]);
+          acc[1] = fmaf(d[i][2], __uint_as_float(((sbw >> (8 * i)) & 0xffu) << 23), acc[1]);
         }
       }
-      // rows g and g + 8 of the tile, tokens 2q and 2q + 1
-      float* o = red + (size_t)(i0 + t0 + g) * 8 + 2 * q;
-      if (t0 + g < nr) *reinterpret_cast<float2*>(o) = make_float2(acc[0], acc[1]);
-      if (t0 + 8 + g < nr) *reinterpret_cast<float2*>(o + 64) = make_float2(acc[2], acc[3]);
+      // rows g and g + 8 of the tile
+      float* o = red + (size_t)(i0 + t0 + g) * 8;
+      if (q == 0 && t0 + g < nr) o[0] = acc[0];
+      if (q == 0 && t0 + 8 + g < nr) o[64] = acc[1];
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[at.sl]);
@@ -842,7 +831,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
   const Split P(a.d_model, KU, warp);
   XFrag<FP4 ? 1 : KU, NG> x;
   if constexpr (FP4) {
-    stage_x(a, sm, u.nt);
+    stage_x(a, sm);
     csync();
   } else {
     load_x<KU, NG>(a, sm, P, x, lane);
@@ -874,7 +863,7 @@ __device__ __forceinline__ void compute_run(const MoeArgs& a, const Ring& R, Rin
         j[k] = r < n ? (list ? list[r] : jb + r) : -1;
         bias[k] = bs && j[k] >= 0 ? __ldg(bs + j[k]) : 0.0f;
       }
-      if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, u.nt, second ? M.s2 : M.s1, list, jb, n, lane);
+      if constexpr (FP4) dot_rows_fp4(a, R, at, sm, P, second ? M.s2 : M.s1, list, jb, n, lane);
       else dot_rows_bf16<KU, NG>(a, R, at, sm, P, x, n, lane);
       csync();
       if (!second) {
@@ -1578,9 +1567,9 @@ MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y
   p.router_items = p.local ? 0 : (n_experts + 15) / 16 * ((T + 7) / 8) + p.x_items;
   p.hidden_items = p.grid;
   // tokens per pass: two groups of 8 where x of both fits the registers; 4-bit
-  // weights: one token, x in shared memory
+  // weights: the one token, x in shared memory
   p.hidden_tokens = fp4 ? 1 : d_model <= 4096 ? 16 : 8;
-  p.x_bytes = fp4 ? (d_model * 2 + 63) / 128 * 128 + 128 : 0;
+  p.x_bytes = fp4 ? (d_model * 2 + 127) / 128 * 128 : 0;
   // the ring: stages of about 36 KB, whole tiles of 8 or 16 rows where rows are
   // short
   p.row_bytes = fp4 ? d_model / 2 : d_model * 2;
