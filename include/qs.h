@@ -506,8 +506,7 @@ qs_status qs_fp4_sparse_linear(const void* x, int dtype, int T, int d_in, int d_
  *             s_gate, s_up, s_down all NULL: bf16.  All given: 4-bit codes
  *             [n_experts, d_ff, d_model/2] and scales [n_experts, d_ff,
  *             d_model/32] (qs_fp4_quantize of these matrices, QS_FP4_MX,
- *             QS_FP4_SCALES_ROWS); they enter as the numbers they stand for
- *             (one token: a scale of 2^-127, the least there is, counts as 0).
+ *             QS_FP4_SCALES_ROWS); they enter as the numbers they stand for.
  *             x is not quantised: it enters with 24 bits below the largest of
  *             its block of 32 (one token: float16 with all of bf16's bits, down
  *             to 2^-39 of the token's largest).

@@ -63,3 +63,27 @@ def test_a_down_row_that_is_not_finite_stays_in_its_expert(dff, fp4):
         check(qs.MoeResult(r.y, r.experts, r.weights), want, dm, torch.bfloat16)
     else:
         assert not finite.any()
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_the_least_scale(T):
+    """Blocks with the scale 2^-127 in the first and second factors, of inputs large enough to see them:
+    products of 2^-127 and 2^126, exact in float32 but for the sums."""
+    need_gpu()
+    dm, dff, E = 256, 128, 2
+    a, _ = make(43, T, dm, dff, E, "relu2_glu", True)
+    a["x"] = (a["x"].float().clamp(-3, 3) * 2.0 ** 126).to(torch.bfloat16)
+    a["w_router"][:] = 0.0
+    vals = {}
+    for n in ("gate", "up", "down"):
+        if n != "down":
+            a["s_" + n][:] = 0
+        lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], device=DEV, dtype=torch.float64)
+        c = a["w_" + n].long()
+        vals[n] = torch.stack((lut[c & 15], lut[c >> 4]), -1).flatten(-2) * torch.exp2(
+            a["s_" + n].double() - 127).repeat_interleave(32, -1)
+    r = qs.qs_moe_ffn(top_k=1, act="relu2_glu", y_dtype=torch.float32, experts=True, weights=True, **a)
+    x, d = a["x"].double(), {n: v[0] for n, v in vals.items()}          # equal logits: the first expert
+    want = (torch.relu(x @ d["up"].t()) ** 2 * (x @ d["gate"].t())) @ d["down"]
+    assert bool((want != 0).any(1).all())
+    check(r, dict(y=want.cpu().numpy(), experts=[[0]] * T, weights=[[1.0]] * T), dm, torch.float32)

@@ -47,7 +47,7 @@
 // error below 2^-24).  4-bit weights are expanded in registers, exactly.
 //
 // 1 token, 2 of 8 dReLU experts of 14336 x 4096: bf16 76 us (46 at the memory's rate),
-// 4-bit 64 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
+// 4-bit 65 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
 // about 7 us of routing, 4 for the first rows, 8 for the last sums).  2 tokens, 8 experts of
 // 11008 x 4096, bf16: 157 us.
 #pragma once
@@ -697,10 +697,10 @@ __device__ __forceinline__ void dot_rows_fp4(const MoeArgs& a, const Ring& R, Ri
         for (int i = 0; i < 4; ++i) mma_f16(d[i], ha[i][2], hb[i][2], ha[i][3], hb[i][3], x[i].z, x[i].w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // (a scale of 2^-127 counts as 0; 255 as an infinity, which makes a NaN
-          // of its codes, all 0)
-          acc[0] = fmaf(d[i][0], __uint_as_float(((sa >> (8 * i)) & 0xffu) << 23), acc[0]);
-          acc[1] = fmaf(d[i][2], __uint_as_float(((sbw >> (8 * i)) & 0xffu) << 23), acc[1]);
+          // (the least scale, 2^-127, is the subnormal number below them; 255 counts as an
+          // infinity, which makes a NaN of its codes, all 0)
+          acc[0] = fmaf(d[i][0], __uint_as_float(max(((sa >> (8 * i)) & 0xffu) << 23, 0x400000u)), acc[0]);
+          acc[1] = fmaf(d[i][2], __uint_as_float(max(((sbw >> (8 * i)) & 0xffu) << 23, 0x400000u)), acc[1]);
         }
       }
       // rows g and g + 8 of the tile
