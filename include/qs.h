@@ -535,6 +535,11 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
                      const float* b_gate, const float* b_up, void* y, int y_dtype, int32_t* experts,
                      float* weights, void* ws, size_t ws_bytes, void* stream);
 
+/* Kernels that a qs_moe_ffn call with these sizes launches (fp4: scales given): per 64
+ * tokens 1, or 4 where all rows of the experts used are read on the tensor cores; 0 if the
+ * sizes are invalid.  Host-only: nothing is enqueued. */
+int qs_moe_ffn_kernels(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4, int y_dtype);
+
 /* Bytes of workspace `op` needs for these sizes (0 if the sizes are invalid).
  * Arguments: QS_OP_TOPK_MASK (T, d, 0, k); QS_OP_SPARSE_LINEAR (T, d_in, d_out,
  * k); QS_OP_SPARSE_FFN, QS_OP_SPARSE_FFN_GATE_FIRST and QS_OP_QUANT_SPARSE_FFN (T,

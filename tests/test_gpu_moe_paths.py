@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import top_activation_sparse_b200 as qs
-from gpu_common import need_gpu
+from gpu_common import check_status, need_gpu
 from test_gpu_moe import DEV, check, make, reference
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +87,153 @@ def test_the_least_scale(T):
     want = (torch.relu(x @ d["up"].t()) ** 2 * (x @ d["gate"].t())) @ d["down"]
     assert bool((want != 0).any(1).all())
     check(r, dict(y=want.cpu().numpy(), experts=[[0]] * T, weights=[[1.0]] * T), dm, torch.float32)
+
+
+# ---- the queue kernel ----------------------------------------------------------------------
+# several tokens: (T, d_model, d_ff, experts, top_k); the second is routed through the workspace
+# (a router that the CTAs do not each evaluate), the third has more than 8 tokens
+SEVERAL = [(3, 4096, 1832, 8, 2), (3, 4096, 3664, 20, 1), (20, 2048, 1368, 16, 1)]
+bf = torch.bfloat16
+
+
+def one_kernel(T, dm, dff, E, top_k, fp4=False, y_dtype=bf):
+    """These sizes take the queue kernel."""
+    assert qs.qs_moe_ffn_kernels(T, dm, dff, E, top_k, fp4, y_dtype) == 1
+
+
+def queue(a, top_k, act, **kw):
+    return qs.qs_moe_ffn(top_k=top_k, act=act, experts=True, weights=True, **kw, **a)
+
+
+@pytest.mark.parametrize("size", SEVERAL)
+@pytest.mark.parametrize("act,bias", [("drelu", -0.8), ("drelu", None), ("drelu", 30.0), ("relu2_glu", None)])
+def test_queue_kernel(size, act, bias):
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(50 + T + E, T, dm, dff, E, act, False, bias)
+    check(queue(a, top_k, act), reference(a, vals, top_k, act), dm, bf)
+
+
+@pytest.mark.parametrize("size", SEVERAL)
+def test_queue_kernel_leaves_its_workspace_ready(size):
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(51, T, dm, dff, E, "relu2_glu", False)
+    ws = qs.new_workspace(qs.QS_OP_MOE_FFN, T, dm, dff, top_k, DEV)
+    first = queue(a, top_k, "relu2_glu", ws=ws)
+    for _ in range(6):
+        r = queue(a, top_k, "relu2_glu", ws=ws)
+        assert torch.equal(r.y, first.y) and torch.equal(r.experts, first.experts)
+    check_status(ws)
+    assert int(ws[256:256 + 65536].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("size", SEVERAL)
+def test_queue_kernel_twice_at_once(size):
+    """Two calls that share the SMs, each with its stream's own workspace."""
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(52, T, dm, dff, E, "drelu", False)
+    want = queue(a, top_k, "drelu").y
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [queue(a, top_k, "drelu", stream=s).y for _ in range(20) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, g) for g in got)
+
+
+@pytest.mark.parametrize("size", SEVERAL)
+def test_queue_kernel_captured_and_replayed(size):
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(53, T, dm, dff, E, "drelu", False)
+    eager = queue(a, top_k, "drelu").y
+    x = a.pop("x")
+    static = torch.zeros_like(x)
+    graphs = []
+    for _ in range(2):                       # two graphs, each with its own workspace
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = queue({**a, "x": static}, top_k, "drelu").y
+        graphs.append((graph, y))
+    static.copy_(x)
+    for _ in range(3):
+        for graph, y in graphs:
+            y.zero_()
+            graph.replay()
+            assert torch.equal(y, eager)
+    assert torch.equal(queue({**a, "x": x}, top_k, "drelu").y, eager)
+
+
+@pytest.mark.parametrize("size", SEVERAL)
+def test_queue_kernel_a_token_that_is_not_finite_stays_alone(size):
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(54, T, dm, dff, E, "drelu", False)
+    want = reference(a, vals, top_k, "drelu")
+    a["x"][1, 5] = float("nan")
+    r = queue(a, top_k, "drelu")
+    assert torch.isnan(r.y[1]).all()
+    keep = [t for t in range(T) if t != 1]
+    check(qs.MoeResult(r.y[keep], r.experts[keep], r.weights[keep]), {k: v[keep] for k, v in want.items()}, dm, bf)
+
+
+def test_queue_kernel_closed_batches():
+    """No neuron is open over many batches in a row (empty lists), then one is, then its second
+    factor is 0 as well; rows of y behind the last are left as they were."""
+    need_gpu()
+    T, dm, dff, E = 3, 512, 40000, 4
+    one_kernel(T, dm, dff, E, 1)
+    a, vals = make(55, T, dm, dff, E, "drelu", False, bias=-100.0)
+    buf = torch.full((T + 2, dm), 7.0, device=DEV, dtype=bf)
+    r = queue(a, 1, "drelu", y=buf[:T])
+    assert torch.count_nonzero(r.y).item() == 0 and bool((buf[T:] == 7.0).all())
+    a["b_gate"][:, 39990] = 50.0                       # open, but the second factor is closed
+    assert torch.count_nonzero(queue(a, 1, "drelu").y).item() == 0
+    a["b_gate"][:, 17] = a["b_up"][:, 17] = 50.0
+    a["b_gate"][:, 20011] = a["b_up"][:, 20011] = 50.0
+    check(queue(a, 1, "drelu"), reference(a, vals, 1, "drelu"), dm, bf)
+
+
+# one token: a router of more than 64 experts, or of more than 128 KB, is not evaluated by
+# each CTA: queue items, whose result is handed over through the workspace
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("act", ["drelu", "relu2_glu"])
+@pytest.mark.parametrize("dm,dff,E,top_k", [(4096, 264, 32, 2), (256, 520, 100, 4), (96, 72, 256, 16), (1056, 136, 65, 1)])
+def test_one_token_and_a_large_router(dm, dff, E, top_k, act, fp4):
+    need_gpu()
+    y = torch.float32
+    one_kernel(1, dm, dff, E, top_k, fp4, y)
+    a, vals = make(56 + E, 1, dm, dff, E, act, fp4)
+    ws = qs.new_workspace(qs.QS_OP_MOE_FFN, 1, dm, dff, top_k, DEV)
+    first = queue(a, top_k, act, y_dtype=y, ws=ws)
+    check(first, reference(a, vals, top_k, act), dm, y)
+    for _ in range(4):
+        assert torch.equal(queue(a, top_k, act, y_dtype=y, ws=ws).y, first.y)
+    check_status(ws)
+    assert int(ws[256:256 + 65536].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_one_token_captured_on_two_streams(fp4):
+    need_gpu()
+    dm, dff, E = 4096, 264, 32
+    one_kernel(1, dm, dff, E, 2, fp4)
+    a, vals = make(57, 1, dm, dff, E, "drelu", fp4)
+    want = queue(a, 2, "drelu").y
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = queue(a, 2, "drelu").y
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):                      # beside the graph, on another stream
+        y.zero_()
+        graph.replay()
+        got = queue(a, 2, "drelu", stream=s).y
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(got, want)

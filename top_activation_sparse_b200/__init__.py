@@ -98,6 +98,7 @@ _SIGNATURES = {
                                   _vp, _sz, _vp]),
     "qs_moe_ffn": (_i, [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                         _i, _vp, _vp, _vp, _sz, _vp]),
+    "qs_moe_ffn_kernels": (_i, [_i, _i, _i, _i, _i, _i, _i]),
     "qs_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "qs_workspace_init": (_i, [_vp, _sz, _vp]),
     "qs_device_status": (_i, [_vp, _vp]),
@@ -720,6 +721,14 @@ def qs_moe_ffn(x, w_router, w_gate, w_up, w_down, top_k: int, act, s_gate=None, 
             _ptr(b_up), y.data_ptr(), _dtype_code(y), _ptr(experts), _ptr(weights), ws.data_ptr(),
             ws.numel(), _current_stream_ptr(dev)))
     return MoeResult(y, experts, weights)
+
+
+def qs_moe_ffn_kernels(T: int, d_model: int, d_ff: int, n_experts: int, top_k: int, fp4: bool = False,
+                       y_dtype=torch.bfloat16) -> int:
+    """Kernels that a qs_moe_ffn call with these sizes launches: 1 or 4 per 64
+    tokens (0: invalid sizes)."""
+    return int(lib().qs_moe_ffn_kernels(T, d_model, d_ff, n_experts, top_k, 1 if fp4 else 0,
+                                        QS_BF16 if y_dtype == torch.bfloat16 else QS_F32))
 
 
 def qs_ternary_pack(w: torch.Tensor, eps: float = 1e-5, wt_packed=None, alpha_out=None, ws=None,

@@ -986,6 +986,17 @@ qs_status qs_moe_ffn(const void* x, int T, int d_model, int d_ff, int n_experts,
   return QS_OK;
 }
 
+int qs_moe_ffn_kernels(int T, int d_model, int d_ff, int n_experts, int top_k, int fp4, int y_dtype) {
+  if (n_experts < top_k || n_experts > kMoeMaxE || !valid_dtype(y_dtype) ||
+      qs_workspace_size(QS_OP_MOE_FFN, T, d_model, d_ff, top_k) == 0)
+    return 0;
+  int n = 0;
+  for (int t0 = 0; t0 < T; t0 += kMoeMaxT)
+    n += (fp4 ? plan_moe_fp4 : plan_moe_bf16)(T - t0 < kMoeMaxT ? T - t0 : kMoeMaxT, d_model, d_ff, n_experts, top_k,
+                                              y_dtype == QS_BF16).tensor ? 4 : 1;
+  return n;
+}
+
 qs_status qs_sparse_linear_backward(const void* x, int dtype, int T, int d_in, int d_out, int k,
                                     int block, const void* wt, const void* grad_y, float* grad_x,
                                     float* grad_wt, void* ws, size_t ws_bytes, void* stream) {
