@@ -22,12 +22,9 @@
 // operands alone); the copies of the scales to tensor memory, which do not run beside
 // the products (20 us; asking for them a step ahead: 95 us), the products (11 us) and the
 // last tiles' stores add to it.  Every wait is bounded.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
-#include "fp4.cuh"
+#include "fp4_mma.cuh"
 
 namespace qs {
 namespace {
@@ -55,15 +52,6 @@ template <bool NV>
 __device__ constexpr uint32_t w_idesc(uint32_t sf_id) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | ((NV ? 0u : 1u) << 23) |
          ((uint32_t)(256 >> 4) << 24) | (sf_id << 29);
-}
-__device__ __forceinline__ uint64_t w_desc(uint32_t saddr, uint32_t sbo, uint32_t layout) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)layout << 61;
-  return d;
 }
 template <bool NV>
 __device__ __forceinline__ void w_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -124,25 +112,9 @@ __device__ __forceinline__ void w_ld32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void w_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void w_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void w_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity, int* abort_flag, DevStatus* st, uint32_t where) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 15u) == 15u && *(volatile int*)abort_flag) return false;
-  }
-  dev_fail(st, DEV_TIMEOUT, where, 0u);
-  atomicExch(abort_flag, 1);
-  return false;
-}
-// the same for a warp that goes on as a whole: its lanes agree
-__device__ __forceinline__ bool w_wait_warp(uint64_t* bar, uint32_t parity, int* abort_flag, DevStatus* st, uint32_t where) {
-  return __all_sync(0xffffffffu, w_wait(bar, parity, abort_flag, st, where));
-}
-
 struct WMaps {
   CUtensorMap xc, wc, xs, ws, y;
 };
@@ -185,10 +157,10 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
-  w_before();
+  g_before();
   __syncthreads();
   w_cluster_sync();                                // the peer's barriers exist before any signal
-  w_after();
+  g_after();
   const uint32_t tmem = s_tmem;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -225,7 +197,7 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
       int it = head;
       for (; it < n; ++it) {
         const int s = it % kWStages;
-        if (!w_wait(&s_empty[s], (uint32_t)((it / kWStages) - 1) & 1u, &s_abort, a.status, 90)) break;
+        if (!g_wait(&s_empty[s], (uint32_t)((it / kWStages) - 1) & 1u, &s_abort, a.status, 90)) break;
         copy_w(it, s);
         copy_x(it, s);
       }
@@ -242,23 +214,23 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
       int it = 0;
       bool issued = false, ok = true;
       for (int lt = 0; lt < mine && ok; ++lt) {
-        if (lt >= 1 && !w_wait(&s_tempty, (uint32_t)(lt - 1) & 1u, &s_abort, a.status, 91)) break;
-        w_after();
+        if (lt >= 1 && !g_wait(&s_tempty, (uint32_t)(lt - 1) & 1u, &s_abort, a.status, 91)) break;
+        g_after();
         for (int kb = 0; kb < nk; ++kb, ++it) {
           const int s = it % kWStages;
-          if (!w_wait(&s_full[s], (uint32_t)(it / kWStages) & 1u, &s_abort, a.status, 92)) {
+          if (!g_wait(&s_full[s], (uint32_t)(it / kWStages) & 1u, &s_abort, a.status, 92)) {
             ok = false;
             break;
           }
-          w_after();
+          g_after();
           const uint32_t st = base + (uint32_t)(s * S::kStage);
           const uint32_t sfa = tmem + 256u + (uint32_t)(s * S::kSfCols), sfb = sfa + S::kAtoms * 4;
 #pragma unroll
           for (int t = 0; t < S::kAtoms; ++t) {
-            w_cp_sf(sfa + t * 4, w_desc(st + 2 * kWOp + t * kSfTile, 128, 0));
+            w_cp_sf(sfa + t * 4, g_desc(st + 2 * kWOp + t * kSfTile, 128, 0));
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              w_cp_sf(sfb + (t * 2 + r) * 4, w_desc(st + 2 * kWOp + S::kSfA + (r * S::kAtoms + t) * kSfTile, 128, 0));
+              w_cp_sf(sfb + (t * 2 + r) * 4, g_desc(st + 2 * kWOp + S::kSfA + (r * S::kAtoms + t) * kSfTile, 128, 0));
           }
           const int rest = a.d_in - kb * kWK;
 #pragma unroll
@@ -266,7 +238,7 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
             if (kk * 64 < rest) {
               const int t = NV ? kk : kk >> 1;
               const uint32_t id = NV ? 0u : (uint32_t)(kk & 1) * 2u;
-              w_mma<NV>(tmem, w_desc(st + kk * 32, 1024, 2), w_desc(st + kWOp + kk * 32, 1024, 2), w_idesc<NV>(id), sfa + t * 4,
+              w_mma<NV>(tmem, g_desc(st + kk * 32, 1024, 2), g_desc(st + kWOp + kk * 32, 1024, 2), w_idesc<NV>(id), sfa + t * 4,
                         sfb + t * 8, (kb > 0 || kk > 0) ? 1u : 0u);
             }
           }
@@ -292,8 +264,8 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
     for (int lt = 0; lt < mine; ++lt) {
       const int t = pair + lt * npairs;
       const int m0 = (t % mtiles) * 256 + (int)rank * kWRows, n0 = (t / mtiles) * 256;
-      const bool ok = w_wait_warp(&s_tfull, (uint32_t)lt & 1u, &s_abort, a.status, 93);
-      w_after();
+      const bool ok = g_wait_warp(&s_tfull, (uint32_t)lt & 1u, &s_abort, a.status, 93);
+      g_after();
 #pragma unroll
       for (int half = 0; half < (BF16 ? 1 : 2); ++half) {
         // the stores of the results before have read the shared memory
@@ -330,7 +302,7 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
           }
         }
         if (half == (BF16 ? 0 : 1)) {
-          w_before();
+          g_before();
           __syncwarp();
           if (lane == 0)
             asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(tempty0) : "memory");
@@ -349,31 +321,18 @@ __global__ void __launch_bounds__(kWThreads, 1) fp4_gemm_wide_kernel(const __gri
     }
     if (threadIdx.x == 64) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
-  w_before();
+  g_before();
   __syncthreads();
   w_cluster_sync();                                // both CTAs are done with the pair's tensor memory
   if (warp == 0) {
-    w_after();
+    g_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 w_encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 bool w_map(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t bx,
            uint32_t by, bool swizzle) {
-  auto fn = w_encode_fn();
+  auto fn = g_encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {pitch};

@@ -1,5 +1,5 @@
-// Block-scaled 4-bit products on the tensor cores: the instructions, descriptors
-// and tensor maps that the kernels with one CTA per tile share.
+// Tensor-core products of 4-bit and bf16 matrices: the instructions, descriptors, waits and
+// tensor maps that these kernels share.
 #pragma once
 
 #include <cuda.h>
@@ -21,6 +21,23 @@ __device__ __forceinline__ uint64_t g_desc(uint32_t saddr, uint32_t sbo, uint32_
   d |= (uint64_t)1 << 46;                          // sm_100 descriptor version
   d |= (uint64_t)layout << 61;
   return d;
+}
+
+// bf16 x bf16: a descriptor with a leading offset (128-byte swizzle), instruction descriptor (M = 128, f32
+// sums; b_mn: neighbouring columns of B are contiguous), product
+__device__ __forceinline__ uint64_t g_desc_bf16(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint32_t g_idesc_bf16(uint32_t n, uint32_t b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void g_mma_bf16(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 template <bool NV>

@@ -78,6 +78,7 @@ cudaError_t launch_moe_bf16_tensor(const MoeArgs& a, cudaStream_t s);
 cudaError_t launch_moe_sum(const MoeArgs& a, cudaStream_t s);
 constexpr int kMoeDownTokens = 40;                        // tensor-core down projections: per pass
 constexpr int kMoeDownCols = 512, kMoeDownColsBf16 = 256; // ... columns per item
+__device__ __forceinline__ float relu_nan(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
 constexpr int kMoeXTerms = 8;
 __host__ __device__ constexpr int moe_xs_pitch(int d_model) { return (d_model / 32 + 31) / 32 * 32; }
 

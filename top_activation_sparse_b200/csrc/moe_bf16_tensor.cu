@@ -42,20 +42,6 @@ constexpr int kTA = 128 * kTK * 2;              // 16 KB: h
 constexpr int kTTenth = 10;                     // tokens per 32 rows of h
 static_assert(kMoeDownTokens == 4 * kTTenth, "four quarters of 10 tokens");
 
-__device__ __forceinline__ uint32_t t_idesc(uint32_t n, uint32_t b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ uint64_t t_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ void t_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 __device__ __forceinline__ void t_tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -72,7 +58,6 @@ __device__ __forceinline__ void t_add16(uint32_t taddr, float* s) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] += __uint_as_float(u[i >> 3][i & 7]);
 }
-__device__ __forceinline__ float t_relu(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
 
 struct TShared {
   uint64_t full[kTMaxStages], empty[kTMaxStages], tfull[2], tempty[2], done;
@@ -159,8 +144,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
   } else if (warp == 1) {
     const bool issues = g_elect();
-    const uint32_t id = t_idesc((uint32_t)f.rows, 0u);
-    const uint64_t d0 = t_desc(base, 16, 1024);
+    const uint32_t id = g_idesc_bf16((uint32_t)f.rows, 0u);
+    const uint64_t d0 = g_desc_bf16(base, 16, 1024);
     int sl = 0, piece = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -178,7 +163,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
           for (int kk = 0; kk < kTK / 16; ++kk)
 #pragma unroll
             for (int o = 0; o < 2; ++o)
-              t_mma(tmem + ab * 128 + o * 64, st + o * (kTW / 16) + kk * 2, st + 2 * (kTW / 16) + kk * 2, id,
+              g_mma_bf16(tmem + ab * 128 + o * 64, st + o * (kTW / 16) + kk * 2, st + 2 * (kTW / 16) + kk * 2, id,
                     ks % kTChunk > 0 || kk > 0);
           g_commit(&s.empty[sl]);
           if (last) g_commit(&s.tfull[ab]);
@@ -231,9 +216,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       for (int t = 0; t < ROWS; ++t) {
         const int c = place[t];
         if (c < 0) continue;
-        float h = t_relu(v[0][t] + b1), g = v[1][t] + b2;
+        float h = relu_nan(v[0][t] + b1), g = v[1][t] + b2;
         if (!a.drelu) h *= h;
-        else g = t_relu(g);
+        else g = relu_nan(g);
         // (a closed first factor is 0 whatever the other is)
         h = h == 0.0f ? 0.0f : h * g;
         // h as the sum of three bf16 numbers (an infinity or a NaN has no rest)
@@ -294,13 +279,13 @@ __global__ void __launch_bounds__(kTDThreads, 1)
     }
   } else if (warp == 1) {
     const bool issues = g_elect();
-    const uint64_t a0 = t_desc(base + kTB, 16, 1024), b0 = t_desc(base, kTBox, 1024);
+    const uint64_t a0 = g_desc_bf16(base + kTB, 16, 1024), b0 = g_desc_bf16(base, kTBox, 1024);
     int sl = 0, piece = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const MoeDownItem d = moe_down_item(a, s.tb, it, S, kTCols, kTK);
-      const uint32_t id = t_idesc((uint32_t)d.cw, 1u);
+      const uint32_t id = g_idesc_bf16((uint32_t)d.cw, 1u);
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens)
         for (int ks = 0; ks < d.steps; ++ks) {
           const int ab = piece & 1;
@@ -314,7 +299,7 @@ __global__ void __launch_bounds__(kTDThreads, 1)
           if (issues) {
 #pragma unroll
             for (int kk = 0; kk < kTK / 16; ++kk)
-              t_mma(tmem + ab * 256, ad + kk * 2, bd + kk * 128, id, ks % kTChunk > 0 || kk > 0);
+              g_mma_bf16(tmem + ab * 256, ad + kk * 2, bd + kk * 128, id, ks % kTChunk > 0 || kk > 0);
             g_commit(&s.empty[sl]);
             if (last) g_commit(&s.tfull[ab]);
           }

@@ -47,21 +47,6 @@ constexpr int kDTenth = 10;                     // tokens per 32 rows (30 of the
 static_assert(kMoeDownTokens == 4 * kDTenth, "four quarters of 10 tokens");
 constexpr int kDSmem = 2 * (kDB + kDA) + kDCodeStages * kDCodes + 1024;
 
-__device__ __forceinline__ uint32_t d_idesc(uint32_t n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ uint64_t d_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ void d_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Nibbles c and c + 4 of a word as a pair of bf16.  A code's two exponent bits (bias 1) and
 // its mantissa bit, moved to the two lowest exponent bits and the highest mantissa bit of a bf16
 // number (bias 127), read as the code's value times 2^-126, subnormal codes too; one product
@@ -173,14 +158,14 @@ __global__ void __launch_bounds__(kDThreads, 1)
     // ---- MMAs.  (The whole warp goes through the steps, one lane issues: what the
     // instructions take is then uniform and need not be moved there lane by lane) ----
     const bool issues = g_elect();
-    const uint64_t a0 = d_desc(sa, 16, 1024), b0 = d_desc(base, kDBox, 1024);
+    const uint64_t a0 = g_desc_bf16(sa, 16, 1024), b0 = g_desc_bf16(base, kDBox, 1024);
     int b = 0, piece = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const MoeDownItem d = moe_down_item(a, tb, it, S, kDCols, kDK);
       for (int t0 = 0; t0 < d.cnt && ok; t0 += kMoeDownTokens) {
-        const uint32_t id0 = d_idesc((uint32_t)min(256, d.cw)), id1 = d_idesc((uint32_t)max(16, d.cw - 256));
+        const uint32_t id0 = g_idesc_bf16((uint32_t)min(256, d.cw), 1u), id1 = g_idesc_bf16((uint32_t)max(16, d.cw - 256), 1u);
         for (int ks = 0, in = 0; ks < d.steps; ++ks) {         // in: this step's place in its sum
           if (in == 0 && piece > 0 && !(ok = g_wait_warp(&s_tempty, (uint32_t)(piece - 1) & 1u, &s_abort, a.status, 91))) break;
           // (h has arrived too: the first expanding warp has waited for it)
@@ -194,7 +179,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
               if (half * 256 >= d.cw) break;
 #pragma unroll
               for (int kk = 0; kk < kDK / 16; ++kk)
-                d_mma(tmem + half * 256, ad + kk * 2, bd + half * (4 * kDBox / 16) + kk * 128, half ? id1 : id0, in > 0 || kk > 0);
+                g_mma_bf16(tmem + half * 256, ad + kk * 2, bd + half * (4 * kDBox / 16) + kk * 128, half ? id1 : id0, in > 0 || kk > 0);
             }
             g_commit(&s_empty[b]);
             if (last) g_commit(&s_tfull);

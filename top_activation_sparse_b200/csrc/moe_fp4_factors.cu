@@ -80,8 +80,6 @@ __device__ __forceinline__ uint32_t f_idesc(uint32_t sf_id, uint32_t n) {
   return (sf_id << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((uint32_t)(kFM >> 4) << 24) | (sf_id << 29);
 }
 
-__device__ __forceinline__ float f_relu(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
-
 __global__ void __launch_bounds__(kFThreads, 1)
     moe_fp4_factors_kernel(const __grid_constant__ CUtensorMap map_1, const __grid_constant__ CUtensorMap map_2,
                          const __grid_constant__ CUtensorMap map_x, const __grid_constant__ FArgs f) {
@@ -229,11 +227,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
           for (int i = 6; i >= 0; --i) s[o] += __uint_as_float(v[o][i]);
         }
-        float h = f_relu(s[0] + b1);
+        float h = relu_nan(s[0] + b1);
         if (!a.drelu) h *= h;
         // (a closed first factor is 0 whatever the other is)
         float g = s[1] + b2;
-        if (a.drelu) g = f_relu(g);
+        if (a.drelu) g = relu_nan(g);
         h = h == 0.0f ? 0.0f : h * g;
         // h as the sum of three bf16 numbers, for the down projection (an
         // infinity or a NaN has no rest)

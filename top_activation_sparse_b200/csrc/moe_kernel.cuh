@@ -432,8 +432,6 @@ __device__ __noinline__ void route_here(const MoeArgs& a, bool publish, int lane
 }
 
 // ---- hidden layer ------------------------------------------------------------
-__device__ __forceinline__ float relu_nan(float v) { return v <= 0.0f ? 0.0f : v; }   // keeps a NaN
-
 // How rows lie in the ring, from the plan; the same in both roles.
 struct Ring {
   int rb, sb;          // bytes of a row, and of its scales where they travel with it (else 0)
