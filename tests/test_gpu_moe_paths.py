@@ -115,6 +115,20 @@ def test_queue_kernel(size, act, bias):
     check(queue(a, top_k, act), reference(a, vals, top_k, act), dm, bf)
 
 
+@pytest.mark.parametrize("size", [(1, 4128, 200, 4, 2), (1, 8192, 264, 4, 2), (1, 8160, 136, 9, 1), (3, 8192, 920, 8, 2)])
+@pytest.mark.parametrize("act,bias", [("drelu", -0.8), ("relu2_glu", None)])
+def test_queue_kernel_rows_longer_than_4096(size, act, bias):
+    need_gpu()
+    T, dm, dff, E, top_k = size
+    one_kernel(*size)
+    a, vals = make(60 + T + dm, T, dm, dff, E, act, False, bias)
+    ws = qs.new_workspace(qs.QS_OP_MOE_FFN, T, dm, dff, top_k, DEV)
+    r = queue(a, top_k, act, ws=ws)
+    check(r, reference(a, vals, top_k, act), dm, bf)
+    assert torch.equal(queue(a, top_k, act, ws=ws).y, r.y)
+    assert int(ws[256:256 + 65536].count_nonzero()) == 0
+
+
 @pytest.mark.parametrize("size", SEVERAL)
 def test_queue_kernel_leaves_its_workspace_ready(size):
     need_gpu()

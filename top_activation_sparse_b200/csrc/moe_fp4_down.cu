@@ -75,7 +75,8 @@ __device__ __forceinline__ void d_expand(const uint32_t (&v)[4], uint32_t s, uin
 }
 
 // (an address is added to by one thread only, so that the order is fixed; a reduction at
-// L2, for which nothing waits: loading, adding and storing took 30 us per sum more)
+// L2, for which nothing waits: loading, adding and storing took 30 us per sum more.  Subnormal
+// sums count as 0 there)
 __device__ __forceinline__ void d_add4(float* p, float x, float y, float z, float w) {
   asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }

@@ -49,7 +49,7 @@
 // 1 token, 2 of 8 dReLU experts of 14336 x 4096: bf16 76 us (46 at the memory's rate),
 // 4-bit 65 (12: bound by the expansion, 1.5 instructions per cycle, and by latencies:
 // about 7 us of routing, 4 for the first rows, 8 for the last sums).  2 tokens, 8 experts of
-// 11008 x 4096, bf16: 157 us.
+// 11008 x 4096, bf16: 138 us.
 #pragma once
 
 #include "fp4.cuh"
@@ -1536,21 +1536,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_kernel(const __grid_constant_
 // One kernel or the tensor-core ones.
 // 4-bit weights: one token's layer (d_model <= 4096) in this kernel, everything else
 // by the tensor-core kernels, which read all weights but expand none of them in
-// registers.  8 experts of 4096 x 11008, 2 per token, dReLU without bias: 1 token 55
-// against 73 us, 2 tokens 120 against 106, 8: 244 against 172, 64: 1089 against 249; 60 of
-// 2048 x 1408, 4 per token: 34 / 44, 58 / 44, 104 / 69, 286 / 135.
+// registers.  One token, this kernel / the tensor-core ones, us, dReLU (79% of the gates closed;
+// squared ReLU): 2 of 8 experts of 11008 x 4096 53 / 74 (74 / 74), 4 of 60 of 1408 x 2048 32 / 41
+// (37 / 41), 2 of 16 of 512 x 512 22 / 30 (23 / 29).  (Several tokens in registers: 8 tokens of the
+// first layer 244, 64 tokens 1089, on the tensor cores 190 and 271.)
 // bf16 weights: reading every row costs no more than picking the open ones once two
 // tokens share an expert, or where an expert's rows take less time than the batches'
-// waits.  The same layers, one kernel / tensor cores: 8 experts 2 tokens 157 / 191, 8: 329 /
-// 326 (squared ReLU 443 / 328), 64: 913 / 369; 60 experts 2 tokens 59 / 51, 8: 105 / 102, 64:
-// 370 / 242; 16 of 512 x 512, 2 per token: 4 tokens 36 / 26.
+// waits.  The same layers: first 2 tokens 138 / 151 (186 / 151), 4: 232 / 287 (322 / 285), 8: 308 /
+// 316 (418 / 317), 64: 878 / 371 (994 / 372); second 2 tokens 59 / 55 (64 / 53), 8: 104 / 105 (132 / 105),
+// 64: 370 / 251 (418 / 250); third 4 tokens 34 / 28 (35 / 27).  Sizes do not tell how often gates are
+// closed: the first layer's 8 tokens (8 experts used) take 441 / 345 with 50% of them closed, 276 / 345 with
+// 93%, 239 / 345 with 99%; the rule is made for what is closed about as often as in the cases.
 // f32 results: matrix instructions cut a sum off at each step, 3e-8 of it.  This kernel's
 // sums over d_model and its down sums (200 steps and more) put y off by 2e-6 to 3e-6, the bf16
 // tensor-core kernels' (which add up every 128 terms) by 6e-7: those for every call of several
 // tokens or of d_model above 4096 (one token, whose results are bf16 or whose d_model is at most
 // 4096, stays here: 2 of 4 experts of 11008 x 8192, f32: 330 / 210 us, of 64 of 1024 x 8192: 69 / 78).  4-bit
 // weights: sums of 1024 neurons (4e-7, as of a plain float32 product), of 2048 for bf16 results
-// (8e-7; the 32-token layer 202 instead of 214 us).
+// (8e-7; 32 tokens of the first layer 204 instead of 216 us).
 MoePlan make_plan(int T, int d_model, int d_ff, int n_experts, int top_k, bool y_bf16) {
   constexpr bool fp4 = kFp4;
   MoePlan p;
