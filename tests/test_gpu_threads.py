@@ -98,3 +98,41 @@ def test_a_dropped_workspace_is_not_handed_out_while_its_call_runs():
         torch.cuda.synchronize()
         assert torch.equal(y, want)
         del other
+
+
+@pytest.mark.parametrize("T", [1, 8])
+def test_projection_and_ffn_captured_without_a_workspace(T):
+    """Two graphs, each call with a workspace of its own: several tokens replayed at once on two streams, one
+    token (whose layer may be one kernel that needs its whole grid resident) in turn."""
+    need_gpu()
+    d, dff = 1024, 2048
+    wt = rnd(1, d, dff, std=0.03).to(torch.bfloat16)
+    up, gate, down = (rnd(4 + i, *s, std=0.03).to(torch.bfloat16) for i, s in enumerate(((d, dff), (d, dff), (dff, d))))
+    x = rnd(2, T, d).to(torch.bfloat16)
+
+    def layer():
+        return qs.qs_sparse_linear(x, wt, 700), qs.qs_sparse_ffn(x, up, gate, down, "relu2_glu", 700, 1400).y
+
+    want = layer()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer()                              # its workspaces' memory goes to the second layer's
+            got = layer()
+        graphs.append((graph, got, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, got, s in graphs:
+            with torch.cuda.stream(s):
+                for g in got:
+                    g.zero_()
+                graph.replay()
+            if T == 1:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        for _, got, _ in graphs:
+            for g, w in zip(got, want):
+                assert (g.float() - w.float()).norm() <= 2.0 ** -7 * w.float().norm()
+    after = layer()                              # the eager workspaces are as they were
+    assert all((g.float() - w.float()).norm() <= 2.0 ** -7 * w.float().norm() for g, w in zip(after, want))
